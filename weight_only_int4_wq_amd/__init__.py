@@ -1,7 +1,8 @@
 """Weight-only quantized linear layers on AMD gfx950 (MI355X).
 
 Thin Python binding over libwq.so, the HIP library whose C ABI is declared in
-include/wq.h.  Every function here only checks and marshals arguments (torch
+include/wq.h and, for the products of a feed-forward block and their backward
+passes, include/wq_block.h.  Every function here only checks and marshals arguments (torch
 tensors for device memory, torch's current HIP stream) and calls the entry
 point of the same name; all computation runs in the library's kernels.
 There is no fallback: if libwq.so is missing or cannot be loaded, every call
@@ -19,7 +20,8 @@ __all__ = [
     "quantize_rtn", "awq_scales", "awq_fold", "awq_search", "awq_clip", "gptq_quantize", "act_order_perm", "pack", "unpack",
     "dequant", "scale_act", "workspace_size", "gemv", "gemm", "linear", "gemv_silu_mul", "gemv_ex", "gemv_max_m",
     "linear_noalloc", "noalloc_scratch_bytes", "stream_read",
-    "status_str", "version", "QuantizedLinear",
+    "ACTIVATIONS", "linear_act", "linear_act_backward", "gated", "gated_backward", "block_workspace_size",
+    "status_str", "version", "QuantizedLinear", "QuantizedGatedMLP",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -58,7 +60,16 @@ _SIG["wq_gemv_ex"] = (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I3
 for _name in ("wq_gemv", "wq_gemm", "wq_linear"):
     _SIG[_name] = (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32,
                                   _VP, ctypes.c_size_t, _VP])
+_SIZE = ctypes.c_size_t
+_SIG["wq_linear_act"] = (ctypes.c_int, [_VP] * 7 + [_I32, _VP, _VP] + [_I32] * 5 + [_VP, _SIZE, _VP])
+_SIG["wq_gated"] = (ctypes.c_int, [_VP] * 6 + [_I32, _VP, _VP] + [_I32] * 5 + [_VP, _SIZE, _VP])
+for _name in ("wq_linear_act_backward", "wq_gated_backward"):
+    _SIG[_name] = (ctypes.c_int, [_VP, _VP, _I32] + [_VP] * 8 + [_I32] * 5 + [_VP, _SIZE, _VP])
+for _name in ("wq_linear_act", "wq_gated", "wq_linear_act_backward", "wq_gated_backward"):
+    _SIG[_name + "_workspace_size"] = (_SIZE, [_I32] * 5)
 
+# Activations of the block's products, by the numbers of wq_act.
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 WQ_ERR_ARG, WQ_ERR_UNSUPPORTED, WQ_ERR_HIP, WQ_ERR_TOO_LARGE = 1, 2, 3, 4
 
@@ -486,6 +497,156 @@ def gemv_ex(x, packed, scales, zeros, bits: int, group_size: int, perm=None, act
     return y
 
 
+# ------------------------------------------------- feed-forward block ----
+
+def block_workspace_size(entry: str, M: int, N: int, K: int, bits: int, has_perm: bool) -> int:
+    """Bytes of workspace of `entry` ("linear_act", "gated",
+    "linear_act_backward" or "gated_backward"); N counts one projection's
+    columns for the gated ones."""
+    return int(getattr(lib(), f"wq_{entry}_workspace_size")(M, N, K, bits, int(bool(has_perm))))
+
+
+def _act(act) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _block_call(entry, device, args, M, N, K, bits, group_size, has_perm, workspace):
+    """Take or allocate the workspace and call wq_<entry> on the tensors'
+    device (made current for the call) and its current stream."""
+    torch = _torch()
+    if workspace is None:
+        need = block_workspace_size(entry, M, N, K, bits, has_perm)
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    nbytes = 0 if workspace is None else workspace.numel()
+    fn = getattr(lib(), "wq_" + entry)
+
+    def call():
+        return fn(*args, M, N, K, bits, group_size, _ptr(workspace), nbytes, _stream(device))
+
+    if device.type == "cuda" and torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            code = call()
+    else:
+        code = call()
+    _check(code, "wq_" + entry)
+
+
+def _weight_args(packed, scales, zeros, perm, bits, group_size, device, gated):
+    """Check a layer's weights; returns (projection columns, K)."""
+    torch = _torch()
+    packed = _dev(packed, torch.int32, "packed", 2, device=device)
+    scales = _dev(scales, torch.float16, "scales", 2, device=device)
+    zeros = _dev(zeros, torch.uint8, "zeros", 2, allow_none=True, device=device)
+    perm = _dev(perm, torch.int32, "perm", 1, allow_none=True, device=device)
+    if bits not in (2, 3, 4, 8):
+        raise ValueError("bits must be 2, 3, 4 or 8")
+    rows, words = packed.shape
+    if words * 32 % bits:
+        raise ValueError("packed must be [N][K*bits/32]")
+    K = words * 32 // bits
+    _check_meta(rows, K, bits, group_size, packed, scales, zeros, perm)
+    if gated and rows % 2:
+        raise ValueError("the stacked gate/up weight needs an even row count")
+    return (rows // 2 if gated else rows), K
+
+
+def _forward(entry, x, packed, scales, zeros, bits, group_size, perm, bias, residual, act, save_preact, out, preact,
+             workspace):
+    torch = _torch()
+    act = _act(act)
+    x = _dev(x, torch.float16, "x", 2)
+    d = x.device
+    workspace = _dev(workspace, torch.uint8, "workspace", 1, allow_none=True, device=d)
+    is_gated = entry == "gated"
+    N, K = _weight_args(packed, scales, zeros, perm, bits, group_size, d, is_gated)
+    M = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"x must have {K} columns, got {x.shape[1]}")
+    rows = packed.shape[0]
+    bias = _dev(bias, torch.float16, "bias", 1, allow_none=True, shape=(rows,), device=d)
+    residual = _dev(residual, torch.float16, "residual", 2, allow_none=True, shape=(M, N), device=d)
+    y = torch.empty((M, N), dtype=torch.float16, device=d) if out is None else \
+        _dev(out, torch.float16, "out", 2, shape=(M, N), device=d)
+    if preact is not None:
+        preact = _dev(preact, torch.float16, "preact", 2, shape=(M, rows), device=d)
+    elif save_preact:
+        preact = torch.empty((M, rows), dtype=torch.float16, device=d)
+    args = [_ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm), _ptr(bias)]
+    args += ([] if is_gated else [_ptr(residual)]) + [act, _ptr(y), _ptr(preact)]
+    _block_call(entry, d, args, M, N, K, bits, group_size, perm is not None, workspace)
+    return y if preact is None else (y, preact)
+
+
+def linear_act(x, packed, scales, zeros, bits: int, group_size: int, perm=None, bias=None, residual=None,
+               act: str = "none", save_preact: bool = False, out=None, preact=None, workspace=None):
+    """y fp16 [M][N] = act(x . W^T + bias) + residual, any M, rounded once.
+    `out` may be `residual` (update in place).  With save_preact (or a
+    `preact` tensor to fill) returns (y, preact), preact = fp16(x . W^T + bias)
+    for linear_act_backward."""
+    return _forward("linear_act", x, packed, scales, zeros, bits, group_size, perm, bias, residual, act, save_preact,
+                    out, preact, workspace)
+
+
+def gated(x, packed, scales, zeros, bits: int, group_size: int, perm=None, bias=None, act: str = "silu",
+          save_preact: bool = False, out=None, preact=None, workspace=None):
+    """h fp16 [M][I] = act(x . Wg^T + bg) * (x . Wu^T + bu), any M, the gate
+    rows stacked over the up rows (2 I weight rows), one kernel for both
+    projections, the activation and the product.  With save_preact returns
+    (h, preact [M][2 I]) for gated_backward."""
+    return _forward("gated", x, packed, scales, zeros, bits, group_size, perm, bias, None, act, save_preact, out,
+                    preact, workspace)
+
+
+def _backward(entry, dy, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add, need_dz, need_dbias, out,
+              workspace):
+    torch = _torch()
+    is_gated = entry == "gated_backward"
+    code = _act(act)
+    dy = _dev(dy, torch.float16, "dy", 2)
+    d = dy.device
+    workspace = _dev(workspace, torch.uint8, "workspace", 1, allow_none=True, device=d)
+    N, K = _weight_args(packed, scales, zeros, perm, bits, group_size, d, is_gated)
+    M, rows = dy.shape[0], packed.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"dy must have {N} columns, got {dy.shape[1]}")
+    needs_z = is_gated or act != "none"
+    if needs_z or preact is not None:
+        preact = _dev(preact, torch.float16, "preact", 2, shape=(M, rows), device=d)
+    dx_add = _dev(dx_add, torch.float16, "dx_add", 2, allow_none=True, shape=(M, K), device=d)
+    dx = torch.empty((M, K), dtype=torch.float16, device=d) if out is None else \
+        _dev(out, torch.float16, "out", 2, shape=(M, K), device=d)
+    dz = torch.empty((M, rows), dtype=torch.float16, device=d) if need_dz and needs_z else None
+    dbias = torch.empty((rows,), dtype=torch.float32, device=d) if need_dbias else None
+    args = [_ptr(dy), _ptr(preact if needs_z else None), code, _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm),
+            _ptr(dx_add), _ptr(dx), _ptr(dz), _ptr(dbias)]
+    _block_call(entry, d, args, M, N, K, bits, group_size, perm is not None, workspace)
+    if need_dz and not needs_z:
+        dz = dy
+    return dx, dz, dbias
+
+
+def linear_act_backward(dy, preact, packed, scales, zeros, bits: int, group_size: int, perm=None, act: str = "none",
+                        dx_add=None, need_dz: bool = True, need_dbias: bool = False, out=None, workspace=None):
+    """Backward of linear_act for dy fp16 [M][N] -> (dx fp16 [M][K] = dz . W +
+    dx_add, dz fp16 [M][N] = dy * act'(preact) or None, dbias fp32 [N] or
+    None).  Without an activation preact may be None and dz is dy.  The
+    residual's gradient is dy.  `out` may be `dx_add`."""
+    return _backward("linear_act_backward", dy, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add,
+                     need_dz, need_dbias, out, workspace)
+
+
+def gated_backward(dh, preact, packed, scales, zeros, bits: int, group_size: int, perm=None, act: str = "silu",
+                   dx_add=None, need_dz: bool = True, need_dbias: bool = False, out=None, workspace=None):
+    """Backward of gated for dh fp16 [M][I] and the kept preact fp16 [M][2 I]
+    -> (dx fp16 [M][K], dz fp16 [M][2 I] = (dg, du) or None, dbias fp32 [2 I]
+    or None)."""
+    return _backward("gated_backward", dh, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add, need_dz,
+                     need_dbias, out, workspace)
+
+
 class QuantizedLinear:
     """A quantized linear layer held in device memory: packed weights, group
     scales and zero-points, optional act-order perm and AWQ input scale.
@@ -527,3 +688,61 @@ class QuantizedLinear:
             x = scale_act(x, self.act_scale)
         fn = {"linear": linear, "gemv": gemv, "gemm": gemm}[kernel]
         return fn(x, self.packed, self.scales, self.zeros, self.bits, self.group_size, self.perm, out, workspace)
+
+    def _scaled(self, x):
+        return x if self.act_scale is None else scale_act(x, self.act_scale)
+
+    def forward_act(self, x, bias=None, residual=None, act: str = "none", save_preact: bool = False, out=None,
+                    workspace=None):
+        """act(x . W^T + bias) + residual (linear_act), AWQ's x / s first."""
+        return linear_act(self._scaled(x), self.packed, self.scales, self.zeros, self.bits, self.group_size,
+                          perm=self.perm, bias=bias, residual=residual, act=act, save_preact=save_preact, out=out,
+                          workspace=workspace)
+
+    def backward(self, dy, preact=None, act: str = "none", dx_add=None, need_dz: bool = True,
+                 need_dbias: bool = False, workspace=None):
+        """(dx, dz, dbias) of forward_act; with an AWQ scale dx is divided by
+        it, which dx_add must not be: it is refused then."""
+        if self.act_scale is not None and dx_add is not None:
+            raise ValueError("dx_add cannot be combined with an AWQ scale")
+        dx, dz, dbias = linear_act_backward(dy, preact, self.packed, self.scales, self.zeros, self.bits,
+                                            self.group_size, perm=self.perm, act=act, dx_add=dx_add, need_dz=need_dz,
+                                            need_dbias=need_dbias, workspace=workspace)
+        return self._scaled(dx), dz, dbias
+
+
+class QuantizedGatedMLP:
+    """A gated feed-forward block on quantized weights:
+    y = (act(x . Wg^T) * (x . Wu^T)) . Wd^T + residual.
+
+    gate_up: a QuantizedLinear of 2 I rows, the gate projection stacked over
+    the up projection; down: one of I input channels.  The weights are frozen:
+    backward returns gradients of the activations and of the projections'
+    outputs (what adapters on them take)."""
+
+    def __init__(self, gate_up: QuantizedLinear, down: QuantizedLinear, act: str = "silu"):
+        if gate_up.N != 2 * down.K:
+            raise ValueError(f"gate_up has {gate_up.N} rows, down {down.K} input channels: twice as many are needed")
+        _act(act)
+        self.gate_up, self.down, self.act = gate_up, down, act
+
+    def __call__(self, x, residual=None, save: bool = False):
+        """y, or with save (y, preact) where preact is what backward takes."""
+        g = self.gate_up
+        r = gated(g._scaled(x), g.packed, g.scales, g.zeros, g.bits, g.group_size, perm=g.perm, act=self.act,
+                  save_preact=save)
+        h, preact = r if save else (r, None)
+        y = self.down.forward_act(h, residual=residual)
+        return (y, preact) if save else y
+
+    def backward(self, dy, preact, dx_add=None):
+        """(dx + dx_add, dz of the gate/up projections [M][2 I], dh [M][I]) for
+        dy fp16 [M][N].  With a residual its gradient is dy: pass dx_add=dy
+        where the residual is x itself."""
+        g = self.gate_up
+        if g.act_scale is not None and dx_add is not None:
+            raise ValueError("dx_add cannot be combined with an AWQ scale on gate_up")
+        dh, _, _ = self.down.backward(dy)
+        dx, dz, _ = gated_backward(dh, preact, g.packed, g.scales, g.zeros, g.bits, g.group_size, perm=g.perm,
+                                   act=self.act, dx_add=dx_add)
+        return g._scaled(dx), dz, dh

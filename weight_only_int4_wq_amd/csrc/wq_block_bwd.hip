@@ -1,0 +1,634 @@
+// The block's backward pass: dz from the incoming gradient and the kept
+// pre-activations, dx = dz . W (+ dx_add), dbias = column sums of dz.
+//
+// dx [M][K] = dz [M][R] . W [R][K] sums over the weight rows, while the codes
+// are packed along K.  The matrix instruction wants 8 consecutive n of one
+// column per lane; a packed word holds 8 columns of one n.  So a lane takes
+// the same 8-code block of 8 consecutive weight rows and turns the 8 x 8
+// square while decoding, at no cost: the byte permutes that expose two codes
+// of one row in the forward decoder here pick one byte of two neighbouring
+// rows, and the pair's two scales and zero-points differ instead of being
+// equal.  (At 4 bits: one permute per two pairs, one and-or per pair, one
+// subtraction and one multiplication: exactly the forward weights.)
+//
+// Since every lane holds 8 columns, a wavefront decodes 256 columns x 16 rows
+// at once, too many to keep for itself: the block (BM x 256 outputs, 64
+// weight rows a stage) decodes each stage once, a quarter per wavefront, into
+// LDS in the order the fragments are read (1 KB per fragment, no bank
+// conflicts either way), and its 2 x 2 wavefronts, BM/2 x 128 outputs each,
+// read it from there.  Decoding costs BM/128 * 1/16 of the vector work per
+// matrix instruction that a wavefront decoding its own columns would spend.
+// The columns are dealt to fragments so that a lane ends up with 4
+// consecutive outputs of a row: one 8-byte store (16 bytes of partial sums).
+//
+// Stages overlap in one loop with one barrier: while stage s is multiplied
+// from its LDS buffers, stage s + 1 is decoded into the others and stage
+// s + 2 is loaded into registers; scales and zero-points (64 rows x the
+// tile's groups) pass through LDS one stage earlier.
+#include <algorithm>
+
+#include "wq_block_common.h"
+
+namespace {
+
+using namespace wq;
+
+// ------------------------------------------------------------------ dz ----
+
+struct DzArgs {
+    const uint16_t* dy;      // [M][N]
+    const uint16_t* preact;  // [M][R], null for WQ_ACT_NONE (linear only)
+    uint16_t* dz;            // [M][R], nullable
+    uint16_t* dzp;           // [M][ld], zero past R, nullable
+    float* dbias;            // [gridDim.y][R] sums of this row range, nullable
+    int M, N, R, ld, act, rows_per;
+};
+
+constexpr int kDzRowLanes = 4;  // rows a block works on at once
+
+// A block takes 64 V-wide column groups and rows_per rows, four at a time;
+// dbias's sums stay in registers, cross the four row lanes through LDS and
+// leave as one partial row per block row.  V = 8 needs N to be a multiple of
+// 8.  Bound by memory: each of dy, preact and dz is touched once.
+template <bool GATED, int V>
+__global__ void __launch_bounds__(64 * kDzRowLanes) block_dz_kernel(const DzArgs p) {
+    constexpr int P = GATED ? 2 : 1;
+    __shared__ float red[kDzRowLanes][P][64 * V];
+    const int cl = threadIdx.x & 63, rl = threadIdx.x >> 6;
+    const int col = (int(blockIdx.x) * 64 + cl) * V;
+    const int r0 = int(blockIdx.y) * p.rows_per, r1 = min(r0 + p.rows_per, p.M);
+    float sum[P][V];
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[q][i] = 0.f;
+    for (int m = r0 + rl; m < r1; m += kDzRowLanes) {
+        if (col < p.N) {
+            float d[V], z[P][V], o[P][V];
+            load_h<V>(p.dy + size_t(m) * p.N + col, d);
+            if (p.preact) {
+#pragma unroll
+                for (int q = 0; q < P; ++q) load_h<V>(p.preact + size_t(m) * p.R + q * p.N + col, z[q]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) z[0][i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float a;
+                const float s = act_slope(z[0][i], p.act, a);
+                if constexpr (GATED) {
+                    o[0][i] = d[i] * z[1][i] * s;
+                    o[1][i] = d[i] * a;
+                } else {
+                    o[0][i] = d[i] * s;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const int n = q * p.N + col;
+                if (p.dz) store_h<V>(p.dz + size_t(m) * p.R + n, o[q]);
+                if (p.dzp) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) p.dzp[size_t(m) * p.ld + n + i] = f2h(o[q][i]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[q][i] += o[q][i];
+            }
+        }
+        // the padding of dzp's rows (fewer than 8 columns)
+        if (p.dzp && blockIdx.x == 0 && cl < p.ld - p.R) p.dzp[size_t(m) * p.ld + p.R + cl] = 0;
+    }
+    if (!p.dbias) return;
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) red[rl][q][i * 64 + cl] = sum[q][i];
+    __syncthreads();
+    for (int t = threadIdx.x; t < P * 64 * V; t += 64 * kDzRowLanes) {
+        const int q = t / (64 * V), at = t - q * 64 * V;
+        const int c = (int(blockIdx.x) * 64 + (at & 63)) * V + (at >> 6);
+        if (c >= p.N) continue;
+        float v = red[0][q][at];
+#pragma unroll
+        for (int l = 1; l < kDzRowLanes; ++l) v += red[l][q][at];
+        p.dbias[size_t(blockIdx.y) * p.R + q * p.N + c] = v;
+    }
+}
+
+// out[i] = sum over the row ranges, in order; zero for none.
+__global__ void __launch_bounds__(256) block_dbias_kernel(const float* __restrict__ part, int ranges, int R,
+                                                          float* __restrict__ out) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= R) return;
+    float v = 0.f;
+    for (int r = 0; r < ranges; ++r) v += part[size_t(r) * R + i];
+    out[i] = v;
+}
+
+// ------------------------------------------------------------------ dx ----
+
+struct DxArgs {
+    const uint16_t* dz;  // [M][ld], ld a multiple of 8, zero from R to ld
+    const uint32_t* packed;
+    const uint16_t* scales;
+    const uint8_t* zeros;
+    const uint16_t* add;  // [M][K], nullable, may be dx
+    uint16_t* dx;
+    float* part;  // [splits][M][K]
+    int M, R, K, ld;
+    GroupDiv gd;
+    int m_tiles, k_tiles, tiles, sps;
+};
+
+// One weight row's 8-code block: 8 * BITS bits in the low bits of w[0] (w[1]
+// above for 8-bit codes).  `blk` is the row's block index.
+template <int BITS>
+struct RowBlock {
+    static constexpr int kWords = BITS == 8 ? 2 : 1;
+};
+template <int BITS>
+__device__ __forceinline__ void load_row_block(const char* row, uint32_t blk, uint32_t* w) {
+    if constexpr (BITS == 4) {
+        w[0] = *reinterpret_cast<const uint32_t*>(row + blk * 4u);
+    } else if constexpr (BITS == 8) {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        const u2 v = *reinterpret_cast<const u2*>(row + blk * 8u);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else if constexpr (BITS == 2) {
+        w[0] = *reinterpret_cast<const uint16_t*>(row + blk * 2u);
+    } else {
+        // the 3 bytes at byte 3 blk: within one aligned word for blocks 0 and 3
+        // of a chunk, across two for blocks 1 and 2 (inside the row either way)
+        const uint32_t b = 3u * blk, q = blk & 3u;
+        const uint32_t at = (b & ~3u);
+        const uint32_t lo = *reinterpret_cast<const uint32_t*>(row + at);
+        const uint32_t hi = *reinterpret_cast<const uint32_t*>(row + (q == 1u || q == 2u ? at + 4u : at));
+        w[0] = __builtin_amdgcn_alignbyte(hi, lo, b & 3u) & 0x00FFFFFFu;
+    }
+}
+
+// Decode rows (2 p, 2 p + 1)'s blocks a, b: out[j] = column j of both rows as
+// a pair, (q - z) * s with the two rows' own z and s.
+template <int BITS>
+__device__ __forceinline__ void decode_columns(const uint32_t* a, const uint32_t* b, uint32_t z, uint32_t ss,
+                                               uint32_t (&out)[8]) {
+    const uint32_t ze = z | kMagic2;
+    if constexpr (BITS == 4) {
+        const uint32_t zo = (z << 4) | 0x54005400u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t sel = 0x0C000C00u | ((4u + i) << 16) | uint32_t(i);
+            const uint32_t t = __builtin_amdgcn_perm(b[0], a[0], sel);
+            out[2 * i] = as_u32(dequant_pair(and_or(t, 0x000F000Fu, kMagic2), ze, ss));
+            out[2 * i + 1] = as_u32(dequant_pair(and_or(t, 0x00F000F0u, 0x54005400u), zo, ss));
+        }
+    } else if constexpr (BITS == 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t i = uint32_t(j & 3);
+            const uint32_t sel = 0x0C000C00u | ((4u + i) << 16) | i;
+            out[j] = as_u32(dequant_pair(__builtin_amdgcn_perm(b[j >> 2], a[j >> 2], sel) | kMagic2, ze, ss));
+        }
+    } else if constexpr (BITS == 2) {
+        const uint32_t t = a[0] | (b[0] << 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            out[j] = as_u32(dequant_pair(and_or(t >> (2 * j), 0x00030003u, kMagic2), ze, ss));
+    } else {
+        const uint32_t lo = (a[0] & 0xFFFu) | (b[0] << 16);  // bits 12.. of b's half are masked below
+        const uint32_t hi = (a[0] >> 12) | ((b[0] >> 12) << 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            out[j] = as_u32(dequant_pair(and_or(lo >> (3 * j), 0x00070007u, kMagic2), ze, ss));
+            out[4 + j] = as_u32(dequant_pair(and_or(hi >> (3 * j), 0x00070007u, kMagic2), ze, ss));
+        }
+    }
+}
+
+// G8: groups of 32 channels, up to 8 groups per tile; otherwise up to 4
+// (group sizes of 64 and more, tiles start at multiples of 256).
+template <int BITS, bool HAS_Z, int BM, bool G8, bool PART>
+__global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
+    constexpr int BK = 64, TM = BM / 64, TN = 4;
+    constexpr int ROW = BK * 2;
+    constexpr int AU = BM * 8 / 256;
+    constexpr int NG = G8 ? 8 : 4;
+    constexpr int A_BYTES = BM * ROW, B_BYTES = 256 * BK * 2, S_BYTES = NG * BK * 2;
+    constexpr int W = RowBlock<BITS>::kWords;
+    extern __shared__ __attribute__((aligned(128))) uint8_t lds[];
+    uint8_t* const lds_a = lds;                        // [2][BM rows][64 n]
+    uint8_t* const lds_b = lds_a + 2 * A_BYTES;        // [2][4 k-steps][2][4][64 lanes] x 16 bytes
+    uint8_t* const lds_s = lds_b + 2 * B_BYTES;        // [2][NG][64] scales, then zero-points
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int c = lane & 31, hh = lane >> 5;
+    int m_t, k_t;
+    tile_coords<4>(blockIdx.x, p.tiles, p.m_tiles, p.k_tiles, m_t, k_t);
+    const int m0 = m_t * BM, k0 = k_t * 256;
+    const int chunks = p.K / 32;
+    const int G = chunk_group(chunks - 1, p.gd) + 1;
+    const int stages = (p.R + BK - 1) / BK;
+    const int st_begin = int(blockIdx.y) * p.sps;
+    const int st_end = min(st_begin + p.sps, stages);
+    const int st_last = st_end - 1;
+
+    // ---- dz: thread t copies unit t % 8 of rows t / 8 + 32 i
+    const int au = tid & 7, ar = tid >> 3;
+    uint32_t a_off[AU];
+#pragma unroll
+    for (int i = 0; i < AU; ++i) a_off[i] = uint32_t(min(m0 + ar + 32 * i, p.M - 1) - m0) * uint32_t(p.ld) * 2u;
+    const char* abase = reinterpret_cast<const char*>(p.dz + size_t(m0) * p.ld);
+    u4 av[AU];
+    auto load_a = [&](int st) {
+        const uint32_t n = min(uint32_t(st * BK + 8 * au), uint32_t(p.ld - 8)) * 2u;
+#pragma unroll
+        for (int i = 0; i < AU; ++i) av[i] = *reinterpret_cast<const u4*>(abase + (a_off[i] + n));
+    };
+    auto store_a = [&](int st, int par) {
+        if (st * BK + 8 * au >= p.ld) {  // only in a last stage that R ends in
+#pragma unroll
+            for (int i = 0; i < AU; ++i) av[i] = u4{0u, 0u, 0u, 0u};
+        }
+        uint8_t* buf = lds_a + par * A_BYTES;
+#pragma unroll
+        for (int i = 0; i < AU; ++i)
+            *reinterpret_cast<u4*>(buf + (ar + 32 * i) * ROW + ((au ^ (ar & 7)) * 16)) = av[i];
+    };
+
+    // ---- scales and zero-points: thread t takes row t % 64 of groups t / 64
+    // (and t / 64 + 4), rows past R with scale 0
+    const int g0 = chunk_group(k0 / 32, p.gd);
+    const int g_last = chunk_group(min(k0 / 32 + 7, chunks - 1), p.gd);
+    uint32_t sv[NG / 4], zv[NG / 4];
+    auto load_s = [&](int st) {
+        const int n = st * BK + (tid & 63);
+        const size_t row = size_t(min(n, p.R - 1)) * G;
+#pragma unroll
+        for (int i = 0; i < NG / 4; ++i) {
+            const int g = min(g0 + (tid >> 6) + 4 * i, g_last);
+            sv[i] = p.scales[row + g];
+            if constexpr (HAS_Z)
+                zv[i] = p.zeros[row + g];
+            else
+                zv[i] = 1u << (BITS - 1);
+        }
+    };
+    auto store_s = [&](int st, int par) {
+        const bool in = st * BK + (tid & 63) < p.R;
+        uint16_t* s = reinterpret_cast<uint16_t*>(lds_s + par * 2 * S_BYTES);
+#pragma unroll
+        for (int i = 0; i < NG / 4; ++i) {
+            const int at = ((tid >> 6) + 4 * i) * BK + (tid & 63);
+            s[at] = in ? uint16_t(sv[i]) : uint16_t(0);
+            s[NG * BK + at] = uint16_t(zv[i]);
+        }
+    };
+
+    // ---- weights: this wavefront decodes rows 16 wave + 8 hh + i of the
+    // stage, block c of the tile's 32 (blocks past K read the last one; their
+    // outputs are not stored)
+    const uint32_t blk = uint32_t(min(k0 / 8 + c, p.K / 8 - 1));
+    const int lg = chunk_group(int(blk >> 2), p.gd) - g0;
+    const size_t row_bytes = size_t(chunks) * BITS * 4;
+    uint32_t wv[8][W];
+    auto load_w = [&](int st) {
+        const char* base = reinterpret_cast<const char*>(p.packed) + size_t(st) * BK * row_bytes;
+        const int left = p.R - 1 - st * BK;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = min(16 * wave + 8 * hh + i, left);
+            load_row_block<BITS>(base + uint32_t(n) * uint32_t(row_bytes), blk, wv[i]);
+        }
+    };
+    auto decode = [&](int par_s, int par_b) {
+        const uint8_t* s = lds_s + par_s * 2 * S_BYTES + (lg * BK + 16 * wave + 8 * hh) * 2;
+        const u4 ss = *reinterpret_cast<const u4*>(s);
+        const u4 zz = *reinterpret_cast<const u4*>(s + S_BYTES);
+        const uint32_t sa[4] = {ss.x, ss.y, ss.z, ss.w}, za[4] = {zz.x, zz.y, zz.z, zz.w};
+        uint32_t f[4][8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) decode_columns<BITS>(wv[2 * q], wv[2 * q + 1], za[q], sa[q], f[q]);
+        uint8_t* dst = lds_b + par_b * B_BYTES + ((wave * 2 + (c >> 4)) * 4 * 64 + hh * 32 + (c & 15)) * 16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<u4*>(dst + ((j & 3) * 64 + (j >> 2) * 16) * 16) = u4{f[0][j], f[1][j], f[2][j], f[3][j]};
+    };
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+    load_s(st_begin);
+    load_w(st_begin);
+    load_a(st_begin);
+    store_s(st_begin, 0);
+    load_s(min(st_begin + 1, st_last));
+    store_s(min(st_begin + 1, st_last), 1);
+    load_s(min(st_begin + 2, st_last));
+    __syncthreads();
+    decode(0, 0);
+    load_w(min(st_begin + 1, st_last));
+    store_a(st_begin, 0);
+    load_a(min(st_begin + 1, st_last));
+    __syncthreads();
+    for (int st = st_begin; st < st_end; ++st) {
+        const int par = (st - st_begin) & 1;
+        decode(par ^ 1, par ^ 1);                    // stage st + 1
+        load_w(min(st + 2, st_last));
+        store_a(min(st + 1, st_last), par ^ 1);
+        load_a(min(st + 2, st_last));
+        store_s(min(st + 2, st_last), par);
+        load_s(min(st + 3, st_last));
+        const uint8_t* ab = lds_a + par * A_BYTES + (wm * (BM / 2) + c) * ROW;
+        const uint8_t* bb = lds_b + par * B_BYTES + (wn * 4 * 64 + lane) * 16;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            h8 af[TM], bf[TN];
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                af[i] = *reinterpret_cast<const h8*>(ab + i * 32 * ROW +
+                                                     ((uint32_t(2 * t + hh) ^ uint32_t(c & 7)) * 16u));
+#pragma unroll
+            for (int j = 0; j < TN; ++j) bf[j] = *reinterpret_cast<const h8*>(bb + (t * 8 + j) * 1024);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
+        }
+        __syncthreads();
+    }
+
+    // ---- acc[i][j][r]: row 32 i + 8 (r / 4) + 4 hh + r % 4, column
+    // 8 (c % 16) + 4 (c / 16) + j of the wavefront's BM/2 x 128
+    const int col = k0 + wn * 128 + 8 * (c & 15) + 4 * (c >> 4);
+    if (col >= p.K) return;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = m0 + wm * (BM / 2) + 32 * i + 8 * (r >> 2) + 4 * hh + (r & 3);
+            if (row >= p.M) continue;
+            const size_t at = size_t(row) * p.K + col;
+            float v[4] = {acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
+            if constexpr (PART) {
+                float* dst = p.part + size_t(blockIdx.y) * p.M * p.K + at;
+                *reinterpret_cast<f4*>(dst) = f4{v[0], v[1], v[2], v[3]};
+            } else {
+                if (p.add) {
+                    float b[4];
+                    load_h<4>(p.add + at, b);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] += b[q];
+                }
+                store_h<4>(p.dx + at, v);
+            }
+        }
+}
+
+// dx = fp16(sum over the ranges, in order, + add); with perm the sum of
+// packed column k' belongs to channel perm[k'].  Four columns per thread.
+__global__ void __launch_bounds__(256) block_dx_finish_kernel(const float* __restrict__ part, int splits, int M,
+                                                              int K, const int32_t* __restrict__ perm,
+                                                              const uint16_t* add, uint16_t* dx) {
+    const int per_row = K / 4;
+    const size_t total = size_t(M) * per_row, step = size_t(M) * K;
+    for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += size_t(gridDim.x) * 256) {
+        const size_t row = i / per_row;
+        const int k = int(i % per_row) * 4;
+        const float* src = part + row * K + k;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < splits; ++s, src += step) {
+            const f4 w = *reinterpret_cast<const f4*>(src);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += w[q];
+        }
+        if (perm) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const size_t at = row * K + perm[k + q];
+                dx[at] = f2h(v[q] + (add ? h2f(add[at]) : 0.f));
+            }
+        } else {
+            const size_t at = row * K + k;
+            if (add) {
+                float b[4];
+                load_h<4>(add + at, b);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += b[q];
+            }
+            store_h<4>(dx + at, v);
+        }
+    }
+}
+
+struct DxPlan {
+    int BM = 128, splits = 1, sps = 0;
+};
+
+// As the forward product's plan: tile height and split of the sum over the
+// weight rows by a time model.
+DxPlan dx_plan(int M, int R, int K, size_t part_bytes) {
+    const int cus = wqh::gemm_slots(1);
+    const int stages = (R + 63) / 64;
+    const int k_tiles = (K + 255) / 256;
+    DxPlan best;
+    best.sps = stages;
+    double best_us = 1e30;
+    const int heights[3] = {64, 128, 256};
+    for (int h = 0; h < 3; ++h) {
+        const int BM = heights[h];
+        const double stage_us = BM == 64 ? 0.4 : BM == 128 ? 0.7 : 1.2;
+        const int slots = cus;  // a block takes more than half of a unit's LDS
+        const long long tiles = (long long)((M + BM - 1) / BM) * k_tiles;
+        for (int S = 1; S <= 64; ++S) {
+            const int sps = (stages + S - 1) / S;
+            const int Se = (stages + sps - 1) / sps;
+            if (Se != S) continue;
+            if (S > 1 && (sps < 4 || double(Se) * M * K * 4.0 > double(part_bytes))) break;
+            const long long blocks = tiles * Se;
+            const double rounds = double((blocks + slots - 1) / slots);
+            double us = rounds * sps * stage_us + 3.0;
+            if (S > 1) us += 2.0 + double(Se) * M * K * 8.0 / 4e6;
+            if (us < best_us * 0.98) {
+                best_us = us;
+                best.BM = BM;
+                best.splits = Se;
+                best.sps = sps;
+            }
+        }
+    }
+    return best;
+}
+
+template <int BITS, bool HAS_Z, int BM, bool G8>
+wq_status launch_dx(const DxPlan& pl, bool part, const DxArgs& a, hipStream_t s) {
+    constexpr int lds = 2 * (BM * 128 + 256 * 128 + 2 * (G8 ? 8 : 4) * 128);
+    const dim3 grid(a.tiles, pl.splits), block(256);
+    auto go = [&](auto kern) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return wqh::hip_status(e);
+        hipLaunchKernelGGL(kern, grid, block, lds, s, a);
+        return wqh::launch_status();
+    };
+    return part ? go(block_dx_kernel<BITS, HAS_Z, BM, G8, true>) : go(block_dx_kernel<BITS, HAS_Z, BM, G8, false>);
+}
+
+template <int BITS, bool HAS_Z>
+wq_status launch_dx_bm(const DxPlan& pl, bool part, bool g8, const DxArgs& a, hipStream_t s) {
+    switch (pl.BM) {
+        case 64:
+            return g8 ? launch_dx<BITS, HAS_Z, 64, true>(pl, part, a, s)
+                      : launch_dx<BITS, HAS_Z, 64, false>(pl, part, a, s);
+        case 128:
+            return g8 ? launch_dx<BITS, HAS_Z, 128, true>(pl, part, a, s)
+                      : launch_dx<BITS, HAS_Z, 128, false>(pl, part, a, s);
+        default:
+            return g8 ? launch_dx<BITS, HAS_Z, 256, true>(pl, part, a, s)
+                      : launch_dx<BITS, HAS_Z, 256, false>(pl, part, a, s);
+    }
+}
+
+template <int BITS>
+wq_status launch_dx_bits(const DxPlan& pl, bool part, bool g8, const DxArgs& a, hipStream_t s) {
+    return a.zeros ? launch_dx_bm<BITS, true>(pl, part, g8, a, s) : launch_dx_bm<BITS, false>(pl, part, g8, a, s);
+}
+
+wq_status dx_finish(const float* part, int splits, int M, int K, const int32_t* perm, const uint16_t* add,
+                    uint16_t* dx, hipStream_t s) {
+    const size_t total = size_t(M) * (K / 4);
+    const int blocks = int(std::min<size_t>((total + 255) / 256, size_t(wqh::gemm_slots(8))));
+    hipLaunchKernelGGL(block_dx_finish_kernel, dim3(blocks), dim3(256), 0, s, part, splits, M, K, perm, add, dx);
+    return wqh::launch_status();
+}
+
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// dbias's row ranges: enough blocks to fill the machine, at least 16 rows
+// each (a partial row costs 4 bytes per column to write and read).
+int dbias_ranges(int M, int R) {
+    const int col_blocks = (R + 511) / 512;
+    const int want = (4 * wqh::gemm_slots(1) + col_blocks - 1) / col_blocks;
+    return std::max(1, std::min(want, (M + 15) / 16));
+}
+
+struct BwdBytes {
+    size_t dz, dbias, dx, split;  // dx: act-order's fp32 sums; split: what a split would like instead
+};
+
+BwdBytes bwd_bytes(int M, int R, int K, bool has_perm) {
+    BwdBytes b{};
+    b.dz = round256(size_t(M) * ((size_t(R) + 7) / 8 * 8) * 2);
+    b.dbias = round256(size_t(dbias_ranges(M, R)) * R * 4);
+    b.dx = has_perm ? size_t(M) * K * 4 : 0;
+    const DxPlan p = dx_plan(M, R, K, ~size_t(0) >> 1);
+    b.split = p.splits > 1 ? size_t(p.splits) * M * K * 4 : 0;
+    return b;
+}
+
+}  // namespace
+
+namespace wqh {
+
+size_t block_bwd_workspace_bytes(int M, int R, int K, bool has_perm) {
+    if (M <= 0 || R <= 0) return 0;
+    const BwdBytes b = bwd_bytes(M, R, K, has_perm);
+    return b.dz + b.dbias + std::max(b.dx, b.split);
+}
+
+wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool gated, const uint32_t* packed,
+                    const uint16_t* scales, const uint8_t* zeros, const int32_t* perm, const uint16_t* add,
+                    uint16_t* dx, uint16_t* dz, float* dbias, int M, int N, int K, int bits, int gs, void* workspace,
+                    size_t ws_bytes, hipStream_t s) {
+    const int R = gated ? 2 * N : N;
+    if (R == 0) {  // an empty sum
+        return M == 0 ? WQ_OK : dx_finish(nullptr, 0, M, K, nullptr, add, dx, s);
+    }
+    if (M == 0) {
+        if (!dbias) return WQ_OK;
+        hipLaunchKernelGGL(block_dbias_kernel, dim3((R + 255) / 256), dim3(256), 0, s, nullptr, 0, R, dbias);
+        return launch_status();
+    }
+    // ---- workspace: [dz][dbias partial sums][fp32 dx]
+    const bool none = act == WQ_ACT_NONE && !gated;
+    const bool aligned = R % 8 == 0;
+    const int ld = (R + 7) / 8 * 8;
+    const bool own_dz = !aligned || (!none && !dz);
+    const int ranges = dbias ? dbias_ranges(M, R) : 0;
+    char* w = static_cast<char*>(workspace);
+    size_t left = workspace ? ws_bytes : 0;
+    auto take = [&](size_t bytes) -> char* {
+        bytes = round256(bytes);
+        if (bytes > left) return nullptr;
+        char* r = w;
+        w += bytes;
+        left -= bytes;
+        return r;
+    };
+    uint16_t* dzp = nullptr;
+    float* dbp = nullptr;
+    if (own_dz && !(dzp = reinterpret_cast<uint16_t*>(take(size_t(M) * ld * 2)))) return WQ_ERR_ARG;
+    const uint16_t* operand = own_dz ? dzp : none ? dy : dz;
+    if (own_dz && aligned) {  // no padding: written as dz is
+        dz = dzp;
+        dzp = nullptr;
+    }
+    if (ranges > 1 && !(dbp = reinterpret_cast<float*>(take(size_t(ranges) * R * 4)))) return WQ_ERR_ARG;
+    if (perm && left < size_t(M) * K * 4) return WQ_ERR_ARG;
+
+    // ---- dz, dbias
+    if (!none || own_dz || dz || dbias) {
+        DzArgs a{dy, none ? nullptr : preact, dz, dzp, ranges > 1 ? dbp : dbias, M, N, R, ld, act, 0};
+        // without dbias: short row ranges, for many blocks
+        const int per = ranges ? (M + ranges - 1) / ranges
+                               : std::max((M + 65534) / 65535, std::max(4, std::min(32, (M + 63) / 64 * 4)));
+        a.rows_per = per;
+        const int gy = (M + per - 1) / per;
+        const bool wide = N % 8 == 0;
+        const int cols = 64 * (wide ? 8 : 1);
+        const dim3 grid((N + cols - 1) / cols, gy), block(64 * kDzRowLanes);
+        if (gated && wide)
+            hipLaunchKernelGGL((block_dz_kernel<true, 8>), grid, block, 0, s, a);
+        else if (gated)
+            hipLaunchKernelGGL((block_dz_kernel<true, 1>), grid, block, 0, s, a);
+        else if (wide)
+            hipLaunchKernelGGL((block_dz_kernel<false, 8>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((block_dz_kernel<false, 1>), grid, block, 0, s, a);
+        wq_status st = launch_status();
+        if (st != WQ_OK) return st;
+        if (ranges > 1) {
+            hipLaunchKernelGGL(block_dbias_kernel, dim3((R + 255) / 256), dim3(256), 0, s, dbp, gy, R, dbias);
+            st = launch_status();
+            if (st != WQ_OK) return st;
+        }
+    }
+
+    // ---- dx
+    const DxPlan pl = dx_plan(M, R, K, left);
+    const bool part = perm || pl.splits > 1;
+    const int m_tiles = (M + pl.BM - 1) / pl.BM, k_tiles = (K + 255) / 256;
+    const DxArgs a{operand, packed, scales, zeros, add, dx, reinterpret_cast<float*>(w), M, R, K,
+                   ld, group_magic(gs), m_tiles, k_tiles, m_tiles * k_tiles, pl.sps};
+    const bool g8 = gs < 64;
+    wq_status st;
+    switch (bits) {
+        case 2: st = launch_dx_bits<2>(pl, part, g8, a, s); break;
+        case 3: st = launch_dx_bits<3>(pl, part, g8, a, s); break;
+        case 4: st = launch_dx_bits<4>(pl, part, g8, a, s); break;
+        default: st = launch_dx_bits<8>(pl, part, g8, a, s); break;
+    }
+    if (st != WQ_OK || !part) return st;
+    return dx_finish(a.part, pl.splits, M, K, perm, add, dx, s);
+}
+
+}  // namespace wqh

@@ -458,6 +458,19 @@ wq_status splitk_reduce(const float* part, int splits, int M, int N, uint16_t* y
     return launch_status();
 }
 
+wq_status gather_activations(const uint16_t* x, const int32_t* perm, int M, int K, uint16_t* x_out, hipStream_t s) {
+    if (size_t(K) * 2 <= 64 * 1024) {
+        hipLaunchKernelGGL(gather_rows_kernel, dim3(std::min(M, 65535)), dim3(256), size_t(K) * 2, s, x, perm, M, K,
+                           x_out);
+    } else {
+        const long long total = (long long)M * K;
+        long long blocks = (total + 255) / 256;
+        if (blocks > 65536) blocks = 65536;
+        hipLaunchKernelGGL(gather_act_kernel, dim3(int(blocks)), dim3(256), 0, s, x, perm, M, K, x_out);
+    }
+    return launch_status();
+}
+
 wq_status gemm_f32(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, const uint8_t* zeros,
                    float* y32, int M, int N, int K, int bits, int gs, hipStream_t s) {
     switch (bits) {
@@ -505,16 +518,7 @@ extern "C" wq_status wq_gemm(const uint16_t* x, const uint32_t* packed, const ui
     if (perm) {
         if (!workspace || workspace_bytes < size_t(M) * size_t(K) * 2) return WQ_ERR_ARG;
         uint16_t* xg = static_cast<uint16_t*>(workspace);
-        if (size_t(K) * 2 <= 64 * 1024) {
-            hipLaunchKernelGGL(gather_rows_kernel, dim3(std::min(M, 65535)), dim3(256), size_t(K) * 2, s, x, perm,
-                               int(M), int(K), xg);
-        } else {
-            long long total = (long long)M * K;
-            long long blocks = (total + 255) / 256;
-            if (blocks > 65536) blocks = 65536;
-            hipLaunchKernelGGL(gather_act_kernel, dim3(int(blocks)), dim3(256), 0, s, x, perm, int(M), int(K), xg);
-        }
-        const wq_status ls = wqh::launch_status();
+        const wq_status ls = wqh::gather_activations(x, perm, M, K, xg, s);
         if (ls != WQ_OK) return ls;
         xa = xg;
     }

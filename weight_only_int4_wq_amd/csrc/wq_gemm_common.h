@@ -26,6 +26,35 @@ __device__ __forceinline__ void load_chunk_b(const uint32_t* p, uint32_t* w) {
     }
 }
 
+// Natural-order pairs (codes 2i, 2i+1 of block b) as fp16 pairs that differ
+// from (q_{2i}, q_{2i+1}) by the constants of zero_pair_nat.
+template <int BITS>
+__device__ __forceinline__ void decode_nat(const uint32_t* w, int b, uint32_t* h) {
+    if constexpr (BITS == 4) {
+        // Byte i of the block word holds codes 2i (low nibble) and 2i+1 (high
+        // nibble).  Copy it into bytes 0 and 2, then keep the low nibble in
+        // the low half under 0x6400 (1024 + q, unit step) and the high nibble
+        // in bits 4..7 of the high half under 0x5400 (64 + q, step 1/16 * 16).
+        const uint32_t v = w[b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t sel = 0x0C000C00u | (uint32_t(i) << 16) | uint32_t(i);
+            h[i] = and_or(__builtin_amdgcn_perm(v, v, sel), 0x00F0000Fu, 0x54006400u);
+        }
+    } else {
+        decode_block_nat<BITS>(w, b, h);
+    }
+}
+
+// The pair subtracted from decode_nat's output to leave q - z exactly.
+template <int BITS>
+__device__ __forceinline__ uint32_t zero_pair_nat(uint32_t z) {
+    if constexpr (BITS == 4)
+        return (0x6400u | z) | ((0x5400u | (z << 4)) << 16);
+    else
+        return zero_pair(z);
+}
+
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
 
@@ -120,6 +149,9 @@ int gemm_slots(int blocks_per_cu);
 
 // y[m][n] = fp16(sum over ranges r = 0..splits-1, in order, of part[r][m][n]).
 wq_status splitk_reduce(const float* part, int splits, int M, int N, uint16_t* y, hipStream_t s);
+
+// x_out[m][k'] = x[m][perm[k']]: activations in packed column order.
+wq_status gather_activations(const uint16_t* x, const int32_t* perm, int M, int K, uint16_t* x_out, hipStream_t s);
 
 // Large-M prefill GEMM (128 x 256 tiles on 32x32x16 instructions).  Its
 // offsets are 32-bit: usable when gemm_large_fits().

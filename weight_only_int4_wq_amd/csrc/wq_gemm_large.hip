@@ -39,35 +39,6 @@ using namespace wq;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Natural-order pairs (codes 2i, 2i+1 of block b) as fp16 pairs that differ
-// from (q_{2i}, q_{2i+1}) by the constants of zero_pair_nat.
-template <int BITS>
-__device__ __forceinline__ void decode_nat(const uint32_t* w, int b, uint32_t* h) {
-    if constexpr (BITS == 4) {
-        // Byte i of the block word holds codes 2i (low nibble) and 2i+1 (high
-        // nibble).  Copy it into bytes 0 and 2, then keep the low nibble in
-        // the low half under 0x6400 (1024 + q, unit step) and the high nibble
-        // in bits 4..7 of the high half under 0x5400 (64 + q, step 1/16 * 16).
-        const uint32_t v = w[b];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t sel = 0x0C000C00u | (uint32_t(i) << 16) | uint32_t(i);
-            h[i] = and_or(__builtin_amdgcn_perm(v, v, sel), 0x00F0000Fu, 0x54006400u);
-        }
-    } else {
-        decode_block_nat<BITS>(w, b, h);
-    }
-}
-
-// The pair subtracted from decode_nat's output to leave q - z exactly.
-template <int BITS>
-__device__ __forceinline__ uint32_t zero_pair_nat(uint32_t z) {
-    if constexpr (BITS == 4)
-        return (0x6400u | z) | ((0x5400u | (z << 4)) << 16);
-    else
-        return zero_pair(z);
-}
-
 template <int BITS, bool HAS_Z, bool FAST, bool PART, int BM>
 __global__ void __launch_bounds__(256) gemm_large_kernel(const uint16_t* __restrict__ x,
                                                          const uint32_t* __restrict__ packed,
