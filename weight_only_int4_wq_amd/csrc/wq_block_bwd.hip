@@ -128,6 +128,11 @@ __global__ void __launch_bounds__(256) block_dbias_kernel(const float* __restric
 
 // ------------------------------------------------------------------ dx ----
 
+// Vector instructions issued after each matrix instruction.
+#ifndef WQ_BLOCK_DX_VALU
+#define WQ_BLOCK_DX_VALU 4
+#endif
+
 struct DxArgs {
     const uint16_t* dz;  // [M][ld], ld a multiple of 8, zero from R to ld
     const uint32_t* packed;
@@ -135,7 +140,7 @@ struct DxArgs {
     const uint8_t* zeros;
     const uint16_t* add;  // [M][K], nullable, may be dx
     uint16_t* dx;
-    float* part;  // [splits][M][K]
+    float* part;  // [splits][M][K], or null
     int M, R, K, ld;
     GroupDiv gd;
     int m_tiles, k_tiles, tiles, sps;
@@ -169,47 +174,40 @@ __device__ __forceinline__ void load_row_block(const char* row, uint32_t blk, ui
     }
 }
 
-// Decode rows (2 p, 2 p + 1)'s blocks a, b: out[j] = column j of both rows as
-// a pair, (q - z) * s with the two rows' own z and s.
+// Columns 2 i and 2 i + 1 of two neighbouring rows' blocks a and b: out[0] and
+// out[1] hold the pairs (row of a, row of b) of (q - z) * s, each row with its
+// own z and s.
 template <int BITS>
-__device__ __forceinline__ void decode_columns(const uint32_t* a, const uint32_t* b, uint32_t z, uint32_t ss,
-                                               uint32_t (&out)[8]) {
+__device__ __forceinline__ void decode_columns(int i, const uint32_t* a, const uint32_t* b, uint32_t z, uint32_t ss,
+                                               uint32_t (&out)[2]) {
     const uint32_t ze = z | kMagic2;
     if constexpr (BITS == 4) {
-        const uint32_t zo = (z << 4) | 0x54005400u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t sel = 0x0C000C00u | ((4u + i) << 16) | uint32_t(i);
-            const uint32_t t = __builtin_amdgcn_perm(b[0], a[0], sel);
-            out[2 * i] = as_u32(dequant_pair(and_or(t, 0x000F000Fu, kMagic2), ze, ss));
-            out[2 * i + 1] = as_u32(dequant_pair(and_or(t, 0x00F000F0u, 0x54005400u), zo, ss));
-        }
+        const uint32_t sel = 0x0C000C00u | ((4u + i) << 16) | uint32_t(i);
+        const uint32_t t = __builtin_amdgcn_perm(b[0], a[0], sel);
+        out[0] = as_u32(dequant_pair(and_or(t, 0x000F000Fu, kMagic2), ze, ss));
+        out[1] = as_u32(dequant_pair(and_or(t, 0x00F000F0u, 0x54005400u), (z << 4) | 0x54005400u, ss));
     } else if constexpr (BITS == 8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t i = uint32_t(j & 3);
-            const uint32_t sel = 0x0C000C00u | ((4u + i) << 16) | i;
-            out[j] = as_u32(dequant_pair(__builtin_amdgcn_perm(b[j >> 2], a[j >> 2], sel) | kMagic2, ze, ss));
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t k = uint32_t((2 * i + e) & 3), w = uint32_t(2 * i) >> 2;
+            const uint32_t sel = 0x0C000C00u | ((4u + k) << 16) | k;
+            out[e] = as_u32(dequant_pair(__builtin_amdgcn_perm(b[w], a[w], sel) | kMagic2, ze, ss));
         }
     } else if constexpr (BITS == 2) {
-        const uint32_t t = a[0] | (b[0] << 16);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            out[j] = as_u32(dequant_pair(and_or(t >> (2 * j), 0x00030003u, kMagic2), ze, ss));
+        const uint32_t t = (a[0] | (b[0] << 16)) >> (4 * i);
+        out[0] = as_u32(dequant_pair(and_or(t, 0x00030003u, kMagic2), ze, ss));
+        out[1] = as_u32(dequant_pair(and_or(t >> 2, 0x00030003u, kMagic2), ze, ss));
     } else {
-        const uint32_t lo = (a[0] & 0xFFFu) | (b[0] << 16);  // bits 12.. of b's half are masked below
-        const uint32_t hi = (a[0] >> 12) | ((b[0] >> 12) << 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            out[j] = as_u32(dequant_pair(and_or(lo >> (3 * j), 0x00070007u, kMagic2), ze, ss));
-            out[4 + j] = as_u32(dequant_pair(and_or(hi >> (3 * j), 0x00070007u, kMagic2), ze, ss));
-        }
+        // six bits of each row; what b's half carries above them is masked
+        const uint32_t t = ((a[0] >> (6 * i)) & 0x3Fu) | ((b[0] >> (6 * i)) << 16);
+        out[0] = as_u32(dequant_pair(and_or(t, 0x00070007u, kMagic2), ze, ss));
+        out[1] = as_u32(dequant_pair(and_or(t >> 3, 0x00070007u, kMagic2), ze, ss));
     }
 }
 
 // G8: groups of 32 channels, up to 8 groups per tile; otherwise up to 4
 // (group sizes of 64 and more, tiles start at multiples of 256).
-template <int BITS, bool HAS_Z, int BM, bool G8, bool PART>
+template <int BITS, int BM, bool G8>
 __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
     constexpr int BK = 64, TM = BM / 64, TN = 4;
     constexpr int ROW = BK * 2;
@@ -249,32 +247,34 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
         for (int i = 0; i < AU; ++i) av[i] = *reinterpret_cast<const u4*>(abase + (a_off[i] + n));
     };
     auto store_a = [&](int st, int par) {
-        if (st * BK + 8 * au >= p.ld) {  // only in a last stage that R ends in
-#pragma unroll
-            for (int i = 0; i < AU; ++i) av[i] = u4{0u, 0u, 0u, 0u};
-        }
+        const uint32_t keep = st * BK + 8 * au < p.ld ? ~0u : 0u;  // zeros past R
         uint8_t* buf = lds_a + par * A_BYTES;
 #pragma unroll
         for (int i = 0; i < AU; ++i)
-            *reinterpret_cast<u4*>(buf + (ar + 32 * i) * ROW + ((au ^ (ar & 7)) * 16)) = av[i];
+            *reinterpret_cast<u4*>(buf + (ar + 32 * i) * ROW + ((au ^ ((ar >> 1) & 7)) * 16)) =
+                av[i] & u4{keep, keep, keep, keep};
     };
 
     // ---- scales and zero-points: thread t takes row t % 64 of groups t / 64
     // (and t / 64 + 4), rows past R with scale 0
     const int g0 = chunk_group(k0 / 32, p.gd);
     const int g_last = chunk_group(min(k0 / 32 + 7, chunks - 1), p.gd);
-    uint32_t sv[NG / 4], zv[NG / 4];
+    const uint8_t* zp = p.zeros ? p.zeros : reinterpret_cast<const uint8_t*>(p.scales);  // always loaded
+    uint32_t sv[NG / 4], zv[NG / 4], s_off[NG / 4];
+    int s_g[NG / 4];
+#pragma unroll
+    for (int i = 0; i < NG / 4; ++i) {
+        s_g[i] = min(g0 + (tid >> 6) + 4 * i, g_last);
+        s_off[i] = uint32_t(tid & 63) * uint32_t(G) + uint32_t(s_g[i]);
+    }
     auto load_s = [&](int st) {
-        const int n = st * BK + (tid & 63);
-        const size_t row = size_t(min(n, p.R - 1)) * G;
+        const size_t row0 = size_t(st) * BK * G;
+        const uint32_t most = uint32_t(min(p.R - 1 - st * BK, BK - 1)) * uint32_t(G);  // the last row's
 #pragma unroll
         for (int i = 0; i < NG / 4; ++i) {
-            const int g = min(g0 + (tid >> 6) + 4 * i, g_last);
-            sv[i] = p.scales[row + g];
-            if constexpr (HAS_Z)
-                zv[i] = p.zeros[row + g];
-            else
-                zv[i] = 1u << (BITS - 1);
+            const uint32_t o = min(s_off[i], most + uint32_t(s_g[i]));
+            sv[i] = (p.scales + row0)[o];
+            zv[i] = (zp + row0)[o];
         }
     };
     auto store_s = [&](int st, int par) {
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
         for (int i = 0; i < NG / 4; ++i) {
             const int at = ((tid >> 6) + 4 * i) * BK + (tid & 63);
             s[at] = in ? uint16_t(sv[i]) : uint16_t(0);
-            s[NG * BK + at] = uint16_t(zv[i]);
+            s[NG * BK + at] = uint16_t(p.zeros ? zv[i] : 1u << (BITS - 1));
         }
     };
 
@@ -294,28 +294,36 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
     const uint32_t blk = uint32_t(min(k0 / 8 + c, p.K / 8 - 1));
     const int lg = chunk_group(int(blk >> 2), p.gd) - g0;
     const size_t row_bytes = size_t(chunks) * BITS * 4;
-    uint32_t wv[8][W];
-    auto load_w = [&](int st) {
-        const char* base = reinterpret_cast<const char*>(p.packed) + size_t(st) * BK * row_bytes;
-        const int left = p.R - 1 - st * BK;
+    uint32_t wv[8][W], wnext[8][W];  // the next stage's words, the one's after
+    uint32_t w_off[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int n = min(16 * wave + 8 * hh + i, left);
-            load_row_block<BITS>(base + uint32_t(n) * uint32_t(row_bytes), blk, wv[i]);
-        }
+    for (int i = 0; i < 8; ++i) w_off[i] = uint32_t(16 * wave + 8 * hh + i) * uint32_t(row_bytes);
+    auto load_w = [&](int st, uint32_t (&w)[8][W]) {
+        const char* base = reinterpret_cast<const char*>(p.packed) + size_t(st) * BK * row_bytes;
+        const uint32_t most = uint32_t(min(p.R - 1 - st * BK, BK - 1)) * uint32_t(row_bytes);  // the last row
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load_row_block<BITS>(base + min(w_off[i], most), blk, w[i]);
     };
-    auto decode = [&](int par_s, int par_b) {
-        const uint8_t* s = lds_s + par_s * 2 * S_BYTES + (lg * BK + 16 * wave + 8 * hh) * 2;
+    // Column pairs i0 .. i1 - 1 (of 4) of the wavefront's share, into LDS in
+    // the fragments' order.
+    auto decode = [&](int par, int i0, int i1) {
+        const uint8_t* s = lds_s + par * 2 * S_BYTES + (lg * BK + 16 * wave + 8 * hh) * 2;
         const u4 ss = *reinterpret_cast<const u4*>(s);
         const u4 zz = *reinterpret_cast<const u4*>(s + S_BYTES);
         const uint32_t sa[4] = {ss.x, ss.y, ss.z, ss.w}, za[4] = {zz.x, zz.y, zz.z, zz.w};
-        uint32_t f[4][8];
+        uint8_t* dst = lds_b + par * B_BYTES + ((wave * 2 + (c >> 4)) * 4 * 64 + hh * 32 + (c & 15)) * 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) decode_columns<BITS>(wv[2 * q], wv[2 * q + 1], za[q], sa[q], f[q]);
-        uint8_t* dst = lds_b + par_b * B_BYTES + ((wave * 2 + (c >> 4)) * 4 * 64 + hh * 32 + (c & 15)) * 16;
+        for (int i = i0; i < i1; ++i) {
+            uint32_t f[4][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<u4*>(dst + ((j & 3) * 64 + (j >> 2) * 16) * 16) = u4{f[0][j], f[1][j], f[2][j], f[3][j]};
+            for (int q = 0; q < 4; ++q) decode_columns<BITS>(i, wv[2 * q], wv[2 * q + 1], za[q], sa[q], f[q]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = 2 * i + e;
+                *reinterpret_cast<u4*>(dst + ((j & 3) * 64 + (j >> 2) * 16) * 16) =
+                    u4{f[0][e], f[1][e], f[2][e], f[3][e]};
+            }
+        }
     };
 
     f32x16 acc[TM][TN];
@@ -326,45 +334,67 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
+    auto read_ab = [&](int par, int t, h8 (&a)[TM], h8 (&b)[TN]) {
+        const uint8_t* ab = lds_a + par * A_BYTES + (wm * (BM / 2) + c) * ROW +
+                            ((uint32_t(2 * t + hh) ^ uint32_t((c >> 1) & 7)) * 16u);
+        const uint8_t* bb = lds_b + par * B_BYTES + (wn * 4 * 64 + lane) * 16 + t * 8192;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = *reinterpret_cast<const h8*>(ab + i * 32 * ROW);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = *reinterpret_cast<const h8*>(bb + j * 1024);
+    };
+    auto multiply = [&](const h8 (&a)[TM], const h8 (&b)[TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i], b[j], acc[i][j], 0, 0, 0);
+    };
+    constexpr int NM = TM * TN, NR = TM + TN, NV = WQ_BLOCK_DX_VALU;
+
     load_s(st_begin);
-    load_w(st_begin);
+    load_w(st_begin, wv);
     load_a(st_begin);
     store_s(st_begin, 0);
     load_s(min(st_begin + 1, st_last));
     store_s(min(st_begin + 1, st_last), 1);
-    load_s(min(st_begin + 2, st_last));
     __syncthreads();
-    decode(0, 0);
-    load_w(min(st_begin + 1, st_last));
+    decode(0, 0, 4);
     store_a(st_begin, 0);
+    // (in the loop's order, so that its waits count the same loads from the
+    // first stage on)
+    load_w(min(st_begin + 1, st_last), wnext);
+    load_s(min(st_begin + 2, st_last));
     load_a(min(st_begin + 1, st_last));
     __syncthreads();
+    h8 af[2][TM], bf[2][TN];
+    read_ab(0, 0, af[0], bf[0]);
     for (int st = st_begin; st < st_end; ++st) {
         const int par = (st - st_begin) & 1;
-        decode(par ^ 1, par ^ 1);                    // stage st + 1
-        load_w(min(st + 2, st_last));
-        store_a(min(st + 1, st_last), par ^ 1);
-        load_a(min(st + 2, st_last));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int w = 0; w < W; ++w) wv[i][w] = wnext[i][w];
+        read_ab(par, 1, af[1], bf[1]);
+        load_w(min(st + 2, st_last), wnext);
+        decode(par ^ 1, 0, 2);  // stage st + 1
+        multiply(af[0], bf[0]);
+        sched_step<NM, NR + 2, 4, 8, NV>();
+        read_ab(par, 2, af[0], bf[0]);
+        decode(par ^ 1, 2, 4);
         store_s(min(st + 2, st_last), par);
         load_s(min(st + 3, st_last));
-        const uint8_t* ab = lds_a + par * A_BYTES + (wm * (BM / 2) + c) * ROW;
-        const uint8_t* bb = lds_b + par * B_BYTES + (wn * 4 * 64 + lane) * 16;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            h8 af[TM], bf[TN];
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                af[i] = *reinterpret_cast<const h8*>(ab + i * 32 * ROW +
-                                                     ((uint32_t(2 * t + hh) ^ uint32_t(c & 7)) * 16u));
-#pragma unroll
-            for (int j = 0; j < TN; ++j) bf[j] = *reinterpret_cast<const h8*>(bb + (t * 8 + j) * 1024);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
-        }
+        multiply(af[1], bf[1]);
+        sched_step<NM, NR + 2, 4 + NG / 2, NG / 2, NV>();
+        read_ab(par, 3, af[1], bf[1]);
+        store_a(min(st + 1, st_last), par ^ 1);
+        load_a(min(st + 2, st_last));
+        multiply(af[0], bf[0]);
+        sched_step<NM, NR, AU, AU, NV>();
         __syncthreads();
+        read_ab(par ^ 1, 0, af[0], bf[0]);
+        multiply(af[1], bf[1]);
+        sched_step<NM, NR, 0, 0, NV>();
     }
 
     // ---- acc[i][j][r]: row 32 i + 8 (r / 4) + 4 hh + r % 4, column
@@ -379,7 +409,7 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
             if (row >= p.M) continue;
             const size_t at = size_t(row) * p.K + col;
             float v[4] = {acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
-            if constexpr (PART) {
+            if (p.part) {
                 float* dst = p.part + size_t(blockIdx.y) * p.M * p.K + at;
                 *reinterpret_cast<f4*>(dst) = f4{v[0], v[1], v[2], v[3]};
             } else {
@@ -430,77 +460,31 @@ __global__ void __launch_bounds__(256) block_dx_finish_kernel(const float* __res
     }
 }
 
-struct DxPlan {
-    int BM = 128, splits = 1, sps = 0;
-};
+constexpr wqh::TileCost kDxCosts[3] = {
+    {64, 0.80, 0.28, 6.0, false}, {128, 1.09, 0.27, 6.5, false}, {256, 1.37, 0.30, 9.9, false}};
 
-// As the forward product's plan: tile height and split of the sum over the
-// weight rows by a time model.
-DxPlan dx_plan(int M, int R, int K, size_t part_bytes) {
-    const int cus = wqh::gemm_slots(1);
-    const int stages = (R + 63) / 64;
-    const int k_tiles = (K + 255) / 256;
-    DxPlan best;
-    best.sps = stages;
-    double best_us = 1e30;
-    const int heights[3] = {64, 128, 256};
-    for (int h = 0; h < 3; ++h) {
-        const int BM = heights[h];
-        const double stage_us = BM == 64 ? 0.4 : BM == 128 ? 0.7 : 1.2;
-        const int slots = cus;  // a block takes more than half of a unit's LDS
-        const long long tiles = (long long)((M + BM - 1) / BM) * k_tiles;
-        for (int S = 1; S <= 64; ++S) {
-            const int sps = (stages + S - 1) / S;
-            const int Se = (stages + sps - 1) / sps;
-            if (Se != S) continue;
-            if (S > 1 && (sps < 4 || double(Se) * M * K * 4.0 > double(part_bytes))) break;
-            const long long blocks = tiles * Se;
-            const double rounds = double((blocks + slots - 1) / slots);
-            double us = rounds * sps * stage_us + 3.0;
-            if (S > 1) us += 2.0 + double(Se) * M * K * 8.0 / 4e6;
-            if (us < best_us * 0.98) {
-                best_us = us;
-                best.BM = BM;
-                best.splits = Se;
-                best.sps = sps;
-            }
-        }
-    }
-    return best;
+wqh::TilePlan dx_plan(int M, int R, int K, size_t part_bytes) {
+    return wqh::plan_tiles(M, (K + 255) / 256, (R + 63) / 64, K, kDxCosts, 1, part_bytes, wqh::gemm_slots(1));
 }
 
-template <int BITS, bool HAS_Z, int BM, bool G8>
-wq_status launch_dx(const DxPlan& pl, bool part, const DxArgs& a, hipStream_t s) {
+template <int BITS, int BM, bool G8>
+wq_status launch_dx(const wqh::TilePlan& pl, const DxArgs& a, hipStream_t s) {
     constexpr int lds = 2 * (BM * 128 + 256 * 128 + 2 * (G8 ? 8 : 4) * 128);
-    const dim3 grid(a.tiles, pl.splits), block(256);
-    auto go = [&](auto kern) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return wqh::hip_status(e);
-        hipLaunchKernelGGL(kern, grid, block, lds, s, a);
-        return wqh::launch_status();
-    };
-    return part ? go(block_dx_kernel<BITS, HAS_Z, BM, G8, true>) : go(block_dx_kernel<BITS, HAS_Z, BM, G8, false>);
-}
-
-template <int BITS, bool HAS_Z>
-wq_status launch_dx_bm(const DxPlan& pl, bool part, bool g8, const DxArgs& a, hipStream_t s) {
-    switch (pl.BM) {
-        case 64:
-            return g8 ? launch_dx<BITS, HAS_Z, 64, true>(pl, part, a, s)
-                      : launch_dx<BITS, HAS_Z, 64, false>(pl, part, a, s);
-        case 128:
-            return g8 ? launch_dx<BITS, HAS_Z, 128, true>(pl, part, a, s)
-                      : launch_dx<BITS, HAS_Z, 128, false>(pl, part, a, s);
-        default:
-            return g8 ? launch_dx<BITS, HAS_Z, 256, true>(pl, part, a, s)
-                      : launch_dx<BITS, HAS_Z, 256, false>(pl, part, a, s);
-    }
+    auto kern = block_dx_kernel<BITS, BM, G8>;
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return wqh::hip_status(e);
+    hipLaunchKernelGGL(kern, dim3(a.tiles, pl.splits), dim3(256), lds, s, a);
+    return wqh::launch_status();
 }
 
 template <int BITS>
-wq_status launch_dx_bits(const DxPlan& pl, bool part, bool g8, const DxArgs& a, hipStream_t s) {
-    return a.zeros ? launch_dx_bm<BITS, true>(pl, part, g8, a, s) : launch_dx_bm<BITS, false>(pl, part, g8, a, s);
+wq_status launch_dx_bits(const wqh::TilePlan& pl, bool g8, const DxArgs& a, hipStream_t s) {
+    switch (pl.BM) {
+        case 64: return g8 ? launch_dx<BITS, 64, true>(pl, a, s) : launch_dx<BITS, 64, false>(pl, a, s);
+        case 128: return g8 ? launch_dx<BITS, 128, true>(pl, a, s) : launch_dx<BITS, 128, false>(pl, a, s);
+        default: return g8 ? launch_dx<BITS, 256, true>(pl, a, s) : launch_dx<BITS, 256, false>(pl, a, s);
+    }
 }
 
 wq_status dx_finish(const float* part, int splits, int M, int K, const int32_t* perm, const uint16_t* add,
@@ -530,7 +514,7 @@ BwdBytes bwd_bytes(int M, int R, int K, bool has_perm) {
     b.dz = round256(size_t(M) * ((size_t(R) + 7) / 8 * 8) * 2);
     b.dbias = round256(size_t(dbias_ranges(M, R)) * R * 4);
     b.dx = has_perm ? size_t(M) * K * 4 : 0;
-    const DxPlan p = dx_plan(M, R, K, ~size_t(0) >> 1);
+    const wqh::TilePlan p = dx_plan(M, R, K, ~size_t(0));
     b.split = p.splits > 1 ? size_t(p.splits) * M * K * 4 : 0;
     return b;
 }
@@ -614,18 +598,18 @@ wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool ga
     }
 
     // ---- dx
-    const DxPlan pl = dx_plan(M, R, K, left);
+    const TilePlan pl = dx_plan(M, R, K, left);
     const bool part = perm || pl.splits > 1;
     const int m_tiles = (M + pl.BM - 1) / pl.BM, k_tiles = (K + 255) / 256;
-    const DxArgs a{operand, packed, scales, zeros, add, dx, reinterpret_cast<float*>(w), M, R, K,
+    const DxArgs a{operand, packed, scales, zeros, add, dx, part ? reinterpret_cast<float*>(w) : nullptr, M, R, K,
                    ld, group_magic(gs), m_tiles, k_tiles, m_tiles * k_tiles, pl.sps};
     const bool g8 = gs < 64;
     wq_status st;
     switch (bits) {
-        case 2: st = launch_dx_bits<2>(pl, part, g8, a, s); break;
-        case 3: st = launch_dx_bits<3>(pl, part, g8, a, s); break;
-        case 4: st = launch_dx_bits<4>(pl, part, g8, a, s); break;
-        default: st = launch_dx_bits<8>(pl, part, g8, a, s); break;
+        case 2: st = launch_dx_bits<2>(pl, g8, a, s); break;
+        case 3: st = launch_dx_bits<3>(pl, g8, a, s); break;
+        case 4: st = launch_dx_bits<4>(pl, g8, a, s); break;
+        default: st = launch_dx_bits<8>(pl, g8, a, s); break;
     }
     if (st != WQ_OK || !part) return st;
     return dx_finish(a.part, pl.splits, M, K, perm, add, dx, s);

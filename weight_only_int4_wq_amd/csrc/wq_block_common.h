@@ -12,6 +12,133 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ float h2f(uint16_t v) { return float(__builtin_bit_cast(_Float16, v)); }
 __device__ __forceinline__ uint16_t f2h(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 
+// Items (of `total`, spread evenly over steps first .. first + len - 1) that
+// fall on step m.
+constexpr int step_share(int total, int first, int len, int m) {
+    return m < first || m >= first + len ? 0 : total * (m - first + 1) / len - total * (m - first) / len;
+}
+
+// Issue order of one k-step of a software-pipelined product: after each of
+// its NM matrix instructions a share of the step's NR LDS reads (first half),
+// NS LDS writes and NL loads (second half), and NV vector instructions.  In-order
+// issue would otherwise hold all of them behind the matrix instructions.
+template <int NM, int NR, int NS, int NL, int NV, int M = 0>
+__device__ __forceinline__ void sched_step() {
+    if constexpr (M < NM) {
+        constexpr int H = NM / 2;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (step_share(NR, 0, H, M) > 0)
+            __builtin_amdgcn_sched_group_barrier(0x100, step_share(NR, 0, H, M), 0);
+        if constexpr (step_share(NS, H, NM - H, M) > 0)
+            __builtin_amdgcn_sched_group_barrier(0x200, step_share(NS, H, NM - H, M), 0);
+        if constexpr (step_share(NL, H, NM - H, M) > 0)
+            __builtin_amdgcn_sched_group_barrier(0x020, step_share(NL, H, NM - H, M), 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, NV, 0);
+        sched_step<NM, NR, NS, NL, NV, M + 1>();
+    } else {
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ------------------------------------------------ copies into LDS ----
+//
+// Tiles go from memory straight into LDS (no registers, no LDS writes, which
+// hold a wavefront up by 25 cycles each where a read costs it 3).  A copy is
+// an asm statement that writes no register: for its own form the compiler
+// would wait for every copy in flight before any read of LDS that it cannot
+// tell from the copy's target.  It does not know of these copies, so
+//  - a target must be free when the copy is issued: behind the barrier that
+//    follows its last reads;
+//  - copies_landed<N>() (all but the wavefront's newest N loads and copies
+//    are complete) comes before the barrier that publishes them;
+//  - a kernel that leaves copies in flight across its waits (N > 0) has no
+//    other memory loads there, or waits for them too.
+// m0 (the target's LDS address) holds nothing else in these kernels.
+
+// Buffer resource over `bytes` bytes at p (at most 2 GiB of them): accesses
+// add a 32-bit offset to it, and those past its end read zeros.
+__device__ __forceinline__ u4 copy_source(const void* p, uint64_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    u4 r;
+    r.x = __builtin_amdgcn_readfirstlane(uint32_t(at));
+    r.y = __builtin_amdgcn_readfirstlane(uint32_t(at >> 32) & 0xFFFFu);  // stride 0
+    r.z = __builtin_amdgcn_readfirstlane(bytes < 0x80000000u ? uint32_t(bytes) : 0x80000000u);
+    r.w = 0x00020000u;  // raw 32-bit data
+    return r;
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every resource's end
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((lptr_t)(p)));
+}
+
+// Lane l's B bytes at offset `off` to lds + 16 l (B = 16 and 12) or lds + 4 l
+// (2 and 1, zero-extended to 4 bytes).
+template <int B>
+__device__ __forceinline__ void copy_to_lds(u4 src, uint32_t off, uint32_t lds) {
+    const uint32_t l = __builtin_amdgcn_readfirstlane(lds);
+    if constexpr (B == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+    else if constexpr (B == 12)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+    else if constexpr (B == 2)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+}
+
+template <int N>
+__device__ __forceinline__ void copies_landed() {
+    static_assert(N < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// 64-column stages of a BM-row tile of a row-major fp16 matrix, into
+// [BM][64] with 16-byte unit u of row r at position u ^ ((r / 2) mod 8): 16
+// consecutive rows read at one u fall on all 64 banks.  Copy i of a wavefront
+// fills rows 8 (wave COPIES + i) + l / 8, lane l the row's position l % 8;
+// eight lanes read one 128-byte line.  Rows past the matrix and columns past
+// `cols` (a multiple of 8) become zeros.  Offsets are below 2^31: 256 rows of
+// at most 2^22 columns.
+template <int BM>
+struct TileCopy {
+    static constexpr int COPIES = BM / 32;  // of 1 KB per wavefront and stage
+    u4 src;
+    uint32_t off[2];  // byte offset of an even and of an odd copy, without its 8-row steps
+    uint32_t u0;      // unit of an even copy (an odd one's is u0 ^ 4)
+    uint32_t cols, row8, wave;
+
+    // first: the tile's first row; rows: how many the matrix has from there
+    __device__ __forceinline__ TileCopy(const uint16_t* first, int rows, int cols_, int wave_, int lane)
+        : src(copy_source(first, uint64_t(uint32_t(rows)) * uint32_t(cols_) * 2u)), cols(cols_),
+          row8(uint32_t(cols_) * 16u), wave(wave_) {
+        u0 = uint32_t(lane & 7) ^ uint32_t(lane >> 4);  // (row / 2) % 8 of an even copy: l / 16
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            off[e] = (uint32_t(lane >> 3) + 8u * (wave * COPIES + e)) * cols * 2u + unit(e) * 16u;
+    }
+    __device__ __forceinline__ uint32_t unit(int e) const { return u0 ^ (e ? 4u : 0u); }
+    // Where a stage's even and odd copies read, and their first target.
+    struct Stage {
+        uint32_t off[2], lds;
+    };
+    __device__ __forceinline__ Stage stage(int st, const uint8_t* buf) const {
+        Stage s;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            s.off[e] = uint32_t(st) * 64u + 8u * unit(e) < cols ? off[e] + uint32_t(st) * 128u : kNowhere;
+        s.lds = lds_address(buf) + wave * COPIES * 1024u;
+        return s;
+    }
+    __device__ __forceinline__ void copy(const Stage& s, int i) const {
+        copy_to_lds<16>(src, s.off[i & 1] + uint32_t(i >> 1) * 2u * row8, s.lds + uint32_t(i) * 1024u);
+    }
+    __device__ __forceinline__ void copy(const Stage& s, int i0, int i1) const {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) copy(s, i);
+    }
+};
+
 // V fp16 values at p as floats, and back with one rounding each.  V > 1 needs
 // p aligned to 2 V bytes.
 template <int V>
@@ -141,6 +268,58 @@ __device__ __forceinline__ void finish(const Epilogue& e, int row, int col, floa
 
 namespace wqh {
 
+// Time of a tile kernel's block, in us on MI355X: `idle` + `load` * (share of
+// the compute units that work) per 64-deep stage, plus `fixed` per tile (the
+// clock falls as more units feed their matrix cores).  `overlap`: two blocks
+// share a unit, so that rounds need not be whole.
+struct TileCost {
+    int BM;
+    double idle, load, fixed;
+    bool overlap;
+};
+struct TilePlan {
+    int BM = 128, splits = 1, sps = 0;
+};
+
+// Tile height and split of the summed dimension with the least modelled time:
+// blocks run in rounds of one per unit; a split writes and re-reads fp32
+// partial sums of M x cols and launches a second kernel.  Ranges are multiples
+// of `align` stages, at least four.  The costs are fitted to 1458 timings of
+// the two tile kernels (M = 33 .. 2048, five layers from 1024 x 2048 to
+// 28672 x 8192, all heights and 1 .. 32 ranges), over which the plan's choice
+// is within 2 % of the best on average and 20 % at worst.
+inline TilePlan plan_tiles(int M, int n_tiles, int stages, int cols, const TileCost (&costs)[3], int align,
+                           size_t part_bytes, int units) {
+    TilePlan best;
+    best.sps = stages;
+    double best_us = 1e300;
+    for (const TileCost& c : costs) {
+        for (int S = 1; S <= 32; ++S) {
+            const int sps = ((stages + S - 1) / S + align - 1) / align * align;
+            if ((stages + sps - 1) / sps != S) continue;
+            const double bytes = double(S) * M * cols * 4.0;
+            if (S > 1 && (sps < 4 || bytes > double(part_bytes))) continue;
+            const double blocks = double((M + c.BM - 1) / c.BM) * n_tiles * S;
+            auto round_us = [&](double share) { return sps * (c.idle + c.load * share) + c.fixed; };
+            double us;
+            if (blocks <= units)
+                us = round_us(blocks / units);
+            else if (c.overlap)
+                us = round_us(1.0) * (blocks / units);
+            else {
+                const double whole = double((long long)(blocks / units)), rest = blocks / units - whole;
+                us = whole * round_us(1.0) + (rest > 0 ? round_us(rest) : 0.0);
+            }
+            if (S > 1) us += 2.1 + 2.0 * bytes / 5.1e6;
+            if (us < best_us) {
+                best_us = us;
+                best = TilePlan{c.BM, S, sps};
+            }
+        }
+    }
+    return best;
+}
+
 // One forward product of the block: x [M][K] in packed channel order, `rows`
 // weight rows (gated: 2 * e.out).
 struct BlockFwd {
@@ -154,12 +333,12 @@ struct BlockFwd {
 };
 
 // Bytes of fp32 partial sums the product would like.
-size_t block_fwd_part_bytes(int M, int rows, int K, int bits, bool gated);
+size_t block_fwd_part_bytes(int M, int rows, int K, bool gated);
 wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
 // Small M (decode batches).
 constexpr int kBlockSmallM = 32;
-size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated);
+size_t block_small_part_bytes(int M, int rows, int K, bool gated);
 wq_status block_small(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
 // e applied to the sum over `splits` partial products [splits][M][rows].

@@ -1,28 +1,37 @@
 // The block's forward products for more rows than a decode batch:
 // epilogue(x . W^T) on 32x32x16 fp16 matrix-core instructions.
 //
-// A 256-thread block owns BM x 256 weight rows' worth of products; its four
-// wavefronts sit side by side along the weight rows, BM x 64 each, so that
-// every weight is decoded by one wavefront only, and the vector work of
+// A 256-thread block owns BM activation rows x 256 weight rows of products;
+// its four wavefronts sit side by side along the weight rows, BM x 64 each, so
+// that every weight is decoded by one wavefront only, and the vector work of
 // decoding is spread over BM / 32 matrix instructions per fragment.  K
 // advances in stages of 64.
 //
 //  - Weights: lane l supplies 8 consecutive channels (half l / 32 of the
-//    stage's 64) of one weight row, which is one packed 8-code block.  A lane
-//    loads its own 32-code chunk, scale and zero-point per stage and column
-//    block one stage ahead and dequantizes in registers straight into the B
-//    operand: decoded weights touch neither LDS nor memory.
+//    stage's 64) of one weight row, which is one packed 8-code block.  The
+//    packed codes pass through LDS in windows of GS stages (64 bytes of a
+//    row, 48 at 3 bits), copied with four lanes to a row, scales and
+//    zero-points in windows of their own: lanes that load their own chunk,
+//    scale and zero-point per stage straight from memory fetch a whole line
+//    for each of them every time.  A lane reads its 32-code chunk, scale and
+//    zero-point from LDS once per stage and dequantizes in registers straight
+//    into the B operand.
 //  - The lane's two weight rows are neighbours (2c, 2c + 1) in the linear
 //    layer, and gate row o with up row o + I in the gated block: both
 //    factors of an output then sit in the same lane's accumulators.
-//  - Activations: the BM x 64 tile goes through registers into one of two
-//    LDS buffers, a stage ahead; 16-byte unit u of row r at u ^ (r mod 8), so
-//    the eight rows that a fragment read takes at a time fall on all banks.
-//  - Epilogue: accumulators cross LDS (the activation buffers, free by then)
-//    in passes of 32 or 64 rows, so that bias, activation, product, residual
-//    and every store work on 8 neighbouring columns (16-byte accesses).
+//  - Activations: three LDS buffers of BM x 64; stage s + 2 is on its way
+//    while stage s is multiplied.
+//  - All of it is copied from memory straight into LDS, and each stage ends
+//    with one wait that leaves the newest stage's copies in flight.  (With
+//    loads through registers the same loop took 553 us at 4096 x 8192 x 8192,
+//    4 bits; 428 us with its loads taken out and 374 us with nothing but its
+//    matrix instructions: the loads' latency was the loss.)
+//  - Epilogue: accumulators cross LDS in passes of 64 rows, so that bias,
+//    activation, product, residual and every store work on 8 neighbouring
+//    columns (16-byte accesses).
 //  - Tiles are dealt to the XCDs in contiguous ranges (tile_coords).
 #include <algorithm>
+#include <type_traits>
 
 #include "wq_block_common.h"
 
@@ -30,92 +39,108 @@ namespace {
 
 using namespace wq;
 
+// Vector instructions issued after each matrix instruction.
+#ifndef WQ_BLOCK_FWD_VALU
+#define WQ_BLOCK_FWD_VALU 4
+#endif
+
 struct FwdArgs {
     const uint16_t* x;
     const uint32_t* packed;
     const uint16_t* scales;
     const uint8_t* zeros;
-    float* part;
+    float* part;  // fp32 sums of a K split, or null
     int M, rows, K;
     GroupDiv gd;
     int m_tiles, n_tiles, tiles, sps;
+    int gated;
     Epilogue e;
 };
 
-template <int BITS, bool HAS_Z, int BM, bool GATED, bool PART>
-__global__ void __launch_bounds__(256, BM == 256 ? 1 : 2) block_fwd_kernel(const FwdArgs p) {
-    constexpr int BN = 256, BK = 64, TM = BM / 32, TN = 2;
-    constexpr int OC = GATED ? BN / 2 : BN;  // output columns of the tile
-    constexpr int ROW = BK * 2;              // bytes of an activation row in LDS
-    constexpr int AU = BM * 8 / 256;         // 16-byte units per thread and stage
-    constexpr int PASS = BM == 256 ? 64 : 32;
-    constexpr int LDS = 2 * BM * ROW > PASS * BN * 4 ? 2 * BM * ROW : PASS * BN * 4;
-    __shared__ __attribute__((aligned(128))) uint8_t lds[LDS];
+// Shape of the tile kernel's shared memory.
+template <int BITS, bool FAST, int BM>
+struct FwdShape {
+    static constexpr int BK = 64;
+    static constexpr int GS = BITS == 8 ? 1 : BITS == 2 ? 4 : 2;  // stages of a weight window
+    static constexpr int UNIT = BITS == 3 ? 12 : 16;              // bytes a lane copies (16 apart in LDS)
+    static constexpr int SG = FAST ? 4 : 2;                       // stages of a window of scales
+    static constexpr int NS = FAST ? 2 : 4;                       // scales of a row in it
+    static constexpr int A_BYTES = BM * BK * 2;
+    static constexpr int W_BYTES = 256 * 4 * 16;
+    static constexpr int S_BYTES = NS * 2 * 256 * 4;
+    static constexpr int PASS = 64;                               // rows of an epilogue pass
+    static constexpr int MAIN = 3 * A_BYTES + 2 * (W_BYTES + S_BYTES);
+    static constexpr int LDS = MAIN > PASS * 256 * 4 ? MAIN : PASS * 256 * 4;
+};
+
+// FAST: the group size is a multiple of 128 (or all of K, itself a multiple),
+// so two stages share a scale and zero-point.
+template <int BITS, bool FAST, int BM>
+__global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
+    using Sh = FwdShape<BITS, FAST, BM>;
+    constexpr int BN = 256, BK = Sh::BK, TM = BM / 32, TN = 2;
+    constexpr int GS = Sh::GS, SG = Sh::SG, NS = Sh::NS, UNIT = Sh::UNIT;
+    constexpr int ROW = BK * 2;  // bytes of an activation row in LDS
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[Sh::LDS];
+    uint8_t* const lds_a = lds;                       // [3][BM][64]
+    uint8_t* const lds_w = lds_a + 3 * Sh::A_BYTES;   // [2][256 rows][4 units]
+    uint8_t* const lds_s = lds_w + 2 * Sh::W_BYTES;   // [2][NS][scale, zero-point][256 rows]
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 31, hh = lane >> 5;
+    const bool gated = p.gated != 0;
+    const int oc_tile = gated ? BN / 2 : BN;  // output columns of the tile
     int m_t, n_t;
     tile_coords<4>(blockIdx.x, p.tiles, p.m_tiles, p.n_tiles, m_t, n_t);
-    const int m0 = m_t * BM, o0 = n_t * OC;
+    const int m0 = m_t * BM, o0 = n_t * oc_tile;
     const int chunks = p.K / 32;
     const int G = chunk_group(chunks - 1, p.gd) + 1;
     const int stages = (p.K + BK - 1) / BK;
-    const int st_begin = int(blockIdx.y) * p.sps;
+    const int st_begin = int(blockIdx.y) * p.sps;  // a multiple of 4
     const int st_end = min(st_begin + p.sps, stages);
 
-    // ---- activations: thread t copies unit t % 8 of rows t / 8 + 32 i (rows
-    // past M read the last one; their outputs are not stored)
-    const int au = tid & 7, ar = tid >> 3;
-    uint32_t a_off[AU];
-#pragma unroll
-    for (int i = 0; i < AU; ++i) a_off[i] = uint32_t(min(m0 + ar + 32 * i, p.M - 1) - m0) * uint32_t(p.K) * 2u;
-    const char* xbase = reinterpret_cast<const char*>(p.x + size_t(m0) * p.K);
-    u4 av[AU];
-    auto load_a = [&](int st) {
-        const uint32_t k = min(uint32_t(st * BK + 8 * au), uint32_t(p.K - 8)) * 2u;
-#pragma unroll
-        for (int i = 0; i < AU; ++i) av[i] = *reinterpret_cast<const u4*>(xbase + (a_off[i] + k));
-    };
-    auto store_a = [&](int st, uint8_t* buf) {
-        if (st * BK + 8 * au >= p.K) {  // only in a last stage that K ends in
-#pragma unroll
-            for (int i = 0; i < AU; ++i) av[i] = u4{0u, 0u, 0u, 0u};
-        }
-#pragma unroll
-        for (int i = 0; i < AU; ++i)
-            *reinterpret_cast<u4*>(buf + (ar + 32 * i) * ROW + ((au ^ (ar & 7)) * 16)) = av[i];
-    };
+    const TileCopy<BM> xcopy(p.x + size_t(m0) * p.K, p.M - m0, p.K, wave, lane);
 
-    // ---- weights
-    const uint32_t* wrow[TN];
-    const uint16_t* srow[TN];
-    const uint8_t* zrow[TN];
+    // ---- weights.  LDS row r = 128 j + 32 w + c is what lane c of wavefront w
+    // multiplies as its j-th row: gate (j = 0) or up row o0 + 32 w + c, or row
+    // o0 + 64 w + 2 c + j.  Wavefront k copies LDS rows 64 k .. 64 k + 63, all
+    // of one j, from the matrix row `first` on (rows past the matrix become
+    // zeros or other rows; their outputs are not stored).
+    const int kj = wave >> 1, kh = wave & 1;
+    const int first = o0 + (gated ? kj * p.e.out : kj);
+    const uint32_t row_bytes = uint32_t(chunks) * BITS * 4u;
+    const int rows_left = p.rows - first;  // may be <= 0
+    auto left = [&](uint64_t per_row) { return rows_left > 0 ? uint64_t(rows_left) * per_row : 0; };
+    const u4 wsrc = copy_source(reinterpret_cast<const char*>(p.packed) + size_t(first) * row_bytes, left(row_bytes));
+    // Part cp = 0 .. 3 of a window: LDS rows 64 k + 16 cp + l / 4, lane l the
+    // row's position l % 4, which holds unit (l % 4) ^ ((row / 4) % 4): 16
+    // consecutive rows read at one unit fall on all banks.
+    const uint32_t wstep = (gated ? 16u : 32u) * row_bytes;
+    const uint32_t wunit = uint32_t(lane & 3) ^ uint32_t(lane >> 4);
+    const uint32_t woff = (gated ? 64u * kh + uint32_t(lane >> 2) : 128u * kh + 2u * uint32_t(lane >> 2)) * row_bytes +
+                          wunit * UNIT;
+    // Parts GS-th by GS-th in one sequence over the stages: the Q-th belongs
+    // to window Q / GS.
+    constexpr int WP = 4 / GS;  // parts a stage copies
+    auto copy_w = [&](int Q) {
+        const uint32_t off = woff + uint32_t(Q / GS) * (4u * UNIT);
+        const uint32_t cp0 = uint32_t(Q & (GS - 1)) * WP;
+        const uint32_t dst = lds_address(lds_w + ((Q / GS) & 1) * Sh::W_BYTES) + (64u * wave + 16u * cp0) * 64u;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        size_t n;
-        if constexpr (GATED)
-            n = size_t(min(o0 + wave * 32 + c, p.e.out - 1)) + size_t(j) * p.e.out;
-        else
-            n = size_t(min(o0 + wave * 64 + 2 * c + j, p.rows - 1));
-        wrow[j] = p.packed + n * chunks * BITS;
-        srow[j] = p.scales + n * G;
-        zrow[j] = HAS_Z ? p.zeros + n * G : nullptr;
-    }
-    struct BRegs {
-        uint32_t w[TN][BITS], s[TN], z[TN];
+        for (int e = 0; e < WP; ++e) copy_to_lds<UNIT>(wsrc, off + (cp0 + e) * wstep, dst + e * 1024u);
     };
-    auto load_b = [&](BRegs& b, int st) {
-        const int cg = min(2 * st + hh, chunks - 1);  // past K: x is zero there
-        const int g = chunk_group(cg, p.gd);
+    // Scales and zero-points: thread t copies LDS row t's.
+    const u4 ssrc = copy_source(p.scales + size_t(first) * G, left(uint64_t(G) * 2));
+    const u4 zsrc = copy_source(p.zeros ? p.zeros + size_t(first) * G : nullptr, p.zeros ? left(G) : 0);
+    const uint32_t soff = (gated ? 64u * kh + uint32_t(lane) : 128u * kh + 64u * uint32_t(lane >> 5) + 2u * c) * uint32_t(G);
+    auto copy_s = [&](int g) {
+        const uint32_t dst = lds_address(lds_s + (g & 1) * Sh::S_BYTES) + 256u * wave;
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            load_chunk_b<BITS>(wrow[j] + cg * BITS, b.w[j]);
-            b.s[j] = srow[j][g];
-            if constexpr (HAS_Z)
-                b.z[j] = zrow[j][g];
-            else
-                b.z[j] = 1u << (BITS - 1);
+        for (int q = 0; q < NS; ++q) {
+            const uint32_t at = soff + uint32_t(chunk_group(min((g * SG * 2) + q * (SG * 2 / NS), chunks - 1), p.gd));
+            copy_to_lds<2>(ssrc, at * 2u, dst + q * 2048u);
+            copy_to_lds<1>(zsrc, at, dst + q * 2048u + 1024u);
         }
     };
 
@@ -127,113 +152,203 @@ __global__ void __launch_bounds__(256, BM == 256 ? 1 : 2) block_fwd_kernel(const
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
+    // The k-steps of a stage are software-pipelined: while k-step t's matrix
+    // instructions run, the A fragments of t + 1 are read and its B fragments
+    // decoded.  The stage's barrier sits before its last k-step, whose
+    // instructions then cover the first reads of the next stage's buffers.
     const uint32_t a_lane = uint32_t(c) * ROW;
-    BRegs cur, nxt;
-    load_a(st_begin);
-    load_b(cur, st_begin);
-    store_a(st_begin, lds);
-    load_a(min(st_begin + 1, st_end - 1));
-    __syncthreads();
-    for (int st = st_begin; st < st_end; ++st) {
-        const int par = (st - st_begin) & 1;
-        const uint8_t* buf = lds + par * (BM * ROW);
-        load_b(nxt, min(st + 1, st_end - 1));
-        store_a(min(st + 1, st_end - 1), lds + (par ^ 1) * (BM * ROW));
-        load_a(min(st + 2, st_end - 1));
-        uint32_t zz[TN], ss[TN];
+    const uint32_t w_lane = uint32_t(wave) * 32u + uint32_t(c);  // LDS row of j = 0
+    h8 af[2][TM], bf[2][TN];
+    uint32_t wc[TN][BITS], zz[TN], ss[TN];  // the stage's chunk of each row
+    auto read_w = [&](int st) {
+        const uint32_t i = uint32_t(st) & (GS - 1);
+        const uint8_t* win = lds_w + ((st / GS) & 1) * Sh::W_BYTES;
+        const uint32_t q = FAST ? uint32_t(st >> 1) & 1u : 2u * (uint32_t(st) & 1u) + hh;
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(lds_s + ((st / SG) & 1) * Sh::S_BYTES) + q * 512u;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            zz[j] = zero_pair_nat<BITS>(cur.z[j]);
-            ss[j] = scale_pair(uint16_t(cur.s[j]));
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            h8 af[TM], bf[TN];
-            const uint8_t* ap = buf + a_lane + ((uint32_t(4 * hh + t) ^ uint32_t(c & 7)) * 16u);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) af[i] = *reinterpret_cast<const h8*>(ap + i * 32 * ROW);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                uint32_t hq[4], v[4];
-                decode_nat<BITS>(cur.w[j], t, hq);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = as_u32(dequant_pair(hq[i], zz[j], ss[j]));
-                bf[j] = __builtin_bit_cast(h8, (u4{v[0], v[1], v[2], v[3]}));
+            const uint32_t r = w_lane + 128u * j, sw = (r >> 2) & 3u;
+            const uint8_t* row = win + r * 64u;
+            if constexpr (BITS == 4) {
+                const u4 v = *reinterpret_cast<const u4*>(row + ((2u * i + hh) ^ sw) * 16u);
+                wc[j][0] = v.x; wc[j][1] = v.y; wc[j][2] = v.z; wc[j][3] = v.w;
+            } else if constexpr (BITS == 8) {
+                const u4 a = *reinterpret_cast<const u4*>(row + ((2u * hh) ^ sw) * 16u);
+                const u4 b = *reinterpret_cast<const u4*>(row + ((2u * hh + 1u) ^ sw) * 16u);
+                wc[j][0] = a.x; wc[j][1] = a.y; wc[j][2] = a.z; wc[j][3] = a.w;
+                wc[j][4] = b.x; wc[j][5] = b.y; wc[j][6] = b.z; wc[j][7] = b.w;
+            } else if constexpr (BITS == 2) {
+                typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+                const u2 v = *reinterpret_cast<const u2*>(row + (i ^ sw) * 16u + hh * 8u);
+                wc[j][0] = v.x; wc[j][1] = v.y;
+            } else {
+                const u4 v = *reinterpret_cast<const u4*>(row + ((2u * i + hh) ^ sw) * 16u);
+                wc[j][0] = v.x; wc[j][1] = v.y; wc[j][2] = v.z;
             }
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
+            ss[j] = s[r];
+            zz[j] = s[256u + r];
         }
-        cur = nxt;
-        __syncthreads();
-    }
-
-    // ---- acc[i][j][r]: row 32 i + 8 (r / 4) + 4 hh + r % 4, the lane's j-th
-    // weight row
-    if constexpr (PART) {
-        float* pr = p.part + size_t(blockIdx.y) * p.M * p.rows;
+    };
+    auto group_pairs = [&]() {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            ss[j] = __builtin_amdgcn_perm(ss[j], ss[j], 0x01000100u);
+            zz[j] = zero_pair_nat<BITS>(p.zeros ? zz[j] : 1u << (BITS - 1));
+        }
+    };
+    auto read_a = [&](const uint8_t* buf, int t, h8 (&f)[TM]) {
+        const uint8_t* ap = buf + a_lane + ((uint32_t(4 * hh + t) ^ uint32_t((c >> 1) & 7)) * 16u);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) f[i] = *reinterpret_cast<const h8*>(ap + i * 32 * ROW);
+    };
+    auto make_b = [&](int t, h8 (&f)[TN]) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            uint32_t hq[4], v[4];
+            decode_nat<BITS>(wc[j], t, hq);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = as_u32(dequant_pair(hq[q], zz[j], ss[j]));
+            f[j] = __builtin_bit_cast(h8, (u4{v[0], v[1], v[2], v[3]}));
+        }
+    };
+    auto multiply = [&](const h8 (&a)[TM], const h8 (&b)[TN]) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = m0 + 32 * i + 8 * (r >> 2) + 4 * hh + (r & 3);
-                const int col = GATED ? o0 + wave * 32 + c : o0 + wave * 64 + 2 * c;
-                if (row < p.M) {
-                    float* dst = pr + size_t(row) * p.rows;
-                    if constexpr (GATED) {
-                        if (col < p.e.out) {
-                            dst[col] = acc[i][0][r];
-                            dst[p.e.out + col] = acc[i][1][r];
-                        }
-                    } else {
-                        if (col < p.rows) dst[col] = acc[i][0][r];
-                        if (col + 1 < p.rows) dst[col + 1] = acc[i][1][r];
-                    }
-                }
-            }
-    } else {
-        float* tile = reinterpret_cast<float*>(lds);  // [PASS][BN]
-        const bool wide = p.e.out % 8 == 0;
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i], b[j], acc[i][j], 0, 0, 0);
+    };
+    constexpr int NM = TM * TN, NV = WQ_BLOCK_FWD_VALU;
+    constexpr int C = TileCopy<BM>::COPIES;
+    auto abuf = [&](int k) { return lds_a + k * Sh::A_BYTES; };
+
+    // ---- the first windows, two stages of x.  Scales' window g + 1 is copied
+    // in window g's first stage, the weights' parts one by one.
+    copy_s(st_begin / SG);
 #pragma unroll
-        for (int ps = 0; ps < BM / PASS; ++ps) {
-            if (ps) __syncthreads();
+    for (int q = 0; q <= GS; ++q) copy_w(st_begin + q);
+    xcopy.copy(xcopy.stage(st_begin, abuf(0)), 0, C);
+    xcopy.copy(xcopy.stage(st_begin + 1, abuf(1)), 0, C);
+    copies_landed<C>();
+    __syncthreads();
+    read_w(st_begin);
+    read_a(abuf(0), 0, af[0]);
+    group_pairs();
+    make_b(0, bf[0]);
+    int b0 = 0, b1 = 1, b2 = 2;  // buffers of stages st, st + 1, st + 2
+    for (int st = st_begin; st < st_end; ++st) {
+        // stage st + 2's copies (past K: zeros) into the buffer that every
+        // wavefront has left by the last barrier
+        const auto next = xcopy.stage(st + 2, abuf(b2));
+        const uint8_t* buf = abuf(b0);
+        read_a(buf, 1, af[1]);
+        make_b(1, bf[1]);
+        xcopy.copy(next, 0, (C + 2) / 3);
+        multiply(af[0], bf[0]);
+        sched_step<NM, TM, 0, 0, NV>();
+        read_a(buf, 2, af[0]);
+        make_b(2, bf[0]);
+        xcopy.copy(next, (C + 2) / 3, (2 * C + 2) / 3);
+        multiply(af[1], bf[1]);
+        sched_step<NM, TM, 0, 0, NV>();
+        read_a(buf, 3, af[1]);
+        make_b(3, bf[1]);
+        xcopy.copy(next, (2 * C + 2) / 3, C);
+        multiply(af[0], bf[0]);
+        sched_step<NM, TM, 0, 0, NV>();
+        copies_landed<C>();  // all but stage st + 2's
+        __syncthreads();
+        read_w(st + 1);
+        read_a(abuf(b1), 0, af[0]);
+        copy_w(st + 1 + GS);  // into a part whose window's last reads lie before this barrier
+        group_pairs();
+        make_b(0, bf[0]);
+        multiply(af[1], bf[1]);
+        sched_step<NM, TM + 2 * TN, 0, 0, NV>();
+        if ((st & (SG - 1)) == 0) copy_s(st / SG + 1);
+        const int t = b0;
+        b0 = b1;
+        b1 = b2;
+        b2 = t;
+    }
+    copies_landed<0>();  // none may still be writing when LDS is reused or the block ends
+    __syncthreads();
+
+    // ---- acc[i][j][r]: row 32 i + 8 (r / 4) + 4 hh + r % 4, the lane's j-th
+    // weight row
+    if (p.part) {
+        float* pr = p.part + size_t(blockIdx.y) * p.M * p.rows;
+        const int col = gated ? o0 + wave * 32 + c : o0 + wave * 64 + 2 * c;
+        const int lim = gated ? p.e.out : p.rows;
+        auto put = [&](auto jc, int at) {
 #pragma unroll
-            for (int ii = 0; ii < PASS / 32; ++ii) {
-                const int i = ps * (PASS / 32) + ii;
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    float* dst = tile + (32 * ii + 8 * (r >> 2) + 4 * hh + (r & 3)) * BN;
-                    if constexpr (GATED) {
-                        dst[wave * 32 + c] = acc[i][0][r];
-                        dst[OC + wave * 32 + c] = acc[i][1][r];
-                    } else {
-                        *reinterpret_cast<float2*>(dst + wave * 64 + 2 * c) = float2{acc[i][0][r], acc[i][1][r]};
-                    }
+                    const int row = m0 + 32 * i + 8 * (r >> 2) + 4 * hh + (r & 3);
+                    if (row < p.M) pr[size_t(row) * p.rows + at] = acc[i][decltype(jc)::value][r];
                 }
+        };
+        if (col < lim) put(std::integral_constant<int, 0>{}, col);
+        if (gated ? col < lim : col + 1 < lim) put(std::integral_constant<int, 1>{}, gated ? p.e.out + col : col + 1);
+        return;
+    }
+    // LDS tile: the wavefront's first rows' products in columns 32 w + c, the
+    // second rows' in 128 + 32 w + c
+    float* tile = reinterpret_cast<float*>(lds);  // [PASS][BN]
+    const bool wide = p.e.out % 8 == 0;
+    const int per_row = oc_tile / 8;
+#pragma unroll
+    for (int ps = 0; ps < BM / Sh::PASS; ++ps) {
+        if (ps) __syncthreads();
+#pragma unroll
+        for (int ii = 0; ii < Sh::PASS / 32; ++ii) {
+            const int i = ps * (Sh::PASS / 32) + ii;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float* dst = tile + (32 * ii + 8 * (r >> 2) + 4 * hh + (r & 3)) * BN + wave * 32 + c;
+                dst[0] = acc[i][0][r];
+                dst[128] = acc[i][1][r];
             }
-            __syncthreads();
-            constexpr int PER_ROW = OC / 8;
+        }
+        __syncthreads();
 #pragma unroll 1
-            for (int q = tid; q < PASS * PER_ROW; q += 256) {
-                const int rr = q / PER_ROW, oc = (q % PER_ROW) * 8;
-                const int row = m0 + ps * PASS + rr, col = o0 + oc;
-                if (row >= p.M || col >= p.e.out) continue;
+        for (int q = tid; q < Sh::PASS * per_row; q += 256) {
+            const int rr = q / per_row, oc = (q % per_row) * 8;
+            const int row = m0 + ps * Sh::PASS + rr, col = o0 + oc;
+            if (row >= p.M || col >= p.e.out) continue;
+            if (gated) {
                 const float* src = tile + rr * BN + oc;
                 float a[8], u[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     a[i] = src[i];
-                    u[i] = GATED ? src[OC + i] : 0.f;
+                    u[i] = src[128 + i];
                 }
                 if (wide) {
-                    finish<GATED, 8>(p.e, row, col, a, u);
+                    finish<true, 8>(p.e, row, col, a, u);
                 } else {
 #pragma unroll 1
                     for (int i = 0; i < 8 && col + i < p.e.out; ++i) {
-                        float a1[1] = {src[i]}, u1[1] = {GATED ? src[OC + i] : 0.f};
-                        finish<GATED, 1>(p.e, row, col + i, a1, u1);
+                        float a1[1] = {src[i]}, u1[1] = {src[128 + i]};
+                        finish<true, 1>(p.e, row, col + i, a1, u1);
+                    }
+                }
+            } else {  // column 2 c + j of a wavefront's 64
+                const float* src = tile + rr * BN + oc / 2;
+                float a[8], u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a[i] = src[128 * (i & 1) + (i >> 1)];
+                    u[i] = 0.f;
+                }
+                if (wide) {
+                    finish<false, 8>(p.e, row, col, a, u);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < 8 && col + i < p.e.out; ++i) {
+                        float a1[1] = {src[128 * (i & 1) + (i >> 1)]}, u1[1] = {0.f};
+                        finish<false, 1>(p.e, row, col + i, a1, u1);
                     }
                 }
             }
@@ -270,104 +385,57 @@ __global__ void __launch_bounds__(256) block_finish_kernel(const Epilogue e, con
     }
 }
 
-struct FwdPlan {
-    int BM = 128, splits = 1, sps = 0;
-};
+constexpr wqh::TileCost kFwdCosts[3] = {
+    {64, 0.65, 0.27, 9.7, true}, {128, 0.59, 0.69, 10.1, false}, {256, 1.20, 0.33, 18.7, false}};
 
-// Tile height and K split by a time model: a tile takes a fixed time per
-// 64-deep stage (the larger of its matrix instructions and its weight
-// stream), tiles run in rounds of the resident blocks, a split writes and
-// re-reads fp32 partial sums.
-FwdPlan fwd_plan(int M, int rows, int K, int bits, bool gated, size_t part_bytes) {
-    const int cus = wqh::gemm_slots(1);
-    const int stages = (K + 63) / 64;
+wqh::TilePlan fwd_plan(int M, int rows, int K, bool gated, size_t part_bytes) {
     const int n_tiles = gated ? (rows / 2 + 127) / 128 : (rows + 255) / 256;
-    FwdPlan best;
-    best.sps = stages;
-    double best_us = 1e30;
-    const int heights[3] = {64, 128, 256};
-    for (int h = 0; h < 3; ++h) {
-        const int BM = heights[h];
-        const double stage_us = BM == 64 ? 0.45 : BM == 128 ? 0.75 : 1.2;
-        const int slots = cus * (BM == 256 ? 1 : 2);
-        const double share = BM == 256 ? 1.0 : 2.0;  // resident blocks share the unit
-        const long long tiles = (long long)((M + BM - 1) / BM) * n_tiles;
-        for (int S = 1; S <= 32; ++S) {
-            const int sps = (stages + S - 1) / S;
-            const int Se = (stages + sps - 1) / sps;
-            if (Se != S) continue;
-            if (S > 1 && (sps < 4 || double(Se) * M * rows * 4.0 > double(part_bytes))) break;
-            const long long blocks = tiles * Se;
-            const double rounds = double((blocks + slots - 1) / slots);
-            const double fill = blocks < cus ? 1.0 : share;  // one block per unit runs alone
-            double us = rounds * sps * stage_us * (blocks <= cus ? 0.6 : 1.0) * fill / share;
-            if (blocks <= cus) us = sps * stage_us * 0.6;
-            us += 3.0;
-            if (S > 1) us += 2.0 + double(Se) * M * rows * 8.0 / 4e6;
-            if (us < best_us * 0.98) {
-                best_us = us;
-                best.BM = BM;
-                best.splits = Se;
-                best.sps = sps;
-            }
-        }
-    }
-    (void)bits;
-    return best;
+    // ranges of whole windows of weights and scales (four stages)
+    return wqh::plan_tiles(M, n_tiles, (K + 63) / 64, rows, kFwdCosts, 4, part_bytes, wqh::gemm_slots(1));
 }
 
-template <int BITS, bool HAS_Z, int BM>
-void launch_fwd(const wqh::BlockFwd& f, const FwdPlan& pl, const FwdArgs& a, hipStream_t s) {
-    const dim3 grid(a.tiles, pl.splits), block(256);
-    if (f.gated) {
-        if (pl.splits > 1)
-            hipLaunchKernelGGL((block_fwd_kernel<BITS, HAS_Z, BM, true, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((block_fwd_kernel<BITS, HAS_Z, BM, true, false>), grid, block, 0, s, a);
-    } else {
-        if (pl.splits > 1)
-            hipLaunchKernelGGL((block_fwd_kernel<BITS, HAS_Z, BM, false, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((block_fwd_kernel<BITS, HAS_Z, BM, false, false>), grid, block, 0, s, a);
-    }
+template <int BITS, bool FAST, int BM>
+wq_status launch_fwd(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((block_fwd_kernel<BITS, FAST, BM>), dim3(a.tiles, pl.splits), dim3(256), 0, s, a);
+    return wqh::launch_status();
 }
 
-template <int BITS, bool HAS_Z>
-void launch_fwd_bm(const wqh::BlockFwd& f, const FwdPlan& pl, const FwdArgs& a, hipStream_t s) {
+template <int BITS, bool FAST>
+wq_status launch_fwd_bm(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
     switch (pl.BM) {
-        case 64: launch_fwd<BITS, HAS_Z, 64>(f, pl, a, s); break;
-        case 128: launch_fwd<BITS, HAS_Z, 128>(f, pl, a, s); break;
-        default: launch_fwd<BITS, HAS_Z, 256>(f, pl, a, s); break;
+        case 64: return launch_fwd<BITS, FAST, 64>(pl, a, s);
+        case 128: return launch_fwd<BITS, FAST, 128>(pl, a, s);
+        default: return launch_fwd<BITS, FAST, 256>(pl, a, s);
     }
 }
 
 template <int BITS>
-void launch_fwd_bits(const wqh::BlockFwd& f, const FwdPlan& pl, const FwdArgs& a, hipStream_t s) {
-    f.zeros ? launch_fwd_bm<BITS, true>(f, pl, a, s) : launch_fwd_bm<BITS, false>(f, pl, a, s);
+wq_status launch_fwd_bits(int gs, const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
+    return gs % 128 == 0 ? launch_fwd_bm<BITS, true>(pl, a, s) : launch_fwd_bm<BITS, false>(pl, a, s);
 }
 
 }  // namespace
 
 namespace wqh {
 
-size_t block_fwd_part_bytes(int M, int rows, int K, int bits, bool gated) {
-    const FwdPlan p = fwd_plan(M, rows, K, bits, gated, ~size_t(0) >> 1);
+size_t block_fwd_part_bytes(int M, int rows, int K, bool gated) {
+    const TilePlan p = fwd_plan(M, rows, K, gated, ~size_t(0));
     return p.splits > 1 ? size_t(p.splits) * M * rows * 4 : 0;
 }
 
 wq_status block_fwd(const BlockFwd& f, float* part, size_t part_bytes, hipStream_t s) {
-    const FwdPlan pl = fwd_plan(f.M, f.rows, f.K, f.bits, f.gated, part ? part_bytes : 0);
+    const TilePlan pl = fwd_plan(f.M, f.rows, f.K, f.gated, part ? part_bytes : 0);
     const int oc = f.gated ? 128 : 256;
     const int m_tiles = (f.M + pl.BM - 1) / pl.BM, n_tiles = (f.e.out + oc - 1) / oc;
-    const FwdArgs a{f.x,    f.packed,           f.scales, f.zeros, part,    f.M, f.rows,
-                    f.K,    group_magic(f.gs),  m_tiles,  n_tiles, m_tiles * n_tiles, pl.sps, f.e};
+    const FwdArgs a{f.x, f.packed, f.scales, f.zeros, pl.splits > 1 ? part : nullptr, f.M, f.rows, f.K,
+                    group_magic(f.gs), m_tiles, n_tiles, m_tiles * n_tiles, pl.sps, f.gated, f.e};
+    wq_status st;
     switch (f.bits) {
-        case 2: launch_fwd_bits<2>(f, pl, a, s); break;
-        case 3: launch_fwd_bits<3>(f, pl, a, s); break;
-        case 4: launch_fwd_bits<4>(f, pl, a, s); break;
-        default: launch_fwd_bits<8>(f, pl, a, s); break;
+        case 2: st = launch_fwd_bits<2>(f.gs, pl, a, s); break;
+        case 3: st = launch_fwd_bits<3>(f.gs, pl, a, s); break;
+        case 4: st = launch_fwd_bits<4>(f.gs, pl, a, s); break;
+        default: st = launch_fwd_bits<8>(f.gs, pl, a, s); break;
     }
-    const wq_status st = launch_status();
     if (st != WQ_OK || pl.splits == 1) return st;
     return block_finish(f.e, f.gated, part, pl.splits, f.M, s);
 }

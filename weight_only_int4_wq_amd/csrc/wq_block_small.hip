@@ -253,8 +253,7 @@ void launch_small_bits(const wqh::BlockFwd& f, const SmallPlan& pl, const SmallA
 
 namespace wqh {
 
-size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated) {
-    (void)bits;
+size_t block_small_part_bytes(int M, int rows, int K, bool gated) {
     const SmallPlan p = small_plan(M, rows, K, gated, ~size_t(0) >> 1);
     return p.splits > 1 ? size_t(p.splits) * M * rows * 4 : 0;
 }
