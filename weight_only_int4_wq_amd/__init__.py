@@ -512,72 +512,110 @@ def _act(act) -> int:
     return ACTIVATIONS[act]
 
 
+def _arg(t, dtype, name, shape, device):
+    """Address of a tensor argument of exactly this type, shape and device;
+    0 for an empty one.  The checks of _dev in their cheapest order: a decode
+    call's kernel takes a few microseconds."""
+    if t.__class__ is not _torch().Tensor or t.dtype is not dtype or t.shape != shape or t.device != device \
+            or not t.is_contiguous():
+        _dev(t, dtype, name, len(shape), shape=shape, device=device)
+    return t.data_ptr()
+
+
+def _opt(t, dtype, name, shape, device):
+    return None if t is None else _arg(t, dtype, name, shape, device)
+
+
+def _first(t, name):
+    """Check a call's leading activation tensor fp16 [M][*]."""
+    torch = _torch()
+    if t.__class__ is not torch.Tensor or t.dtype is not torch.float16 or t.dim() != 2 or not t.is_contiguous():
+        _dev(t, torch.float16, name, 2)
+    return t
+
+
 def _block_call(entry, device, args, M, N, K, bits, group_size, has_perm, workspace):
     """Take or allocate the workspace and call wq_<entry> on the tensors'
     device (made current for the call) and its current stream."""
     torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensor arguments must be GPU tensors, got one on {device}")
+    handle = lib()
     if workspace is None:
-        need = block_workspace_size(entry, M, N, K, bits, has_perm)
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-    nbytes = 0 if workspace is None else workspace.numel()
-    fn = getattr(lib(), "wq_" + entry)
-
-    def call():
-        return fn(*args, M, N, K, bits, group_size, _ptr(workspace), nbytes, _stream(device))
-
-    if device.type == "cuda" and torch.cuda.current_device() != device.index:
+        need = getattr(handle, _WORKSPACE[entry])(M, N, K, bits, has_perm)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+    at, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    fn = getattr(handle, entry)
+    if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            code = call()
+            code = fn(*args, M, N, K, bits, group_size, at, nbytes, torch.cuda.current_stream(device).cuda_stream)
     else:
-        code = call()
-    _check(code, "wq_" + entry)
+        code = fn(*args, M, N, K, bits, group_size, at, nbytes, torch.cuda.current_stream(device).cuda_stream)
+    if code:
+        _check(code, entry)
+
+
+_WORKSPACE = {name: name + "_workspace_size"
+              for name in ("wq_linear_act", "wq_gated", "wq_linear_act_backward", "wq_gated_backward")}
 
 
 def _weight_args(packed, scales, zeros, perm, bits, group_size, device, gated):
-    """Check a layer's weights; returns (projection columns, K)."""
+    """Check a layer's weights; returns (weight rows, K, their addresses)."""
     torch = _torch()
-    packed = _dev(packed, torch.int32, "packed", 2, device=device)
-    scales = _dev(scales, torch.float16, "scales", 2, device=device)
-    zeros = _dev(zeros, torch.uint8, "zeros", 2, allow_none=True, device=device)
-    perm = _dev(perm, torch.int32, "perm", 1, allow_none=True, device=device)
     if bits not in (2, 3, 4, 8):
         raise ValueError("bits must be 2, 3, 4 or 8")
+    if packed.__class__ is not torch.Tensor or packed.dim() != 2:
+        _dev(packed, torch.int32, "packed", 2, device=device)
     rows, words = packed.shape
+    K = words * 32 // bits
     if words * 32 % bits:
         raise ValueError("packed must be [N][K*bits/32]")
-    K = words * 32 // bits
-    _check_meta(rows, K, bits, group_size, packed, scales, zeros, perm)
+    if group_size != -1 and (group_size <= 0 or K % group_size):
+        raise ValueError(f"group_size {group_size} does not divide K = {K}")
     if gated and rows % 2:
         raise ValueError("the stacked gate/up weight needs an even row count")
-    return (rows // 2 if gated else rows), K
+    meta = (rows, 1 if group_size == -1 else K // group_size)
+    return rows, K, (_arg(packed, torch.int32, "packed", (rows, words), device),
+                     _arg(scales, torch.float16, "scales", meta, device),
+                     _opt(zeros, torch.uint8, "zeros", meta, device), _opt(perm, torch.int32, "perm", (K,), device))
+
+
+def _workspace_arg(workspace, device):
+    return _dev(workspace, _torch().uint8, "workspace", 1, allow_none=True, device=device)
 
 
 def _forward(entry, x, packed, scales, zeros, bits, group_size, perm, bias, residual, act, save_preact, out, preact,
              workspace):
     torch = _torch()
-    act = _act(act)
-    x = _dev(x, torch.float16, "x", 2)
+    half = torch.float16
+    is_gated = entry == "wq_gated"
+    x = _first(x, "x")
     d = x.device
-    workspace = _dev(workspace, torch.uint8, "workspace", 1, allow_none=True, device=d)
-    is_gated = entry == "gated"
-    N, K = _weight_args(packed, scales, zeros, perm, bits, group_size, d, is_gated)
-    M = x.shape[0]
-    if x.shape[1] != K:
-        raise ValueError(f"x must have {K} columns, got {x.shape[1]}")
-    rows = packed.shape[0]
-    bias = _dev(bias, torch.float16, "bias", 1, allow_none=True, shape=(rows,), device=d)
-    residual = _dev(residual, torch.float16, "residual", 2, allow_none=True, shape=(M, N), device=d)
-    y = torch.empty((M, N), dtype=torch.float16, device=d) if out is None else \
-        _dev(out, torch.float16, "out", 2, shape=(M, N), device=d)
+    rows, K, weights = _weight_args(packed, scales, zeros, perm, bits, group_size, d, is_gated)
+    N = rows // 2 if is_gated else rows
+    M, cols = x.shape
+    if cols != K:
+        raise ValueError(f"x must have {K} columns, got {cols}")
+    code = _act(act)
+    if workspace is not None:
+        workspace = _workspace_arg(workspace, d)
+    bias = _opt(bias, half, "bias", (rows,), d)
+    residual = _opt(residual, half, "residual", (M, N), d)
+    if out is None:
+        out = torch.empty((M, N), dtype=half, device=d)
+        y = out.data_ptr()
+    else:
+        y = _arg(out, half, "out", (M, N), d)
+    z = None
     if preact is not None:
-        preact = _dev(preact, torch.float16, "preact", 2, shape=(M, rows), device=d)
+        z = _arg(preact, half, "preact", (M, rows), d)
     elif save_preact:
-        preact = torch.empty((M, rows), dtype=torch.float16, device=d)
-    args = [_ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm), _ptr(bias)]
-    args += ([] if is_gated else [_ptr(residual)]) + [act, _ptr(y), _ptr(preact)]
+        preact = torch.empty((M, rows), dtype=half, device=d)
+        z = preact.data_ptr()
+    args = (x.data_ptr(), *weights, bias, code, y, z) if is_gated else \
+        (x.data_ptr(), *weights, bias, residual, code, y, z)
     _block_call(entry, d, args, M, N, K, bits, group_size, perm is not None, workspace)
-    return y if preact is None else (y, preact)
+    return out if preact is None else (out, preact)
 
 
 def linear_act(x, packed, scales, zeros, bits: int, group_size: int, perm=None, bias=None, residual=None,
@@ -586,7 +624,7 @@ def linear_act(x, packed, scales, zeros, bits: int, group_size: int, perm=None, 
     `out` may be `residual` (update in place).  With save_preact (or a
     `preact` tensor to fill) returns (y, preact), preact = fp16(x . W^T + bias)
     for linear_act_backward."""
-    return _forward("linear_act", x, packed, scales, zeros, bits, group_size, perm, bias, residual, act, save_preact,
+    return _forward("wq_linear_act", x, packed, scales, zeros, bits, group_size, perm, bias, residual, act, save_preact,
                     out, preact, workspace)
 
 
@@ -596,36 +634,43 @@ def gated(x, packed, scales, zeros, bits: int, group_size: int, perm=None, bias=
     rows stacked over the up rows (2 I weight rows), one kernel for both
     projections, the activation and the product.  With save_preact returns
     (h, preact [M][2 I]) for gated_backward."""
-    return _forward("gated", x, packed, scales, zeros, bits, group_size, perm, bias, None, act, save_preact, out,
+    return _forward("wq_gated", x, packed, scales, zeros, bits, group_size, perm, bias, None, act, save_preact, out,
                     preact, workspace)
 
 
 def _backward(entry, dy, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add, need_dz, need_dbias, out,
               workspace):
     torch = _torch()
-    is_gated = entry == "gated_backward"
-    code = _act(act)
-    dy = _dev(dy, torch.float16, "dy", 2)
+    half = torch.float16
+    is_gated = entry == "wq_gated_backward"
+    dy = _first(dy, "dy")
     d = dy.device
-    workspace = _dev(workspace, torch.uint8, "workspace", 1, allow_none=True, device=d)
-    N, K = _weight_args(packed, scales, zeros, perm, bits, group_size, d, is_gated)
-    M, rows = dy.shape[0], packed.shape[0]
-    if dy.shape[1] != N:
-        raise ValueError(f"dy must have {N} columns, got {dy.shape[1]}")
+    rows, K, weights = _weight_args(packed, scales, zeros, perm, bits, group_size, d, is_gated)
+    N = rows // 2 if is_gated else rows
+    M, cols = dy.shape
+    if cols != N:
+        raise ValueError(f"dy must have {N} columns, got {cols}")
+    code = _act(act)
+    if workspace is not None:
+        workspace = _workspace_arg(workspace, d)
     needs_z = is_gated or act != "none"
-    if needs_z or preact is not None:
-        preact = _dev(preact, torch.float16, "preact", 2, shape=(M, rows), device=d)
-    dx_add = _dev(dx_add, torch.float16, "dx_add", 2, allow_none=True, shape=(M, K), device=d)
-    dx = torch.empty((M, K), dtype=torch.float16, device=d) if out is None else \
-        _dev(out, torch.float16, "out", 2, shape=(M, K), device=d)
-    dz = torch.empty((M, rows), dtype=torch.float16, device=d) if need_dz and needs_z else None
+    if needs_z and preact is None:
+        raise ValueError("preact is required")
+    z = _opt(preact, half, "preact", (M, rows), d)
+    dx_add = _opt(dx_add, half, "dx_add", (M, K), d)
+    if out is None:
+        out = torch.empty((M, K), dtype=half, device=d)
+        dx = out.data_ptr()
+    else:
+        dx = _arg(out, half, "out", (M, K), d)
+    dz = torch.empty((M, rows), dtype=half, device=d) if need_dz and needs_z else None
     dbias = torch.empty((rows,), dtype=torch.float32, device=d) if need_dbias else None
-    args = [_ptr(dy), _ptr(preact if needs_z else None), code, _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm),
-            _ptr(dx_add), _ptr(dx), _ptr(dz), _ptr(dbias)]
+    args = (dy.data_ptr(), z if needs_z else None, code, *weights, dx_add, dx,
+            None if dz is None else dz.data_ptr(), None if dbias is None else dbias.data_ptr())
     _block_call(entry, d, args, M, N, K, bits, group_size, perm is not None, workspace)
     if need_dz and not needs_z:
         dz = dy
-    return dx, dz, dbias
+    return out, dz, dbias
 
 
 def linear_act_backward(dy, preact, packed, scales, zeros, bits: int, group_size: int, perm=None, act: str = "none",
@@ -634,7 +679,7 @@ def linear_act_backward(dy, preact, packed, scales, zeros, bits: int, group_size
     dx_add, dz fp16 [M][N] = dy * act'(preact) or None, dbias fp32 [N] or
     None).  Without an activation preact may be None and dz is dy.  The
     residual's gradient is dy.  `out` may be `dx_add`."""
-    return _backward("linear_act_backward", dy, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add,
+    return _backward("wq_linear_act_backward", dy, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add,
                      need_dz, need_dbias, out, workspace)
 
 
@@ -643,7 +688,7 @@ def gated_backward(dh, preact, packed, scales, zeros, bits: int, group_size: int
     """Backward of gated for dh fp16 [M][I] and the kept preact fp16 [M][2 I]
     -> (dx fp16 [M][K], dz fp16 [M][2 I] = (dg, du) or None, dbias fp32 [2 I]
     or None)."""
-    return _backward("gated_backward", dh, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add, need_dz,
+    return _backward("wq_gated_backward", dh, preact, packed, scales, zeros, bits, group_size, perm, act, dx_add, need_dz,
                      need_dbias, out, workspace)
 
 

@@ -30,8 +30,8 @@ bool query_ok(int M, long long rows, int K, int bits) {
     return sizes_ok(M, rows, K) && M > 0 && rows > 0 && wqh::bits_ok(bits);
 }
 
-size_t fwd_workspace(int M, int rows, int K, bool has_perm, bool gated) {
-    const size_t part = M <= wqh::kBlockSmallM ? wqh::block_small_part_bytes(M, rows, K, gated)
+size_t fwd_workspace(int M, int rows, int K, int bits, bool has_perm, bool gated) {
+    const size_t part = M <= wqh::kBlockSmallM ? wqh::block_small_part_bytes(M, rows, K, bits, gated)
                                                : wqh::block_fwd_part_bytes(M, rows, K, gated);
     return (has_perm ? gather_bytes(M, K) : 0) + part;
 }
@@ -66,7 +66,13 @@ wq_status forward(const uint16_t* x, const uint32_t* packed, const uint16_t* sca
     const wqh::BlockFwd f{x, packed, scales, zeros, M, rows, K, bits, gs, gated,
                           wq::Epilogue{bias, residual, y, preact, N, act}};
     float* part = reinterpret_cast<float*>(ws);
-    return M <= wqh::kBlockSmallM ? wqh::block_small(f, part, left, s) : wqh::block_fwd(f, part, left, s);
+    if (M <= wqh::kBlockSmallM) {
+        // (a K too long for one block's registers without room for partial
+        // sums goes to the tiled kernel)
+        const wq_status d = wqh::block_small(f, part, left, s);
+        if (d != WQ_ERR_UNSUPPORTED) return d;
+    }
+    return wqh::block_fwd(f, part, left, s);
 }
 
 wq_status backward(const uint16_t* dy, const uint16_t* preact, int act, const uint32_t* packed,
@@ -132,11 +138,11 @@ extern "C" wq_status wq_gated_backward(const uint16_t* dh, const uint16_t* preac
 }
 
 extern "C" size_t wq_linear_act_workspace_size(int32_t M, int32_t N, int32_t K, int32_t bits, int32_t has_perm) {
-    return query_ok(M, N, K, bits) ? fwd_workspace(M, N, K, has_perm != 0, false) : 0;
+    return query_ok(M, N, K, bits) ? fwd_workspace(M, N, K, bits, has_perm != 0, false) : 0;
 }
 
 extern "C" size_t wq_gated_workspace_size(int32_t M, int32_t I, int32_t K, int32_t bits, int32_t has_perm) {
-    return query_ok(M, 2LL * I, K, bits) ? fwd_workspace(M, 2 * I, K, has_perm != 0, true) : 0;
+    return query_ok(M, 2LL * I, K, bits) ? fwd_workspace(M, 2 * I, K, bits, has_perm != 0, true) : 0;
 }
 
 extern "C" size_t wq_linear_act_backward_workspace_size(int32_t M, int32_t N, int32_t K, int32_t bits,

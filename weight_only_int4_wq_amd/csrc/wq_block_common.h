@@ -338,7 +338,8 @@ wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream
 
 // Small M (decode batches).
 constexpr int kBlockSmallM = 32;
-size_t block_small_part_bytes(int M, int rows, int K, bool gated);
+size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated);
+// WQ_ERR_UNSUPPORTED when K has to be split and `part` has no room for it.
 wq_status block_small(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
 // e applied to the sum over `splits` partial products [splits][M][rows].
