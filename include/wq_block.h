@@ -96,8 +96,9 @@ size_t wq_gated_workspace_size(int32_t M, int32_t I, int32_t K, int32_t bits, in
  * dx_add or zero.
  * The workspace part that cannot be left out: dz rows padded to a multiple of
  * 8 when dz is NULL and the activation is not WQ_ACT_NONE, or when N is no
- * multiple of 8; dbias's partial sums when dbias is given; fp32 dx with
- * act-order.  The rest holds partial sums of an N split. */
+ * multiple of 8; dbias's partial sums when dbias is given; with act-order
+ * fp32 dx, its rows rounded up to 64 and its columns to 256.  The rest holds
+ * partial sums of an N split. */
 wq_status wq_linear_act_backward(const uint16_t* dy, const uint16_t* preact, int32_t act, const uint32_t* packed,
                                  const uint16_t* scales, const uint8_t* zeros, const int32_t* perm,
                                  const uint16_t* dx_add, uint16_t* dx, uint16_t* dz, float* dbias, int32_t M,

@@ -280,7 +280,8 @@ def test_smallest_workspace(entry, M, N, K, ao):
         x = randn(22, M, K)
         call = lambda ws: getattr(wq, entry)(x, *L["args"], perm=L["perm"], act="silu", workspace=ws)  # noqa: E731
     else:
-        least = r256(M * ((rows + 7) // 8 * 8) * 2) + (M * K * 4 if ao else 0)
+        tiles = -(-M // 64) * -(-K // 256)
+        least = r256(M * ((rows + 7) // 8 * 8) * 2) + (tiles * 64 * 256 * 4 if ao else 0)
         dy, z = randn(23, M, N), randn(24, M, rows)
         call = lambda ws: getattr(wq, entry)(dy, z, *L["args"], perm=L["perm"], act="silu", need_dz=False,  # noqa: E731
                                              workspace=ws)[0]

@@ -125,9 +125,15 @@ def _check(code: int, what: str) -> None:
 
 # ----------------------------------------------------------- marshalling --
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev(t, dtype, name, ndim=None, allow_none=False, shape=None, device=None):
@@ -546,11 +552,13 @@ def _block_call(entry, device, args, M, N, K, bits, group_size, has_perm, worksp
         workspace = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
     at, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     fn = getattr(handle, entry)
+    # (the raw handle of torch.cuda.current_stream(device), without its object)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            code = fn(*args, M, N, K, bits, group_size, at, nbytes, torch.cuda.current_stream(device).cuda_stream)
+            code = fn(*args, M, N, K, bits, group_size, at, nbytes, stream)
     else:
-        code = fn(*args, M, N, K, bits, group_size, at, nbytes, torch.cuda.current_stream(device).cuda_stream)
+        code = fn(*args, M, N, K, bits, group_size, at, nbytes, stream)
     if code:
         _check(code, entry)
 

@@ -140,10 +140,10 @@ struct DxArgs {
     const uint8_t* zeros;
     const uint16_t* add;  // [M][K], nullable, may be dx
     uint16_t* dx;
-    float* part;  // [splits][M][K], or null
+    float* part;  // [ranges][tail tiles][BM][256] partial products
     int M, R, K, ld;
     GroupDiv gd;
-    int m_tiles, k_tiles, tiles, sps;
+    int m_tiles, k_tiles, tiles, head, sps;
 };
 
 // One weight row's 8-code block: 8 * BITS bits in the low bits of w[0] (w[1]
@@ -205,6 +205,27 @@ __device__ __forceinline__ void decode_columns(int i, const uint32_t* a, const u
     }
 }
 
+// Four columns of one row: dx = fp16(v + add); with perm, column k' of the
+// packed order belongs to channel perm[k'].
+__device__ __forceinline__ void finish_dx(const uint16_t* add, uint16_t* dx, const int32_t* perm, size_t row_at, int col,
+                                          float (&v)[4]) {
+    if (perm) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const size_t at = row_at + perm[col + q];
+            dx[at] = f2h(v[q] + (add ? h2f(add[at]) : 0.f));
+        }
+        return;
+    }
+    if (add) {
+        float b[4];
+        load_h<4>(add + row_at + col, b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += b[q];
+    }
+    store_h<4>(dx + row_at + col, v);
+}
+
 // G8: groups of 32 channels, up to 8 groups per tile; otherwise up to 4
 // (group sizes of 64 and more, tiles start at multiples of 256).
 template <int BITS, int BM, bool G8>
@@ -224,14 +245,13 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int c = lane & 31, hh = lane >> 5;
-    int m_t, k_t;
-    tile_coords<4>(blockIdx.x, p.tiles, p.m_tiles, p.k_tiles, m_t, k_t);
-    const int m0 = m_t * BM, k0 = k_t * 256;
+    const TileWork tw = tile_work(blockIdx.x, p.tiles, p.head, p.m_tiles, p.k_tiles);
+    const int m0 = tw.m_t * BM, k0 = tw.n_t * 256;
     const int chunks = p.K / 32;
     const int G = chunk_group(chunks - 1, p.gd) + 1;
     const int stages = (p.R + BK - 1) / BK;
-    const int st_begin = int(blockIdx.y) * p.sps;
-    const int st_end = min(st_begin + p.sps, stages);
+    const int st_begin = tw.split * p.sps;
+    const int st_end = tw.part < 0 ? stages : min(st_begin + p.sps, stages);
     const int st_last = st_end - 1;
 
     // ---- dz: thread t copies unit t % 8 of rows t / 8 + 32 i
@@ -399,7 +419,20 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
 
     // ---- acc[i][j][r]: row 32 i + 8 (r / 4) + 4 hh + r % 4, column
     // 8 (c % 16) + 4 (c / 16) + j of the wavefront's BM/2 x 128
-    const int col = k0 + wn * 128 + 8 * (c & 15) + 4 * (c >> 4);
+    const int lc = wn * 128 + 8 * (c & 15) + 4 * (c >> 4);
+    if (tw.part >= 0) {  // the whole tile, rows and columns past the matrix too
+        float* pr = p.part + size_t(tw.part) * (BM * 256) + lc;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int lr = wm * (BM / 2) + 32 * i + 8 * (r >> 2) + 4 * hh + (r & 3);
+                *reinterpret_cast<f4*>(pr + lr * 256) = f4{acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
+                if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few accumulators on their way at a time
+            }
+        return;
+    }
+    const int col = k0 + lc;
     if (col >= p.K) return;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -407,92 +440,72 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
         for (int r = 0; r < 16; ++r) {
             const int row = m0 + wm * (BM / 2) + 32 * i + 8 * (r >> 2) + 4 * hh + (r & 3);
             if (row >= p.M) continue;
-            const size_t at = size_t(row) * p.K + col;
             float v[4] = {acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
-            if (p.part) {
-                float* dst = p.part + size_t(blockIdx.y) * p.M * p.K + at;
-                *reinterpret_cast<f4*>(dst) = f4{v[0], v[1], v[2], v[3]};
-            } else {
-                if (p.add) {
-                    float b[4];
-                    load_h<4>(p.add + at, b);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] += b[q];
-                }
-                store_h<4>(p.dx + at, v);
-            }
+            finish_dx(p.add, p.dx, nullptr, size_t(row) * p.K, col, v);
         }
 }
 
-// dx = fp16(sum over the ranges, in order, + add); with perm the sum of
-// packed column k' belongs to channel perm[k'].  Four columns per thread.
-__global__ void __launch_bounds__(256) block_dx_finish_kernel(const float* __restrict__ part, int splits, int M,
-                                                              int K, const int32_t* __restrict__ perm,
-                                                              const uint16_t* add, uint16_t* dx) {
-    const int per_row = K / 4;
-    const size_t total = size_t(M) * per_row, step = size_t(M) * K;
-    for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += size_t(gridDim.x) * 256) {
-        const size_t row = i / per_row;
-        const int k = int(i % per_row) * 4;
-        const float* src = part + row * K + k;
+// The same for tiles cut in ranges (with act-order, for every tile): block b
+// takes 16 rows of a tail tile, the ranges' partial products are added in
+// order.
+template <int BM>
+__global__ void __launch_bounds__(256) block_dx_tail_kernel(const DxArgs p, int splits,
+                                                            const int32_t* __restrict__ perm) {
+    const int tail = p.tiles - p.head, i = blockIdx.x / (BM / 16), r0 = (blockIdx.x % (BM / 16)) * 16;
+    int m_t, k_t;
+    tile_place(p.head + i, p.m_tiles, p.k_tiles, m_t, k_t);
+    const size_t step = size_t(tail) * (BM * 256);
+    for (int q = threadIdx.x; q < 16 * 64; q += 256) {
+        const int rr = r0 + q / 64, lc = (q & 63) * 4, row = m_t * BM + rr, col = k_t * 256 + lc;
+        if (row >= p.M || col >= p.K) continue;
+        const float* src = p.part + (size_t(i) * BM + rr) * 256 + lc;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < splits; ++s, src += step) {
-            const f4 w = *reinterpret_cast<const f4*>(src);
+        for (int s = 0; s < splits; ++s) {
+            const f4 w = *reinterpret_cast<const f4*>(src + s * step);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] += w[q];
+            for (int e = 0; e < 4; ++e) v[e] += w[e];
         }
-        if (perm) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const size_t at = row * K + perm[k + q];
-                dx[at] = f2h(v[q] + (add ? h2f(add[at]) : 0.f));
-            }
-        } else {
-            const size_t at = row * K + k;
-            if (add) {
-                float b[4];
-                load_h<4>(add + at, b);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += b[q];
-            }
-            store_h<4>(dx + at, v);
-        }
+        finish_dx(p.add, p.dx, perm, size_t(row) * p.K, col, v);
+    }
+}
+
+// dx of an empty sum: dx_add, or zero.
+__global__ void __launch_bounds__(256) block_dx_empty_kernel(size_t n4, const uint16_t* add, uint16_t* dx) {
+    for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n4; i += size_t(gridDim.x) * 256) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        finish_dx(add, dx, nullptr, i * 4, 0, v);
     }
 }
 
 constexpr wqh::TileCost kDxCosts[3] = {
     {64, 0.80, 0.28, 6.0, false}, {128, 1.09, 0.27, 6.5, false}, {256, 1.37, 0.30, 9.9, false}};
 
-wqh::TilePlan dx_plan(int M, int R, int K, size_t part_bytes) {
-    return wqh::plan_tiles(M, (K + 255) / 256, (R + 63) / 64, K, kDxCosts, 1, part_bytes, wqh::gemm_slots(1));
+wqh::TilePlan dx_plan(int M, int R, int K, bool has_perm, size_t part_bytes) {
+    return wqh::plan_tiles(M, (K + 255) / 256, (R + 63) / 64, kDxCosts, 1, part_bytes, wqh::gemm_slots(1), has_perm);
 }
 
 template <int BITS, int BM, bool G8>
-wq_status launch_dx(const wqh::TilePlan& pl, const DxArgs& a, hipStream_t s) {
+wq_status launch_dx(const wqh::TilePlan& pl, const int32_t* perm, const DxArgs& a, hipStream_t s) {
     constexpr int lds = 2 * (BM * 128 + 256 * 128 + 2 * (G8 ? 8 : 4) * 128);
     auto kern = block_dx_kernel<BITS, BM, G8>;
     const hipError_t e =
         hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return wqh::hip_status(e);
-    hipLaunchKernelGGL(kern, dim3(a.tiles, pl.splits), dim3(256), lds, s, a);
+    hipLaunchKernelGGL(kern, dim3(pl.blocks()), dim3(256), lds, s, a);
+    const wq_status st = wqh::launch_status();
+    if (st != WQ_OK || pl.tail() == 0) return st;
+    hipLaunchKernelGGL((block_dx_tail_kernel<BM>), dim3(unsigned(pl.tail()) * (BM / 16)), dim3(256), 0, s, a, pl.splits,
+                       perm);
     return wqh::launch_status();
 }
 
 template <int BITS>
-wq_status launch_dx_bits(const wqh::TilePlan& pl, bool g8, const DxArgs& a, hipStream_t s) {
+wq_status launch_dx_bits(const wqh::TilePlan& pl, const int32_t* perm, bool g8, const DxArgs& a, hipStream_t s) {
     switch (pl.BM) {
-        case 64: return g8 ? launch_dx<BITS, 64, true>(pl, a, s) : launch_dx<BITS, 64, false>(pl, a, s);
-        case 128: return g8 ? launch_dx<BITS, 128, true>(pl, a, s) : launch_dx<BITS, 128, false>(pl, a, s);
-        default: return g8 ? launch_dx<BITS, 256, true>(pl, a, s) : launch_dx<BITS, 256, false>(pl, a, s);
+        case 64: return g8 ? launch_dx<BITS, 64, true>(pl, perm, a, s) : launch_dx<BITS, 64, false>(pl, perm, a, s);
+        case 128: return g8 ? launch_dx<BITS, 128, true>(pl, perm, a, s) : launch_dx<BITS, 128, false>(pl, perm, a, s);
+        default: return g8 ? launch_dx<BITS, 256, true>(pl, perm, a, s) : launch_dx<BITS, 256, false>(pl, perm, a, s);
     }
-}
-
-wq_status dx_finish(const float* part, int splits, int M, int K, const int32_t* perm, const uint16_t* add,
-                    uint16_t* dx, hipStream_t s) {
-    const size_t total = size_t(M) * (K / 4);
-    const int blocks = int(std::min<size_t>((total + 255) / 256, size_t(wqh::gemm_slots(8))));
-    hipLaunchKernelGGL(block_dx_finish_kernel, dim3(blocks), dim3(256), 0, s, part, splits, M, K, perm, add, dx);
-    return wqh::launch_status();
 }
 
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -506,16 +519,14 @@ int dbias_ranges(int M, int R) {
 }
 
 struct BwdBytes {
-    size_t dz, dbias, dx, split;  // dx: act-order's fp32 sums; split: what a split would like instead
+    size_t dz, dbias, dx;  // dx: partial products, act-order's among them
 };
 
 BwdBytes bwd_bytes(int M, int R, int K, bool has_perm) {
     BwdBytes b{};
     b.dz = round256(size_t(M) * ((size_t(R) + 7) / 8 * 8) * 2);
     b.dbias = round256(size_t(dbias_ranges(M, R)) * R * 4);
-    b.dx = has_perm ? size_t(M) * K * 4 : 0;
-    const wqh::TilePlan p = dx_plan(M, R, K, ~size_t(0));
-    b.split = p.splits > 1 ? size_t(p.splits) * M * K * 4 : 0;
+    b.dx = dx_plan(M, R, K, has_perm, ~size_t(0)).part_bytes();
     return b;
 }
 
@@ -526,7 +537,7 @@ namespace wqh {
 size_t block_bwd_workspace_bytes(int M, int R, int K, bool has_perm) {
     if (M <= 0 || R <= 0) return 0;
     const BwdBytes b = bwd_bytes(M, R, K, has_perm);
-    return b.dz + b.dbias + std::max(b.dx, b.split);
+    return b.dz + b.dbias + b.dx;
 }
 
 wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool gated, const uint32_t* packed,
@@ -535,7 +546,11 @@ wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool ga
                     size_t ws_bytes, hipStream_t s) {
     const int R = gated ? 2 * N : N;
     if (R == 0) {  // an empty sum
-        return M == 0 ? WQ_OK : dx_finish(nullptr, 0, M, K, nullptr, add, dx, s);
+        if (M == 0) return WQ_OK;
+        const size_t n4 = size_t(M) * (K / 4);
+        hipLaunchKernelGGL(block_dx_empty_kernel, dim3(unsigned(std::min<size_t>((n4 + 255) / 256, gemm_slots(8)))),
+                           dim3(256), 0, s, n4, add, dx);
+        return launch_status();
     }
     if (M == 0) {
         if (!dbias) return WQ_OK;
@@ -567,7 +582,8 @@ wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool ga
         dzp = nullptr;
     }
     if (ranges > 1 && !(dbp = reinterpret_cast<float*>(take(size_t(ranges) * R * 4)))) return WQ_ERR_ARG;
-    if (perm && left < size_t(M) * K * 4) return WQ_ERR_ARG;
+    const TilePlan pl = dx_plan(M, R, K, perm != nullptr, left);
+    if (pl.tiles == 0) return WQ_ERR_ARG;  // act-order's partial products do not fit
 
     // ---- dz, dbias
     if (!none || own_dz || dz || dbias) {
@@ -598,21 +614,16 @@ wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool ga
     }
 
     // ---- dx
-    const TilePlan pl = dx_plan(M, R, K, left);
-    const bool part = perm || pl.splits > 1;
     const int m_tiles = (M + pl.BM - 1) / pl.BM, k_tiles = (K + 255) / 256;
-    const DxArgs a{operand, packed, scales, zeros, add, dx, part ? reinterpret_cast<float*>(w) : nullptr, M, R, K,
-                   ld, group_magic(gs), m_tiles, k_tiles, m_tiles * k_tiles, pl.sps};
+    const DxArgs a{operand, packed, scales, zeros, add, dx, reinterpret_cast<float*>(w), M, R, K, ld, group_magic(gs),
+                   m_tiles, k_tiles, pl.tiles, pl.head, pl.sps};
     const bool g8 = gs < 64;
-    wq_status st;
     switch (bits) {
-        case 2: st = launch_dx_bits<2>(pl, g8, a, s); break;
-        case 3: st = launch_dx_bits<3>(pl, g8, a, s); break;
-        case 4: st = launch_dx_bits<4>(pl, g8, a, s); break;
-        default: st = launch_dx_bits<8>(pl, g8, a, s); break;
+        case 2: return launch_dx_bits<2>(pl, perm, g8, a, s);
+        case 3: return launch_dx_bits<3>(pl, perm, g8, a, s);
+        case 4: return launch_dx_bits<4>(pl, perm, g8, a, s);
+        default: return launch_dx_bits<8>(pl, perm, g8, a, s);
     }
-    if (st != WQ_OK || !part) return st;
-    return dx_finish(a.part, pl.splits, M, K, perm, add, dx, s);
 }
 
 }  // namespace wqh

@@ -40,6 +40,42 @@ __device__ __forceinline__ void sched_step() {
     }
 }
 
+// What a tile kernel's block does under a TilePlan: its tile's coordinates,
+// whether its product is partial, and which partial product it is.
+struct TileWork {
+    int m_t, n_t, split;
+    long long part;  // (split, tile of the tail), -1 for a whole tile
+};
+
+// Tile t of m_tiles x n_tiles: consecutive tiles cover strips of four M-tiles,
+// so that what runs at a time is a compact rectangle.
+__device__ __forceinline__ void tile_place(int t, int m_tiles, int n_tiles, int& m_t, int& n_t) {
+    constexpr int GM = 4;
+    const int group = t / (GM * n_tiles), first_m = group * GM;
+    const int gsm = min(m_tiles - first_m, GM), r = t - group * (GM * n_tiles);
+    m_t = first_m + r % gsm;
+    n_t = r / gsm;
+}
+
+// Blocks are dealt to the XCDs round-robin; each gets contiguous tiles.
+__device__ __forceinline__ TileWork tile_work(int b, int tiles, int head, int m_tiles, int n_tiles) {
+    TileWork w;
+    int t;
+    if (b < head) {
+        t = xcd_tile(b, head, 8);
+        w.split = 0;
+        w.part = -1;
+    } else {
+        const int tail = tiles - head, q = b - head;
+        w.split = q / tail;
+        const int i = xcd_tile(q - w.split * tail, tail, 8);
+        t = head + i;
+        w.part = (long long)w.split * tail + i;
+    }
+    tile_place(t, m_tiles, n_tiles, w.m_t, w.n_t);
+    return w;
+}
+
 // ------------------------------------------------ copies into LDS ----
 //
 // Tiles go from memory straight into LDS (no registers, no LDS writes, which
@@ -277,43 +313,58 @@ struct TileCost {
     double idle, load, fixed;
     bool overlap;
 };
+// How a tile kernel covers its tiles: tiles 0 .. head - 1 whole, the others cut
+// into `splits` ranges of `sps` stages, whose fp32 partial products meet in a
+// second kernel.
 struct TilePlan {
-    int BM = 128, splits = 1, sps = 0;
+    int BM = 128, splits = 1, sps = 0, tiles = 0, head = 0;
+    int tail() const { return tiles - head; }
+    unsigned blocks() const { return unsigned(head) + unsigned(tail()) * unsigned(splits); }
+    size_t part_bytes() const { return size_t(tail()) * splits * BM * 256 * 4; }
 };
 
-// Tile height and split of the summed dimension with the least modelled time:
-// blocks run in rounds of one per unit; a split writes and re-reads fp32
-// partial sums of M x cols and launches a second kernel.  Ranges are multiples
-// of `align` stages, at least four.  The costs are fitted to 1458 timings of
-// the two tile kernels (M = 33 .. 2048, five layers from 1024 x 2048 to
-// 28672 x 8192, all heights and 1 .. 32 ranges), over which the plan's choice
-// is within 2 % of the best on average and 20 % at worst.
-inline TilePlan plan_tiles(int M, int n_tiles, int stages, int cols, const TileCost (&costs)[3], int align,
-                           size_t part_bytes, int units) {
+// Tile height and cut with the least modelled time: blocks run in rounds of
+// one per unit; whole rounds run whole, and what a last, partly filled round
+// would hold may be cut (or everything, when there is less than a round).  A
+// cut writes and re-reads its partial products and launches a second kernel.
+// Ranges are multiples of `align` stages, at least four.  The costs are fitted
+// to 1458 timings of the two tile kernels (M = 33 .. 2048, five layers from
+// 1024 x 2048 to 28672 x 8192, all heights and 1 .. 32 ranges), over which the
+// choice among uniform cuts is within 2 % of the best on average and 20 % at
+// worst.  all_part: every product goes through the second kernel.
+inline TilePlan plan_tiles(int M, int n_tiles, int stages, const TileCost (&costs)[3], int align, size_t part_bytes,
+                           int units, bool all_part) {
     TilePlan best;
-    best.sps = stages;
     double best_us = 1e300;
     for (const TileCost& c : costs) {
-        for (int S = 1; S <= 32; ++S) {
-            const int sps = ((stages + S - 1) / S + align - 1) / align * align;
-            if ((stages + sps - 1) / sps != S) continue;
-            const double bytes = double(S) * M * cols * 4.0;
-            if (S > 1 && (sps < 4 || bytes > double(part_bytes))) continue;
-            const double blocks = double((M + c.BM - 1) / c.BM) * n_tiles * S;
-            auto round_us = [&](double share) { return sps * (c.idle + c.load * share) + c.fixed; };
-            double us;
-            if (blocks <= units)
-                us = round_us(blocks / units);
-            else if (c.overlap)
-                us = round_us(1.0) * (blocks / units);
-            else {
-                const double whole = double((long long)(blocks / units)), rest = blocks / units - whole;
-                us = whole * round_us(1.0) + (rest > 0 ? round_us(rest) : 0.0);
-            }
-            if (S > 1) us += 2.1 + 2.0 * bytes / 5.1e6;
-            if (us < best_us) {
-                best_us = us;
-                best = TilePlan{c.BM, S, sps};
+        const long long tiles_ll = (long long)((M + c.BM - 1) / c.BM) * n_tiles;
+        if (tiles_ll > (1LL << 30)) continue;
+        const int tiles = int(tiles_ll);
+        auto round_us = [&](int st, double share) { return st * (c.idle + c.load * share) + c.fixed; };
+        // `blocks` of st stages in rounds
+        auto run_us = [&](double blocks, int st) {
+            if (blocks <= units) return blocks > 0 ? round_us(st, blocks / units) : 0.0;
+            if (c.overlap) return round_us(st, 1.0) * (blocks / units);
+            const double whole = double((long long)(blocks / units)), rest = blocks / units - whole;
+            return whole * round_us(st, 1.0) + (rest > 0 ? round_us(st, rest) : 0.0);
+        };
+        const int whole = tiles / units * units;
+        for (int pass = 0; pass < 2; ++pass) {
+            const int head = pass == 0 ? 0 : whole;
+            if (pass == 1 && (head == 0 || head == tiles || all_part)) continue;
+            for (int S = 1; S <= 32; ++S) {
+                const int sps = ((stages + S - 1) / S + align - 1) / align * align;
+                if ((stages + sps - 1) / sps != S || (S == 1 && pass == 1)) continue;
+                TilePlan p{c.BM, S, sps, tiles, S == 1 && !all_part ? tiles : head};
+                const double bytes = double(p.part_bytes());
+                if (p.tail() > 0 && bytes > double(part_bytes)) continue;
+                if (S > 1 && sps < 4) continue;
+                double us = run_us(p.head, stages) + run_us(double(p.tail()) * S, sps);
+                if (p.tail() > 0) us += 2.1 + 2.0 * bytes / 5.1e6;
+                if (us < best_us) {
+                    best_us = us;
+                    best = p;
+                }
             }
         }
     }

@@ -49,10 +49,10 @@ struct FwdArgs {
     const uint32_t* packed;
     const uint16_t* scales;
     const uint8_t* zeros;
-    float* part;  // fp32 sums of a K split, or null
+    float* part;  // [ranges][tail tiles][BM][256] partial products
     int M, rows, K;
     GroupDiv gd;
-    int m_tiles, n_tiles, tiles, sps;
+    int m_tiles, n_tiles, tiles, head, sps;
     int gated;
     Epilogue e;
 };
@@ -73,6 +73,49 @@ struct FwdShape {
     static constexpr int LDS = MAIN > PASS * 256 * 4 ? MAIN : PASS * 256 * 4;
 };
 
+// Outputs oc .. oc + 7 of a tile row.  The tile's column 32 w + c holds the
+// first and 128 + 32 w + c the second weight row of lane c of wavefront w: the
+// gate's and the up projection's of output 32 w + c, or columns 64 w + 2 c and
+// 64 w + 2 c + 1.
+template <class Get>
+__device__ __forceinline__ void finish_piece(const Epilogue& e, bool gated, bool wide, int row, int o0, int oc,
+                                             const Get& get) {
+    const int col = o0 + oc;
+    if (col >= e.out) return;
+    float a[8], u[8];
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = get(oc + i);
+            u[i] = get(128 + oc + i);
+        }
+        if (wide) {
+            finish<true, 8>(e, row, col, a, u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float a1[1] = {a[i]}, u1[1] = {u[i]};
+                if (col + i < e.out) finish<true, 1>(e, row, col + i, a1, u1);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = get(128 * (i & 1) + oc / 2 + (i >> 1));
+            u[i] = 0.f;
+        }
+        if (wide) {
+            finish<false, 8>(e, row, col, a, u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float a1[1] = {a[i]}, u1[1] = {0.f};
+                if (col + i < e.out) finish<false, 1>(e, row, col + i, a1, u1);
+            }
+        }
+    }
+}
+
 // FAST: the group size is a multiple of 128 (or all of K, itself a multiple),
 // so two stages share a scale and zero-point.
 template <int BITS, bool FAST, int BM>
@@ -91,14 +134,13 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
     const int c = lane & 31, hh = lane >> 5;
     const bool gated = p.gated != 0;
     const int oc_tile = gated ? BN / 2 : BN;  // output columns of the tile
-    int m_t, n_t;
-    tile_coords<4>(blockIdx.x, p.tiles, p.m_tiles, p.n_tiles, m_t, n_t);
-    const int m0 = m_t * BM, o0 = n_t * oc_tile;
+    const TileWork tw = tile_work(blockIdx.x, p.tiles, p.head, p.m_tiles, p.n_tiles);
+    const int m0 = tw.m_t * BM, o0 = tw.n_t * oc_tile;
     const int chunks = p.K / 32;
     const int G = chunk_group(chunks - 1, p.gd) + 1;
     const int stages = (p.K + BK - 1) / BK;
-    const int st_begin = int(blockIdx.y) * p.sps;  // a multiple of 4
-    const int st_end = min(st_begin + p.sps, stages);
+    const int st_begin = tw.split * p.sps;  // a multiple of 4
+    const int st_end = tw.part < 0 ? stages : min(st_begin + p.sps, stages);
 
     const TileCopy<BM> xcopy(p.x + size_t(m0) * p.K, p.M - m0, p.K, wave, lane);
 
@@ -276,21 +318,18 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
 
     // ---- acc[i][j][r]: row 32 i + 8 (r / 4) + 4 hh + r % 4, the lane's j-th
     // weight row
-    if (p.part) {
-        float* pr = p.part + size_t(blockIdx.y) * p.M * p.rows;
-        const int col = gated ? o0 + wave * 32 + c : o0 + wave * 64 + 2 * c;
-        const int lim = gated ? p.e.out : p.rows;
-        auto put = [&](auto jc, int at) {
+    if (tw.part >= 0) {
+        // columns as the LDS tile below has them; rows and columns past the
+        // matrix are written too (the tile is whole) and never read
+        float* pr = p.part + size_t(tw.part) * (BM * BN) + wave * 32 + c;
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = m0 + 32 * i + 8 * (r >> 2) + 4 * hh + (r & 3);
-                    if (row < p.M) pr[size_t(row) * p.rows + at] = acc[i][decltype(jc)::value][r];
-                }
-        };
-        if (col < lim) put(std::integral_constant<int, 0>{}, col);
-        if (gated ? col < lim : col + 1 < lim) put(std::integral_constant<int, 1>{}, gated ? p.e.out + col : col + 1);
+            for (int r = 0; r < 16; ++r) {
+                float* dst = pr + (32 * i + 8 * (r >> 2) + 4 * hh + (r & 3)) * BN;
+                dst[0] = acc[i][0][r];
+                dst[128] = acc[i][1][r];
+            }
         return;
     }
     // LDS tile: the wavefront's first rows' products in columns 32 w + c, the
@@ -298,61 +337,52 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
     float* tile = reinterpret_cast<float*>(lds);  // [PASS][BN]
     const bool wide = p.e.out % 8 == 0;
     const int per_row = oc_tile / 8;
-#pragma unroll
-    for (int ps = 0; ps < BM / Sh::PASS; ++ps) {
+    auto pass = [&](auto ps_c) {  // (named at compile time, as the accumulators are)
+        constexpr int ps = decltype(ps_c)::value;
         if (ps) __syncthreads();
 #pragma unroll
-        for (int ii = 0; ii < Sh::PASS / 32; ++ii) {
-            const int i = ps * (Sh::PASS / 32) + ii;
+        for (int ii = 0; ii < Sh::PASS / 32; ++ii)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 float* dst = tile + (32 * ii + 8 * (r >> 2) + 4 * hh + (r & 3)) * BN + wave * 32 + c;
-                dst[0] = acc[i][0][r];
-                dst[128] = acc[i][1][r];
+                dst[0] = acc[ps * (Sh::PASS / 32) + ii][0][r];
+                dst[128] = acc[ps * (Sh::PASS / 32) + ii][1][r];
             }
-        }
         __syncthreads();
 #pragma unroll 1
         for (int q = tid; q < Sh::PASS * per_row; q += 256) {
             const int rr = q / per_row, oc = (q % per_row) * 8;
-            const int row = m0 + ps * Sh::PASS + rr, col = o0 + oc;
-            if (row >= p.M || col >= p.e.out) continue;
-            if (gated) {
-                const float* src = tile + rr * BN + oc;
-                float a[8], u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] = src[i];
-                    u[i] = src[128 + i];
-                }
-                if (wide) {
-                    finish<true, 8>(p.e, row, col, a, u);
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < 8 && col + i < p.e.out; ++i) {
-                        float a1[1] = {src[i]}, u1[1] = {src[128 + i]};
-                        finish<true, 1>(p.e, row, col + i, a1, u1);
-                    }
-                }
-            } else {  // column 2 c + j of a wavefront's 64
-                const float* src = tile + rr * BN + oc / 2;
-                float a[8], u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] = src[128 * (i & 1) + (i >> 1)];
-                    u[i] = 0.f;
-                }
-                if (wide) {
-                    finish<false, 8>(p.e, row, col, a, u);
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < 8 && col + i < p.e.out; ++i) {
-                        float a1[1] = {src[128 * (i & 1) + (i >> 1)]}, u1[1] = {0.f};
-                        finish<false, 1>(p.e, row, col + i, a1, u1);
-                    }
-                }
-            }
+            const int row = m0 + ps * Sh::PASS + rr;
+            if (row < p.M) finish_piece(p.e, gated, wide, row, o0, oc, [&](int i) { return tile[rr * BN + i]; });
         }
+    };
+    pass(std::integral_constant<int, 0>{});
+    if constexpr (BM > 64) pass(std::integral_constant<int, 1>{});
+    if constexpr (BM > 128) {
+        pass(std::integral_constant<int, 2>{});
+        pass(std::integral_constant<int, 3>{});
+    }
+}
+
+// The same for tiles cut in ranges: block b takes 16 rows of a tail tile, the
+// ranges' partial products are added in order.
+template <int BM>
+__global__ void __launch_bounds__(256) block_tail_kernel(const FwdArgs p, int splits) {
+    const int tail = p.tiles - p.head, i = blockIdx.x / (BM / 16), r0 = (blockIdx.x % (BM / 16)) * 16;
+    int m_t, n_t;
+    tile_place(p.head + i, p.m_tiles, p.n_tiles, m_t, n_t);
+    const bool gated = p.gated != 0, wide = p.e.out % 8 == 0;
+    const int oc_tile = gated ? 128 : 256, per_row = oc_tile / 8;
+    const size_t step = size_t(tail) * (BM * 256);
+    for (int q = threadIdx.x; q < 16 * per_row; q += 256) {
+        const int rr = r0 + q / per_row, oc = (q % per_row) * 8, row = m_t * BM + rr;
+        if (row >= p.M) continue;
+        const float* src = p.part + (size_t(i) * BM + rr) * 256;
+        finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](int at) {
+            float v = 0.f;
+            for (int s = 0; s < splits; ++s) v += src[s * step + at];
+            return v;
+        });
     }
 }
 
@@ -391,12 +421,15 @@ constexpr wqh::TileCost kFwdCosts[3] = {
 wqh::TilePlan fwd_plan(int M, int rows, int K, bool gated, size_t part_bytes) {
     const int n_tiles = gated ? (rows / 2 + 127) / 128 : (rows + 255) / 256;
     // ranges of whole windows of weights and scales (four stages)
-    return wqh::plan_tiles(M, n_tiles, (K + 63) / 64, rows, kFwdCosts, 4, part_bytes, wqh::gemm_slots(1));
+    return wqh::plan_tiles(M, n_tiles, (K + 63) / 64, kFwdCosts, 4, part_bytes, wqh::gemm_slots(1), false);
 }
 
 template <int BITS, bool FAST, int BM>
 wq_status launch_fwd(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((block_fwd_kernel<BITS, FAST, BM>), dim3(a.tiles, pl.splits), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((block_fwd_kernel<BITS, FAST, BM>), dim3(pl.blocks()), dim3(256), 0, s, a);
+    const wq_status st = wqh::launch_status();
+    if (st != WQ_OK || pl.tail() == 0) return st;
+    hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(unsigned(pl.tail()) * (BM / 16)), dim3(256), 0, s, a, pl.splits);
     return wqh::launch_status();
 }
 
@@ -420,24 +453,21 @@ namespace wqh {
 
 size_t block_fwd_part_bytes(int M, int rows, int K, bool gated) {
     const TilePlan p = fwd_plan(M, rows, K, gated, ~size_t(0));
-    return p.splits > 1 ? size_t(p.splits) * M * rows * 4 : 0;
+    return p.part_bytes();
 }
 
 wq_status block_fwd(const BlockFwd& f, float* part, size_t part_bytes, hipStream_t s) {
     const TilePlan pl = fwd_plan(f.M, f.rows, f.K, f.gated, part ? part_bytes : 0);
     const int oc = f.gated ? 128 : 256;
     const int m_tiles = (f.M + pl.BM - 1) / pl.BM, n_tiles = (f.e.out + oc - 1) / oc;
-    const FwdArgs a{f.x, f.packed, f.scales, f.zeros, pl.splits > 1 ? part : nullptr, f.M, f.rows, f.K,
-                    group_magic(f.gs), m_tiles, n_tiles, m_tiles * n_tiles, pl.sps, f.gated, f.e};
-    wq_status st;
+    const FwdArgs a{f.x, f.packed, f.scales, f.zeros, part, f.M, f.rows, f.K, group_magic(f.gs), m_tiles, n_tiles,
+                    pl.tiles, pl.head, pl.sps, f.gated, f.e};
     switch (f.bits) {
-        case 2: st = launch_fwd_bits<2>(f.gs, pl, a, s); break;
-        case 3: st = launch_fwd_bits<3>(f.gs, pl, a, s); break;
-        case 4: st = launch_fwd_bits<4>(f.gs, pl, a, s); break;
-        default: st = launch_fwd_bits<8>(f.gs, pl, a, s); break;
+        case 2: return launch_fwd_bits<2>(f.gs, pl, a, s);
+        case 3: return launch_fwd_bits<3>(f.gs, pl, a, s);
+        case 4: return launch_fwd_bits<4>(f.gs, pl, a, s);
+        default: return launch_fwd_bits<8>(f.gs, pl, a, s);
     }
-    if (st != WQ_OK || pl.splits == 1) return st;
-    return block_finish(f.e, f.gated, part, pl.splits, f.M, s);
 }
 
 wq_status block_finish(const wq::Epilogue& e, bool gated, const float* part, int splits, int M, hipStream_t s) {
