@@ -446,27 +446,22 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
 }
 
 // The same for tiles cut in ranges (with act-order, for every tile): block b
-// takes 16 rows of a tail tile, the ranges' partial products are added in
-// order.
+// takes 4 rows of a tail tile, four columns per thread; the ranges' partial
+// products are added in order.
 template <int BM>
 __global__ void __launch_bounds__(256) block_dx_tail_kernel(const DxArgs p, int splits,
                                                             const int32_t* __restrict__ perm) {
-    const int tail = p.tiles - p.head, i = blockIdx.x / (BM / 16), r0 = (blockIdx.x % (BM / 16)) * 16;
+    const int tail = p.tiles - p.head, i = blockIdx.x / (BM / 4);
     int m_t, k_t;
     tile_place(p.head + i, p.m_tiles, p.k_tiles, m_t, k_t);
-    const size_t step = size_t(tail) * (BM * 256);
-    for (int q = threadIdx.x; q < 16 * 64; q += 256) {
-        const int rr = r0 + q / 64, lc = (q & 63) * 4, row = m_t * BM + rr, col = k_t * 256 + lc;
-        if (row >= p.M || col >= p.K) continue;
-        const float* src = p.part + (size_t(i) * BM + rr) * 256 + lc;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < splits; ++s) {
-            const f4 w = *reinterpret_cast<const f4*>(src + s * step);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += w[e];
-        }
-        finish_dx(p.add, p.dx, perm, size_t(row) * p.K, col, v);
-    }
+    const int rr = (blockIdx.x % (BM / 4)) * 4 + threadIdx.x / 64, lc = (threadIdx.x & 63) * 4;
+    const int row = m_t * BM + rr, col = k_t * 256 + lc;
+    if (row >= p.M || col >= p.K) return;
+    const int at[1] = {lc};
+    f4 w[1];
+    sum_ranges(p.part + (size_t(i) * BM + rr) * 256, at, size_t(tail) * (BM * 256), splits, w);
+    float v[4] = {w[0][0], w[0][1], w[0][2], w[0][3]};
+    finish_dx(p.add, p.dx, perm, size_t(row) * p.K, col, v);
 }
 
 // dx of an empty sum: dx_add, or zero.
@@ -494,7 +489,7 @@ wq_status launch_dx(const wqh::TilePlan& pl, const int32_t* perm, const DxArgs& 
     hipLaunchKernelGGL(kern, dim3(pl.blocks()), dim3(256), lds, s, a);
     const wq_status st = wqh::launch_status();
     if (st != WQ_OK || pl.tail() == 0) return st;
-    hipLaunchKernelGGL((block_dx_tail_kernel<BM>), dim3(unsigned(pl.tail()) * (BM / 16)), dim3(256), 0, s, a, pl.splits,
+    hipLaunchKernelGGL((block_dx_tail_kernel<BM>), dim3(unsigned(pl.tail()) * (BM / 4)), dim3(256), 0, s, a, pl.splits,
                        perm);
     return wqh::launch_status();
 }

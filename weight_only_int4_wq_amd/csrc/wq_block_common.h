@@ -300,6 +300,32 @@ __device__ __forceinline__ void finish(const Epilogue& e, int row, int col, floa
     store_h<V>(e.y + at, a);
 }
 
+// Sums over `splits` partial products, `step` floats apart, of four
+// neighbouring columns per entry of `at` (multiples of 4), in order; up to four
+// products' loads are in flight at once.
+template <int P>
+__device__ __forceinline__ void sum_ranges(const float* __restrict__ src, const int (&at)[P], size_t step, int splits,
+                                           f4 (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = f4{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](auto n) {
+        f4 w[decltype(n)::value][P];
+#pragma unroll
+        for (int s = 0; s < decltype(n)::value; ++s)
+#pragma unroll
+            for (int i = 0; i < P; ++i) w[s][i] = *reinterpret_cast<const f4*>(src + s * step + at[i]);
+#pragma unroll
+        for (int s = 0; s < decltype(n)::value; ++s)
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] += w[s][i];
+        src += decltype(n)::value * step;
+    };
+    int s = splits;
+    for (; s >= 4; s -= 4) add(std::integral_constant<int, 4>{});
+    if (s >= 2) add(std::integral_constant<int, 2>{});
+    if (s & 1) add(std::integral_constant<int, 1>{});
+}
+
 }  // namespace wq
 
 namespace wqh {

@@ -77,6 +77,7 @@ struct FwdShape {
 // first and 128 + 32 w + c the second weight row of lane c of wavefront w: the
 // gate's and the up projection's of output 32 w + c, or columns 64 w + 2 c and
 // 64 w + 2 c + 1.
+// get(at, v): four neighbouring columns of the tile row, per entry of `at`.
 template <class Get>
 __device__ __forceinline__ void finish_piece(const Epilogue& e, bool gated, bool wide, int row, int o0, int oc,
                                              const Get& get) {
@@ -84,10 +85,13 @@ __device__ __forceinline__ void finish_piece(const Epilogue& e, bool gated, bool
     if (col >= e.out) return;
     float a[8], u[8];
     if (gated) {
+        const int at[4] = {oc, oc + 4, 128 + oc, 132 + oc};
+        f4 v[4];
+        get(at, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            a[i] = get(oc + i);
-            u[i] = get(128 + oc + i);
+            a[i] = v[i / 4][i % 4];
+            u[i] = v[2 + i / 4][i % 4];
         }
         if (wide) {
             finish<true, 8>(e, row, col, a, u);
@@ -99,9 +103,12 @@ __device__ __forceinline__ void finish_piece(const Epilogue& e, bool gated, bool
             }
         }
     } else {
+        const int at[2] = {oc / 2, 128 + oc / 2};
+        f4 v[2];
+        get(at, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            a[i] = get(128 * (i & 1) + oc / 2 + (i >> 1));
+            a[i] = v[i & 1][i >> 1];
             u[i] = 0.f;
         }
         if (wide) {
@@ -353,7 +360,12 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
         for (int q = tid; q < Sh::PASS * per_row; q += 256) {
             const int rr = q / per_row, oc = (q % per_row) * 8;
             const int row = m0 + ps * Sh::PASS + rr;
-            if (row < p.M) finish_piece(p.e, gated, wide, row, o0, oc, [&](int i) { return tile[rr * BN + i]; });
+            if (row < p.M)
+                finish_piece(p.e, gated, wide, row, o0, oc, [&](const auto& at, auto& v) {
+#pragma unroll
+                    for (unsigned i = 0; i < sizeof(at) / sizeof(at[0]); ++i)
+                        v[i] = *reinterpret_cast<const f4*>(&tile[rr * BN + at[i]]);
+                });
         }
     };
     pass(std::integral_constant<int, 0>{});
@@ -364,26 +376,23 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
     }
 }
 
-// The same for tiles cut in ranges: block b takes 16 rows of a tail tile, the
-// ranges' partial products are added in order.
+// The same for tiles cut in ranges: one piece of a tail tile per thread, the
+// ranges' partial products added in order.  Bound by reading them: 67 MB in
+// 16 us, two ranges of 2048 x 4096.
 template <int BM>
 __global__ void __launch_bounds__(256) block_tail_kernel(const FwdArgs p, int splits) {
-    const int tail = p.tiles - p.head, i = blockIdx.x / (BM / 16), r0 = (blockIdx.x % (BM / 16)) * 16;
+    const bool gated = p.gated != 0, wide = p.e.out % 8 == 0;
+    const int oc_tile = gated ? 128 : 256, per_row = oc_tile / 8, rows = 256 / per_row;
+    const int tail = p.tiles - p.head, per_tile = BM / rows, i = blockIdx.x / per_tile;
     int m_t, n_t;
     tile_place(p.head + i, p.m_tiles, p.n_tiles, m_t, n_t);
-    const bool gated = p.gated != 0, wide = p.e.out % 8 == 0;
-    const int oc_tile = gated ? 128 : 256, per_row = oc_tile / 8;
-    const size_t step = size_t(tail) * (BM * 256);
-    for (int q = threadIdx.x; q < 16 * per_row; q += 256) {
-        const int rr = r0 + q / per_row, oc = (q % per_row) * 8, row = m_t * BM + rr;
-        if (row >= p.M) continue;
-        const float* src = p.part + (size_t(i) * BM + rr) * 256;
-        finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](int at) {
-            float v = 0.f;
-            for (int s = 0; s < splits; ++s) v += src[s * step + at];
-            return v;
-        });
-    }
+    const int rr = (blockIdx.x % per_tile) * rows + threadIdx.x / per_row, oc = (threadIdx.x % per_row) * 8;
+    const int row = m_t * BM + rr;
+    if (row >= p.M) return;
+    const float* src = p.part + (size_t(i) * BM + rr) * 256;
+    finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](const auto& at, auto& v) {
+        sum_ranges(src, at, size_t(tail) * (BM * 256), splits, v);
+    });
 }
 
 // Epilogue of a split product: V outputs of one row per thread, the ranges'
@@ -429,7 +438,8 @@ wq_status launch_fwd(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((block_fwd_kernel<BITS, FAST, BM>), dim3(pl.blocks()), dim3(256), 0, s, a);
     const wq_status st = wqh::launch_status();
     if (st != WQ_OK || pl.tail() == 0) return st;
-    hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(unsigned(pl.tail()) * (BM / 16)), dim3(256), 0, s, a, pl.splits);
+    const unsigned per_tile = BM / (a.gated ? 16 : 8);
+    hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(unsigned(pl.tail()) * per_tile), dim3(256), 0, s, a, pl.splits);
     return wqh::launch_status();
 }
 
