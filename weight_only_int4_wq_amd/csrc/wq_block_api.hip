@@ -5,7 +5,7 @@
 namespace wqh {
 wq_status check_linear_args(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, const uint16_t* y,
                             int M, int N, int K, int bits, int group_size, int* gs_out);
-size_t block_bwd_workspace_bytes(int M, int R, int K, bool has_perm);
+size_t block_bwd_workspace_bytes(int M, int R, int K, int bits, bool has_perm);
 wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool gated, const uint32_t* packed,
                     const uint16_t* scales, const uint8_t* zeros, const int32_t* perm, const uint16_t* add,
                     uint16_t* dx, uint16_t* dz, float* dbias, int M, int N, int K, int bits, int gs, void* workspace,
@@ -147,9 +147,9 @@ extern "C" size_t wq_gated_workspace_size(int32_t M, int32_t I, int32_t K, int32
 
 extern "C" size_t wq_linear_act_backward_workspace_size(int32_t M, int32_t N, int32_t K, int32_t bits,
                                                         int32_t has_perm) {
-    return query_ok(M, N, K, bits) ? wqh::block_bwd_workspace_bytes(M, N, K, has_perm != 0) : 0;
+    return query_ok(M, N, K, bits) ? wqh::block_bwd_workspace_bytes(M, N, K, bits, has_perm != 0) : 0;
 }
 
 extern "C" size_t wq_gated_backward_workspace_size(int32_t M, int32_t I, int32_t K, int32_t bits, int32_t has_perm) {
-    return query_ok(M, 2LL * I, K, bits) ? wqh::block_bwd_workspace_bytes(M, 2 * I, K, has_perm != 0) : 0;
+    return query_ok(M, 2LL * I, K, bits) ? wqh::block_bwd_workspace_bytes(M, 2 * I, K, bits, has_perm != 0) : 0;
 }

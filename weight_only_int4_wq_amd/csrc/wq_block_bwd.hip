@@ -472,11 +472,15 @@ __global__ void __launch_bounds__(256) block_dx_empty_kernel(size_t n4, const ui
     }
 }
 
-constexpr wqh::TileCost kDxCosts[3] = {
-    {64, 0.80, 0.28, 6.0, false}, {128, 1.09, 0.27, 6.5, false}, {256, 1.37, 0.30, 9.9, false}};
+// [3 bits]: codes that straddle bytes take longer to decode, taller tiles
+// decode them fewer times.
+constexpr wqh::TileCosts kDxCosts[2] = {
+    {{{64, 0.55, 0.36, 8.01, false}, {128, 1.09, 0.14, 6.7, false}, {256, 1.44, 0.48, 6.29, false}}, 0.17, 0.314},
+    {{{64, 1.35, 0.29, 0.02, false}, {128, 2.24, 0.17, 0.0, false}, {256, 2.75, 0.0, 0.0, false}}, 7.27, 0.259}};
 
-wqh::TilePlan dx_plan(int M, int R, int K, bool has_perm, size_t part_bytes) {
-    return wqh::plan_tiles(M, (K + 255) / 256, (R + 63) / 64, kDxCosts, 1, part_bytes, wqh::gemm_slots(1), has_perm);
+wqh::TilePlan dx_plan(int M, int R, int K, int bits, bool has_perm, size_t part_bytes) {
+    return wqh::plan_tiles(M, (K + 255) / 256, (R + 63) / 64, kDxCosts[bits == 3], 1, part_bytes, wqh::gemm_slots(1),
+                           has_perm);
 }
 
 template <int BITS, int BM, bool G8>
@@ -517,11 +521,11 @@ struct BwdBytes {
     size_t dz, dbias, dx;  // dx: partial products, act-order's among them
 };
 
-BwdBytes bwd_bytes(int M, int R, int K, bool has_perm) {
+BwdBytes bwd_bytes(int M, int R, int K, int bits, bool has_perm) {
     BwdBytes b{};
     b.dz = round256(size_t(M) * ((size_t(R) + 7) / 8 * 8) * 2);
     b.dbias = round256(size_t(dbias_ranges(M, R)) * R * 4);
-    b.dx = dx_plan(M, R, K, has_perm, ~size_t(0)).part_bytes();
+    b.dx = dx_plan(M, R, K, bits, has_perm, ~size_t(0)).part_bytes();
     return b;
 }
 
@@ -529,9 +533,9 @@ BwdBytes bwd_bytes(int M, int R, int K, bool has_perm) {
 
 namespace wqh {
 
-size_t block_bwd_workspace_bytes(int M, int R, int K, bool has_perm) {
+size_t block_bwd_workspace_bytes(int M, int R, int K, int bits, bool has_perm) {
     if (M <= 0 || R <= 0) return 0;
-    const BwdBytes b = bwd_bytes(M, R, K, has_perm);
+    const BwdBytes b = bwd_bytes(M, R, K, bits, has_perm);
     return b.dz + b.dbias + b.dx;
 }
 
@@ -577,7 +581,7 @@ wq_status block_bwd(const uint16_t* dy, const uint16_t* preact, int act, bool ga
         dzp = nullptr;
     }
     if (ranges > 1 && !(dbp = reinterpret_cast<float*>(take(size_t(ranges) * R * 4)))) return WQ_ERR_ARG;
-    const TilePlan pl = dx_plan(M, R, K, perm != nullptr, left);
+    const TilePlan pl = dx_plan(M, R, K, bits, perm != nullptr, left);
     if (pl.tiles == 0) return WQ_ERR_ARG;  // act-order's partial products do not fit
 
     // ---- dz, dbias

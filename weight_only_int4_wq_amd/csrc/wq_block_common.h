@@ -339,6 +339,12 @@ struct TileCost {
     double idle, load, fixed;
     bool overlap;
 };
+// A tile kernel's heights, and what cutting tiles adds: `cut` us for the second
+// kernel and `cut_mb` for each MB (10^6 bytes) of partial products.
+struct TileCosts {
+    TileCost height[3];
+    double cut, cut_mb;
+};
 // How a tile kernel covers its tiles: tiles 0 .. head - 1 whole, the others cut
 // into `splits` ranges of `sps` stages, whose fp32 partial products meet in a
 // second kernel.
@@ -354,15 +360,16 @@ struct TilePlan {
 // would hold may be cut (or everything, when there is less than a round).  A
 // cut writes and re-reads its partial products and launches a second kernel.
 // Ranges are multiples of `align` stages, at least four.  The costs are fitted
-// to 1458 timings of the two tile kernels (M = 33 .. 2048, five layers from
-// 1024 x 2048 to 28672 x 8192, all heights and 1 .. 32 ranges), over which the
-// choice among uniform cuts is within 2 % of the best on average and 20 % at
-// worst.  all_part: every product goes through the second kernel.
-inline TilePlan plan_tiles(int M, int n_tiles, int stages, const TileCost (&costs)[3], int align, size_t part_bytes,
+// to 6723 timings of the two tile kernels (M = 33 .. 2048, five layers from
+// 1024 x 2048 to 4096 x 11008, three widths and group sizes, all heights, 1 ..
+// 32 ranges, with and without whole rounds): over each kernel's timings the
+// choice is 0.3 .. 2.2 % slower than the fastest on average, 17 % at worst.
+// all_part: every product goes through the second kernel.
+inline TilePlan plan_tiles(int M, int n_tiles, int stages, const TileCosts& costs, int align, size_t part_bytes,
                            int units, bool all_part) {
     TilePlan best;
     double best_us = 1e300;
-    for (const TileCost& c : costs) {
+    for (const TileCost& c : costs.height) {
         const long long tiles_ll = (long long)((M + c.BM - 1) / c.BM) * n_tiles;
         if (tiles_ll > (1LL << 30)) continue;
         const int tiles = int(tiles_ll);
@@ -386,7 +393,7 @@ inline TilePlan plan_tiles(int M, int n_tiles, int stages, const TileCost (&cost
                 if (p.tail() > 0 && bytes > double(part_bytes)) continue;
                 if (S > 1 && sps < 4) continue;
                 double us = run_us(p.head, stages) + run_us(double(p.tail()) * S, sps);
-                if (p.tail() > 0) us += 2.1 + 2.0 * bytes / 5.1e6;
+                if (p.tail() > 0) us += costs.cut + costs.cut_mb * bytes * 1e-6;
                 if (us < best_us) {
                     best_us = us;
                     best = p;
@@ -410,7 +417,7 @@ struct BlockFwd {
 };
 
 // Bytes of fp32 partial sums the product would like.
-size_t block_fwd_part_bytes(int M, int rows, int K, bool gated);
+size_t block_fwd_part_bytes(int M, int rows, int K, bool gated);  // for any group size
 wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
 // Small M (decode batches).

@@ -424,14 +424,21 @@ __global__ void __launch_bounds__(256) block_finish_kernel(const Epilogue e, con
     }
 }
 
-constexpr wqh::TileCost kFwdCosts[3] = {
-    {64, 0.65, 0.27, 9.7, true}, {128, 0.59, 0.69, 10.1, false}, {256, 1.20, 0.33, 18.7, false}};
+// [FAST].  (Not FAST, a lane fetches a scale and zero-point from LDS for every
+// stage, so that fewer, taller tiles pay earlier.)
+constexpr wqh::TileCosts kFwdCosts[2] = {
+    {{{64, 1.034, 0.619, 0.0, false}, {128, 1.094, 0.483, 1.255, false}, {256, 1.643, 0.529, 2.812, false}},
+     8.568, 0.212},
+    {{{64, 0.428, 0.42, 10.497, true}, {128, 0.65, 0.589, 9.933, false}, {256, 1.243, 0.337, 14.647, false}},
+     0.418, 0.328}};
 
-wqh::TilePlan fwd_plan(int M, int rows, int K, bool gated, size_t part_bytes) {
+wqh::TilePlan fwd_plan(int M, int rows, int K, bool gated, bool fast, size_t part_bytes) {
     const int n_tiles = gated ? (rows / 2 + 127) / 128 : (rows + 255) / 256;
     // ranges of whole windows of weights and scales (four stages)
-    return wqh::plan_tiles(M, n_tiles, (K + 63) / 64, kFwdCosts, 4, part_bytes, wqh::gemm_slots(1), false);
+    return wqh::plan_tiles(M, n_tiles, (K + 63) / 64, kFwdCosts[fast], 4, part_bytes, wqh::gemm_slots(1), false);
 }
+
+bool fast_groups(int gs) { return gs % 128 == 0; }
 
 template <int BITS, bool FAST, int BM>
 wq_status launch_fwd(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
@@ -454,7 +461,7 @@ wq_status launch_fwd_bm(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s
 
 template <int BITS>
 wq_status launch_fwd_bits(int gs, const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
-    return gs % 128 == 0 ? launch_fwd_bm<BITS, true>(pl, a, s) : launch_fwd_bm<BITS, false>(pl, a, s);
+    return fast_groups(gs) ? launch_fwd_bm<BITS, true>(pl, a, s) : launch_fwd_bm<BITS, false>(pl, a, s);
 }
 
 }  // namespace
@@ -462,12 +469,12 @@ wq_status launch_fwd_bits(int gs, const wqh::TilePlan& pl, const FwdArgs& a, hip
 namespace wqh {
 
 size_t block_fwd_part_bytes(int M, int rows, int K, bool gated) {
-    const TilePlan p = fwd_plan(M, rows, K, gated, ~size_t(0));
-    return p.part_bytes();
+    return std::max(fwd_plan(M, rows, K, gated, false, ~size_t(0)).part_bytes(),
+                    fwd_plan(M, rows, K, gated, true, ~size_t(0)).part_bytes());
 }
 
 wq_status block_fwd(const BlockFwd& f, float* part, size_t part_bytes, hipStream_t s) {
-    const TilePlan pl = fwd_plan(f.M, f.rows, f.K, f.gated, part ? part_bytes : 0);
+    const TilePlan pl = fwd_plan(f.M, f.rows, f.K, f.gated, fast_groups(f.gs), part ? part_bytes : 0);
     const int oc = f.gated ? 128 : 256;
     const int m_tiles = (f.M + pl.BM - 1) / pl.BM, n_tiles = (f.e.out + oc - 1) / oc;
     const FwdArgs a{f.x, f.packed, f.scales, f.zeros, part, f.M, f.rows, f.K, group_magic(f.gs), m_tiles, n_tiles,
