@@ -564,3 +564,99 @@ def test_preact_must_not_be_the_output():
                                 p(L["args"][1].data_ptr()), p(L["args"][2].data_ptr()), None, None, None, 0,
                                 p(y.data_ptr()), p(y.data_ptr()), 4, 64, 64, 4, 32, None, 0, None)
     assert st == wq.WQ_ERR_ARG
+
+
+@pytest.mark.parametrize("M,K", [(1, 32), (5, 96), (20, 160), (40, 96), (200, 32)])
+@pytest.mark.parametrize("bits,N", [(8, 48), (8, 47), (4, 48)])
+def test_codes_past_k_stay_out(M, K, bits, N):
+    """Where K ends inside a kernel's step, the words behind a row are the next
+    row's.  Every other row holds codes whose distance from the zero-point
+    overflows fp16 with the scale of the row before it: that row's outputs
+    stay finite and right.  (Zero times infinity would be NaN.)"""
+    G, top, zero = K // 32, (1 << bits) - 1, 1 << (bits - 1)
+    codes = np.full((N, K), zero, dtype=np.uint8)
+    codes[0::2] += np.arange(K, dtype=np.uint8) % 2      # weights 0 and s
+    codes[1::2] = top                                    # (top - zero) s > 65504
+    s = np.float16(65504 / (top - zero) * 1.01)
+    scales = np.full((N, G), s, dtype=np.float16)
+    assert float(s) * (top - zero) > 65520  # rounds to infinity
+    x = (randn(161, M, K, sigma=1.0) / 4096).contiguous()
+    y = wq.linear_act(x, torch.from_numpy(O.pack(codes, bits).view(np.int32)).cuda(), torch.from_numpy(scales).cuda(),
+                      torch.full((N, G), zero, dtype=torch.uint8, device="cuda"), bits, 32)
+    w = torch.from_numpy((codes[0::2].astype(np.float64) - zero) * float(s)).cuda()
+    check_linear(dict(w=w), x, None, None, "none", y[:, 0::2].contiguous(), None, "even rows")
+
+
+# tiles beyond one per compute unit: whole rounds of whole tiles, and a last
+# round cut along the sum
+@pytest.mark.parametrize("op,M,N,K,bits,gs,ao", [
+    ("linear", 300, 36002, 3200, 4, 32, False),      # 2 x 141 tiles of 256 rows, 26 of them cut
+    ("linear", 1100, 17800, 3200, 4, 128, False),    # 5 x 70, 94 of them cut
+    ("gated", 1100, 8001, 2080, 8, 32, True),
+    ("linear_backward", 1100, 2085, 14400, 4, 64, False),
+    ("linear_backward", 300, 2500, 36032, 3, 32, False),
+    ("linear_backward", 300, 3200, 25600, 4, 128, False),  # 3 x 100 of 128 rows, 44 of them cut
+    ("gated_backward", 1100, 1043, 14400, 4, 32, True)])
+def test_rounds_of_whole_and_cut_tiles(op, M, N, K, bits, gs, ao):
+    """Large products whose tiles fill the machine more than once, sampled
+    columns against 64 bits, and the same call without a workspace to cut any
+    tile: equal but for the order of the sums."""
+    gated, back = op.startswith("gated"), op.endswith("backward")
+    rows = 2 * N if gated else N
+    L = make_layer(171, rows, K, bits, gs, False, ao)
+    pick = torch.arange(0, M, 37, device="cuda")
+    if not back:
+        x = randn(172, M, K)
+        least = (M * K * 2 + 255) // 256 * 256 if ao else 1
+        small = torch.empty(least, dtype=torch.uint8, device="cuda")
+        for ws in (None, small):
+            if gated:
+                h, z = wq.gated(x, *L["args"], perm=L["perm"], save_preact=True, workspace=ws)
+                check_gated(L, x[pick], None, "silu", h[pick], z[pick], op)
+            else:
+                y, z = wq.linear_act(x, *L["args"], perm=L["perm"], act="gelu", save_preact=True, workspace=ws)
+                check_linear(L, x[pick], None, None, "gelu", y[pick], z[pick], op)
+        return
+    dy = randn(173, M, N)
+    z = randn(174, M, rows) if gated else None
+    f = wq.gated_backward if gated else wq.linear_act_backward
+    ld = (rows + 7) // 8 * 8
+    least = (M * ld * 2 + 255) // 256 * 256 + (-(-M // 64) * -(-K // 256) * 64 * 1024 if ao else 0)
+    small = torch.empty(least, dtype=torch.uint8, device="cuda")
+    for ws in (None, small):
+        dx, dz, _ = f(dy, z, *L["args"], perm=L["perm"], workspace=ws)
+        check_backward("gated" if gated else "linear", L, dy[pick], None if z is None else z[pick],
+                       "silu" if gated else "none", None, dx[pick], dz[pick] if gated else dy[pick], None, op)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 32])
+@pytest.mark.parametrize("N,K,gs,bits", [(48, 4128, 32, 4), (47, 4096, 128, 4), (4100, 8192, 32, 3), (33, 65536, 32, 4),
+                                         (130, 2080, 32, 8)])
+def test_decode_batches_however_scales_lie(M, N, K, gs, bits):
+    """Scales that start off 16 bytes, that do not fill whole 16 bytes, or too
+    many of them to stay in LDS take another way to the decode kernel, with
+    the same sums: bit for bit."""
+    for f, rows in ((wq.linear_act, N), (wq.gated, 2 * N)):
+        L = make_layer(181, rows, K, bits, gs)
+        p, s, z = L["args"][:3]
+        x = randn(182, M, K)
+        y = f(x, p, s, z, bits, gs)
+        if f is wq.gated:
+            check_gated(L, x, None, "silu", y, None, "decode")
+        else:
+            check_linear(L, x, None, None, "none", y, None, "decode")
+        ws = torch.empty(s.numel() + 1, dtype=s.dtype, device="cuda")
+        wz = torch.empty(z.numel() + 1, dtype=z.dtype, device="cuda")
+        s2, z2 = ws[1:].view_as(s).copy_(s), wz[1:].view_as(z).copy_(z)
+        assert torch.equal(f(x, p, s2, z2, bits, gs), y)
+
+
+def test_decode_without_workspace():
+    """A decode batch whose K has to be split falls back where there is no room
+    for the partial sums."""
+    M, N, K = 20, 64, 8192
+    L = make_layer(191, N, K, 4, 128)
+    x = randn(192, M, K)
+    assert wq.block_workspace_size("linear_act", M, N, K, 4, False) > 0
+    y = wq.linear_act(x, *L["args"], workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
+    check_linear(L, x, None, None, "none", y, None, "no room")

@@ -159,18 +159,21 @@ __global__ void __launch_bounds__(64 * W) block_small_kernel(const SmallArgs p) 
                                 dst + uint32_t(k) * 1024u);
         }
     };
-    // a row's units past K are the next row's: finite codes that meet zeros of x
+    // a row's units past K are the next row's codes: their scale is zero, so
+    // that they stay finite, and they meet zeros of x
     const uint32_t w_off0 = w_row * row_bytes + w_unit * UNIT;
     const uint32_t w_off1 = (w_row + 8u) * row_bytes + (w_unit ^ 4u) * UNIT;  // (r / 2) % 8 of rows 8 on
     auto issue = [&]() {
         const uint32_t dst = lds_address(slot);
         const uint32_t step = uint32_t(s0 + is);
-        uint32_t at[HALVES];
+        uint32_t at[HALVES], at2[HALVES];
         if constexpr (!WIDE) {
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-                at[h] = uint32_t(li) * uint32_t(G) +
-                        uint32_t(chunk_group(min(int(step) * STEP + 4 * h + lg, chunks - 1), p.gd));
+            for (int h = 0; h < HALVES; ++h) {
+                const int ch = int(step) * STEP + 4 * h + lg;
+                at[h] = uint32_t(li) * uint32_t(G) + uint32_t(chunk_group(min(ch, chunks - 1), p.gd));
+                at2[h] = ch < chunks ? at[h] * 2u : kNowhere;
+            }
         }
 #pragma unroll
         for (int j = 0; j < T; ++j) {
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(64 * W) block_small_kernel(const SmallArgs p) 
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
                     const uint32_t sd = d + Sh::WCOPIES * 1024u + h * 512u;
-                    copy_to_lds<2>(ssrc[j], at[h] * 2u, sd);
+                    copy_to_lds<2>(ssrc[j], at2[h], sd);
                     copy_to_lds<1>(zsrc[j], at[h], sd + 256u);
                 }
             }
@@ -255,8 +258,10 @@ __global__ void __launch_bounds__(64 * W) block_small_kernel(const SmallArgs p) 
                 }
                 if constexpr (WIDE) {
                     const uint8_t* mt = meta + (parity * T + j) * meta_tile;
-                    const int g = chunk_group(min((s0 + hs / HALVES) * STEP + int(ch), chunks - 1), p.gd);
-                    ss[j][h] = reinterpret_cast<const uint16_t*>(mt)[li * G + g];
+                    const int kc = (s0 + hs / HALVES) * STEP + int(ch);
+                    const int g = chunk_group(min(kc, chunks - 1), p.gd);
+                    const uint32_t sc = reinterpret_cast<const uint16_t*>(mt)[li * G + g];
+                    ss[j][h] = kc < chunks ? sc : 0u;
                     zz[j][h] = mt[s_pieces * 1024 + li * G + g];
                 } else {
                     const uint32_t* sp = reinterpret_cast<const uint32_t*>(t + Sh::WCOPIES * 1024 + h * 512);
