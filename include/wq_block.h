@@ -26,6 +26,8 @@
  *    they are;
  *  - with act-order (perm != NULL) x and dx are in original channel order,
  *    as for wq_linear.  perm must be a permutation of 0 .. K-1;
+ *  - outputs share no memory with inputs or each other (WQ_ERR_ARG), except
+ *    that y may be residual and dx may be dx_add, whole;
  *  - sums run in a fixed order: the same call gives the same bits, whatever
  *    the workspace holds.  A call with less optional workspace, or with
  *    another M, may add in another order;
@@ -59,7 +61,7 @@ typedef enum {
  * preact = fp16(z) for the backward pass.
  * x fp16 [M][K]; bias fp16 [N] (nullable); residual fp16 [M][N] (nullable,
  * may be y itself: an update in place); y fp16 [M][N]; preact fp16 [M][N]
- * (nullable, not y).  act: a wq_act.  M >= 0, N >= 0 (0: nothing is done).
+ * (nullable).  act: a wq_act.  M >= 0, N >= 0 (0: nothing is done).
  * The workspace part that cannot be left out: act-order's gathered
  * activations, M*K*2 bytes rounded up to 256; the rest holds fp32 partial
  * sums of a K split (without it K is not split across blocks).
@@ -89,7 +91,7 @@ size_t wq_gated_workspace_size(int32_t M, int32_t I, int32_t K, int32_t bits, in
  *   dx = fp16(dz . W + dx_add),    dbias[n] = sum over m of dy * act'(preact).
  * preact fp16 [M][N], required unless act is WQ_ACT_NONE; dx_add fp16 [M][K]
  * (nullable, may be dx itself); dx fp16 [M][K]; dz fp16 [M][N] (nullable: the
- * gradient that adapters on this layer take; not dy, not preact); dbias fp32
+ * gradient that adapters on this layer take); dbias fp32
  * [N] (nullable; fp32 because a sum over thousands of rows leaves fp16's
  * range).  The residual's gradient is dy.  dz enters the product in fp16, as
  * the matrix cores take it.  With M = 0 dbias is zero; with N = 0 dx is

@@ -190,3 +190,22 @@ def test_gated_mlp_checks_its_layers():
         wq.QuantizedGatedMLP(mk(128, 64), mk(64, 128))
     with pytest.raises(ValueError, match="act"):
         wq.QuantizedGatedMLP(mk(256, 64), mk(64, 128), act="swish")
+
+
+@fake_pointers
+def test_overlapping_arrays_are_refused():
+    """Outputs on top of inputs, whole or in part: 4 rows of 128 channels in,
+    64 out."""
+    at = lambda b: ctypes.c_void_p(0x100000 + b)  # noqa: E731
+    x, y, z, far = at(0), at(0x10000), at(0x20000), at(0x40000)
+    for name, rows in (("wq_linear_act", 64), ("wq_gated", 128)):
+        for bad in (dict(y=x), dict(y=at(4 * 128 * 2 - 16)), dict(preact=y), dict(preact=at(0x10000 + 4 * 64 * 2 - 16)),
+                    dict(preact=at(0x10000 - 4 * rows * 2 + 16)), dict(preact=x)):
+            assert forward(name, **{"x": x, "y": y, "preact": z, **bad}) == ARG, bad
+    for bad in (dict(res=z), dict(res=at(0x10000 + 16))):
+        assert forward("wq_linear_act", **{"x": x, "y": y, "preact": z, **bad}) == ARG, bad
+    for name in ("wq_linear_act_backward", "wq_gated_backward"):
+        good = dict(dy=x, preact=y, dx=z, dz=far)
+        for bad in (dict(dx=x), dict(dx=at(4 * 64 * 2 - 16)), dict(dx=y), dict(dz=x), dict(dz=y), dict(dz=z),
+                    dict(add=far), dict(add=at(0x20000 + 16))):
+            assert backward(name, **{**good, **bad}) == ARG, bad

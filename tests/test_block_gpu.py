@@ -660,3 +660,27 @@ def test_decode_without_workspace():
     assert wq.block_workspace_size("linear_act", M, N, K, 4, False) > 0
     y = wq.linear_act(x, *L["args"], workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
     check_linear(L, x, None, None, "none", y, None, "no room")
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_subnormal_weights_and_inputs(M):
+    """fp16's subnormals count: weights below 2^-14 (scales of a few steps of
+    2^-24) times ordinary inputs, and ordinary weights times subnormal
+    inputs, forward and backward."""
+    N, K = 144, 288
+    L = make_layer(201, N, K, 4, 32)
+    p, s, z, bits, gs = L["args"]
+    tiny = (torch.arange(1, s.numel() + 1, device="cuda") % 37 + 1).view_as(s) * 2.0 ** -24
+    q = torch.from_numpy(O.unpack(p.cpu().numpy().view(np.uint32), 4, K)).cuda().double()
+    w = ((q - z.double().repeat_interleave(32, 1)) * tiny.double().repeat_interleave(32, 1)).half().double()
+    x, dy = randn(202, M, K, sigma=1000.0), randn(203, M, N, sigma=1000.0)
+    T = dict(w=w)
+    y = wq.linear_act(x, p, tiny.half(), z, bits, gs)
+    assert y.abs().max() > 2.0 ** -10
+    check_linear(T, x, None, None, "none", y, None, "tiny weights")
+    dx, dz, _ = wq.linear_act_backward(dy, None, p, tiny.half(), z, bits, gs)
+    check_backward("linear", T, dy, None, "none", None, dx, dy, None, "tiny weights")
+    x, dy = randn(204, M, K, sigma=2.0 ** -18), randn(205, M, N, sigma=2.0 ** -18)
+    check_linear(L, x, None, None, "none", wq.linear_act(x, *L["args"]), None, "tiny inputs")
+    dx, dz, _ = wq.linear_act_backward(dy, None, *L["args"])
+    check_backward("linear", L, dy, None, "none", None, dx, dy, None, "tiny inputs")

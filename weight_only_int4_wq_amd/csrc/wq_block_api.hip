@@ -30,6 +30,12 @@ bool query_ok(int M, long long rows, int K, int bits) {
     return sizes_ok(M, rows, K) && M > 0 && rows > 0 && wqh::bits_ok(bits);
 }
 
+// Whether two fp16 arrays share memory.
+bool overlap(const uint16_t* a, size_t na, const uint16_t* b, size_t nb) {
+    const uintptr_t ia = reinterpret_cast<uintptr_t>(a), ib = reinterpret_cast<uintptr_t>(b);
+    return a && b && ia < ib + 2 * nb && ib < ia + 2 * na;
+}
+
 size_t fwd_workspace(int M, int rows, int K, int bits, bool has_perm, bool gated) {
     const size_t part = M <= wqh::kBlockSmallM ? wqh::block_small_part_bytes(M, rows, K, bits, gated)
                                                : wqh::block_fwd_part_bytes(M, rows, K, gated);
@@ -50,7 +56,10 @@ wq_status forward(const uint16_t* x, const uint32_t* packed, const uint16_t* sca
                           static_cast<const void*>(workspace)})
         if (!wqh::aligned16(p)) return WQ_ERR_ARG;
     if (M == 0 || N == 0) return WQ_OK;
-    if (preact == y) return WQ_ERR_ARG;
+    const size_t nx = size_t(M) * K, ny = size_t(M) * N, nz = size_t(M) * rows;
+    if (overlap(y, ny, x, nx) || overlap(preact, nz, x, nx) || overlap(preact, nz, y, ny) ||
+        overlap(preact, nz, residual, ny) || (residual != y && overlap(residual, ny, y, ny)))
+        return WQ_ERR_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     size_t left = workspace ? workspace_bytes : 0;
@@ -93,7 +102,11 @@ wq_status backward(const uint16_t* dy, const uint16_t* preact, int act, const ui
     if (M > 0 && !dx) return WQ_ERR_ARG;
     if (M > 0 && N > 0) {
         if (!dy || !packed || !scales || (needs_z && !preact)) return WQ_ERR_ARG;
-        if (dz && (dz == dy || dz == preact || dz == dx)) return WQ_ERR_ARG;
+        const size_t nx = size_t(M) * K, ny = size_t(M) * N, nz = gated ? 2 * ny : ny;
+        const uint16_t* z = needs_z ? preact : nullptr;
+        if (overlap(dx, nx, dy, ny) || overlap(dx, nx, z, nz) || overlap(dz, nz, dy, ny) || overlap(dz, nz, z, nz) ||
+            overlap(dz, nz, dx, nx) || overlap(dz, nz, dx_add, nx) || (dx_add != dx && overlap(dx_add, nx, dx, nx)))
+            return WQ_ERR_ARG;
     }
     return wqh::block_bwd(dy, preact, act, gated, packed, scales, zeros, perm, dx_add, dx, dz, dbias, M, N, K, bits, gs,
                           workspace, workspace_bytes, static_cast<hipStream_t>(stream));

@@ -483,6 +483,7 @@ size_t block_fwd_part_bytes(int M, int rows, int K, bool gated) {
 
 wq_status block_fwd(const BlockFwd& f, float* part, size_t part_bytes, hipStream_t s) {
     const TilePlan pl = fwd_plan(f.M, f.rows, f.K, f.gated, fast_groups(f.gs), part ? part_bytes : 0);
+    if (pl.tiles == 0) return WQ_ERR_ARG;  // more tiles than a grid holds
     const int oc = f.gated ? 128 : 256;
     const int m_tiles = (f.M + pl.BM - 1) / pl.BM, n_tiles = (f.e.out + oc - 1) / oc;
     const FwdArgs a{f.x, f.packed, f.scales, f.zeros, part, f.M, f.rows, f.K, group_magic(f.gs), m_tiles, n_tiles,
