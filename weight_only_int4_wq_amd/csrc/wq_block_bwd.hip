@@ -16,15 +16,22 @@
 // weight rows a stage) decodes each stage once, a quarter per wavefront, into
 // LDS in the order the fragments are read (1 KB per fragment, no bank
 // conflicts either way), and its 2 x 2 wavefronts, BM/2 x 128 outputs each,
-// read it from there.  Decoding costs BM/128 * 1/16 of the vector work per
-// matrix instruction that a wavefront decoding its own columns would spend.
+// read it from there: every weight is decoded once per block, not once per
+// wavefront that multiplies it.
 // The columns are dealt to fragments so that a lane ends up with 4
 // consecutive outputs of a row: one 8-byte store (16 bytes of partial sums).
 //
 // Stages overlap in one loop with one barrier: while stage s is multiplied
 // from its LDS buffers, stage s + 1 is decoded into the others and stage
 // s + 2 is loaded into registers; scales and zero-points (64 rows x the
-// tile's groups) pass through LDS one stage earlier.
+// tile's groups) pass through LDS one stage earlier.  Tiles that would fill a
+// last round only partly are cut along the weight rows.
+//
+// Measured: dz [2048 x 4096] . W [4096 x 11008] at 4 bits 197 us (938
+// TFLOP/s), of which the cut tiles' sums take 10; [2048 x 22016] . [22016 x
+// 4096] 355 us (1040 TFLOP/s).  Bound by the matrix units at the clock that
+// power leaves them (busy 51 % of the counted cycles) and by the LDS writes of
+// the decoded weights, which hold a wavefront up by 25 cycles each.
 #include <algorithm>
 
 #include "wq_block_common.h"
@@ -49,7 +56,9 @@ constexpr int kDzRowLanes = 4;  // rows a block works on at once
 // A block takes 64 V-wide column groups and rows_per rows, four at a time;
 // dbias's sums stay in registers, cross the four row lanes through LDS and
 // leave as one partial row per block row.  V = 8 needs N to be a multiple of
-// 8.  Bound by memory: each of dy, preact and dz is touched once.
+// 8.  Bound by memory: each of dy, preact and dz is touched once (gated, 2048
+// x 11008, 225 MB in 46 us).  Columns that are not 8-byte groups take V = 1,
+// bound by the activation's arithmetic (311 x 5001, gelu, 8.6 us).
 template <bool GATED, int V>
 __global__ void __launch_bounds__(64 * kDzRowLanes) block_dz_kernel(const DzArgs p) {
     constexpr int P = GATED ? 2 : 1;
@@ -122,7 +131,15 @@ __global__ void __launch_bounds__(256) block_dbias_kernel(const float* __restric
     const int i = blockIdx.x * 256 + threadIdx.x;
     if (i >= R) return;
     float v = 0.f;
-    for (int r = 0; r < ranges; ++r) v += part[size_t(r) * R + i];
+    int r = 0;
+    for (; r + 8 <= ranges; r += 8) {  // (eight loads in flight)
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = part[size_t(r + k) * R + i];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += w[k];
+    }
+    for (; r < ranges; ++r) v += part[size_t(r) * R + i];
     out[i] = v;
 }
 

@@ -228,25 +228,31 @@ __device__ __forceinline__ float act_value(float v, int kind) {
     }
 }
 
-// act(v) and act'(v), v held within +-100 for the derivative (it is 0 or 1
-// there to fp32's accuracy).
+// act(v) and act'(v).  v is held within +-100 for the derivative (it is 0 or 1
+// there to fp32's accuracy, and so is the factor that both share).
 __device__ __forceinline__ float act_slope(float v, int kind, float& value) {
-    value = act_value(v, kind);
-    const float c = v < -100.f ? -100.f : v > 100.f ? 100.f : v;
+    const float low = v < -100.f ? -100.f : v, c = low > 100.f ? 100.f : low;
     switch (kind) {
-        case WQ_ACT_RELU: return v > 0.f ? 1.f : v != v ? v : 0.f;
-        case WQ_ACT_GELU:
-            return __builtin_fmaf(c * kInvSqrt2Pi, __expf(-0.5f * c * c), 0.5f * erfcf(-kSqrtHalf * c));
+        case WQ_ACT_RELU:
+            value = v < 0.f ? 0.f : v;
+            return v > 0.f ? 1.f : v != v ? v : 0.f;
+        case WQ_ACT_GELU: {
+            const float t = 0.5f * erfcf(-kSqrtHalf * c);
+            value = low * t;
+            return __builtin_fmaf(c * kInvSqrt2Pi, __expf(-0.5f * c * c), t);
+        }
         case WQ_ACT_GELU_TANH: {
             const float t = sigmoid(2.f * kTanhScale * __builtin_fmaf(kTanhCubic * c * c, c, c));
             const float du = 2.f * kTanhScale * __builtin_fmaf(3.f * kTanhCubic * c, c, 1.f);
+            value = low * t;
             return __builtin_fmaf(c * t * (1.f - t), du, t);
         }
         case WQ_ACT_SILU: {
             const float t = sigmoid(c);
+            value = low * t;
             return t * __builtin_fmaf(c, 1.f - t, 1.f);
         }
-        default: return 1.f;
+        default: value = v; return 1.f;
     }
 }
 
