@@ -22,10 +22,10 @@
 //  - Activations: three LDS buffers of BM x 64; stage s + 2 is on its way
 //    while stage s is multiplied.
 //  - All of it is copied from memory straight into LDS, and each stage ends
-//    with one wait that leaves the newest stage's copies in flight.  (With
-//    loads through registers the same loop took 553 us at 4096 x 8192 x 8192,
-//    4 bits; 428 us with its loads taken out and 374 us with nothing but its
-//    matrix instructions: the loads' latency was the loss.)
+//    with one wait that leaves the newest stage's copies in flight.  (4096 x
+//    8192 x 8192 at 4 bits: 535 us; with loads through registers 553, of
+//    which 428 are left without any loads and 374 with nothing but the matrix
+//    instructions.)
 //  - Epilogue: accumulators cross LDS in passes of 64 rows, so that bias,
 //    activation, product, residual and every store work on 8 neighbouring
 //    columns (16-byte accesses).
