@@ -27,7 +27,7 @@
 // tile's groups) pass through LDS one stage earlier.  Tiles that would fill a
 // last round only partly are cut along the weight rows.
 //
-// Measured: dz [2048 x 4096] . W [4096 x 11008] at 4 bits 197 us (938
+// Measured: dz [2048 x 4096] . W [4096 x 11008] at 4 bits 200 us (923
 // TFLOP/s), of which the cut tiles' sums take 10; [2048 x 22016] . [22016 x
 // 4096] 355 us (1040 TFLOP/s).  Bound by the matrix units at the clock that
 // power leaves them (busy 51 % of the counted cycles) and by the LDS writes of
