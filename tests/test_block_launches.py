@@ -1,0 +1,148 @@
+"""What the feed-forward block's entry points ask of the HIP runtime, on the
+CPU: a small library that records kernel attributes and launches, and runs
+nothing, stands in for the runtime's functions.  The calls pass made-up device
+addresses, which nothing follows."""
+
+import json
+import os
+import shutil
+import subprocess
+import sys
+import textwrap
+
+import pytest
+
+import weight_only_int4_wq_amd as wq
+
+torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+pytestmark = [
+    pytest.mark.skipif(torch.cuda.device_count() > 0, reason="passes made-up device addresses"),
+    pytest.mark.skipif(shutil.which("gcc") is None, reason="no C compiler"),
+]
+
+RECORDER = r"""
+#include <stddef.h>
+#include <stdint.h>
+typedef struct { uint32_t x, y, z; } dim;
+typedef struct { const void *fn; uint32_t gx, gy, gz, bx, by, bz; uint64_t lds; } launch;
+typedef struct { const void *fn; int attr, value; } attribute;
+static launch launches[256];
+static attribute attributes[256];
+static int n_launches, n_attributes;
+static struct { dim g, b; size_t lds; void *s; } next;
+int __hipPushCallConfiguration(dim g, dim b, size_t lds, void *s) {
+    next.g = g; next.b = b; next.lds = lds; next.s = s;
+    return 0;
+}
+int __hipPopCallConfiguration(dim *g, dim *b, size_t *lds, void **s) {
+    *g = next.g; *b = next.b; *lds = next.lds; *s = next.s;
+    return 0;
+}
+int hipLaunchKernel(const void *fn, dim g, dim b, void **args, size_t lds, void *s) {
+    if (n_launches < 256) launches[n_launches++] = (launch){fn, g.x, g.y, g.z, b.x, b.y, b.z, lds};
+    return 0;
+}
+int hipFuncSetAttribute(const void *fn, int attr, int value) {
+    if (n_attributes < 256) attributes[n_attributes++] = (attribute){fn, attr, value};
+    return 0;
+}
+int hipGetLastError(void) { return 0; }
+int recorded_launches(const launch **p) { *p = launches; return n_launches; }
+int recorded_attributes(const attribute **p) { *p = attributes; return n_attributes; }
+void recorded_clear(void) { n_launches = n_attributes = 0; }
+"""
+
+# Runs in a process of its own, where the recorder is loaded before the HIP
+# runtime: `calls` is a list of (entry, arguments by name); prints what each
+# returned and recorded.
+RUNNER = r"""
+import ctypes, json, sys
+rec = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+sys.path.insert(0, sys.argv[2])
+import weight_only_int4_wq_amd as wq
+class Launch(ctypes.Structure):
+    _fields_ = [("fn", ctypes.c_void_p)] + [(n, ctypes.c_uint32) for n in ("gx", "gy", "gz", "bx", "by", "bz")] + \
+        [("lds", ctypes.c_uint64)]
+class Attribute(ctypes.Structure):
+    _fields_ = [("fn", ctypes.c_void_p), ("attr", ctypes.c_int), ("value", ctypes.c_int)]
+def recorded(kind, struct):
+    p = ctypes.POINTER(struct)()
+    n = getattr(rec, "recorded_" + kind)(ctypes.byref(p))
+    return [{f: getattr(p[i], f) for f, _ in struct._fields_} for i in range(n)]
+ORDER = {
+    "wq_linear_act": "x packed scales zeros perm bias residual act y preact M N K bits gs ws wsb",
+    "wq_gated": "x packed scales zeros perm bias act y preact M N K bits gs ws wsb",
+    "wq_linear_act_backward": "dy preact act packed scales zeros perm add dx dz dbias M N K bits gs ws wsb",
+    "wq_gated_backward": "dy preact act packed scales zeros perm add dx dz dbias M N K bits gs ws wsb",
+}
+out = []
+for entry, given in json.loads(sys.stdin.read()):
+    rec.recorded_clear()
+    a = dict.fromkeys("x packed scales zeros perm bias residual y preact dy add dx dz dbias ws".split())
+    a.update(act=0, M=1, N=64, K=128, bits=4, gs=32, wsb=0)
+    a.update(given)
+    need = getattr(wq.lib(), entry + "_workspace_size")(a["M"], a["N"], a["K"], a["bits"], int(a["perm"] is not None))
+    if a["wsb"] == "queried":
+        a["wsb"] = need
+    status = getattr(wq.lib(), entry)(*[a[n] for n in ORDER[entry].split()], None)
+    out.append({"status": status, "workspace": need, "launches": recorded("launches", Launch),
+                "attributes": recorded("attributes", Attribute)})
+print(json.dumps(out))
+"""
+
+
+@pytest.fixture(scope="module")
+def run(tmp_path_factory):
+    """run([(entry, arguments), ...]) -> what each call returned and recorded."""
+    wq.lib()
+    where = tmp_path_factory.mktemp("recorder")
+    (where / "recorder.c").write_text(RECORDER)
+    lib = str(where / "librecorder.so")
+    r = subprocess.run(["gcc", "-std=c99", "-O1", "-shared", "-fPIC", str(where / "recorder.c"), "-o", lib],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    (where / "runner.py").write_text(textwrap.dedent(RUNNER))
+
+    def go(calls):
+        r = subprocess.run([sys.executable, str(where / "runner.py"), lib, ROOT], input=json.dumps(calls),
+                           capture_output=True, text=True, timeout=100)
+        assert r.returncode == 0, r.stderr[-2000:]
+        return json.loads(r.stdout.splitlines()[-1])
+
+    return go
+
+
+def at(n):
+    """Array n's made-up address, 1 TiB from the others."""
+    return (n + 1) << 40
+
+
+FORWARD = dict(x=at(0), packed=at(1), scales=at(2), y=at(3), ws=at(4), wsb="queried")
+BACKWARD = dict(dy=at(0), packed=at(1), scales=at(2), dx=at(3), ws=at(4), wsb="queried")
+
+
+def test_kernel_attributes_do_not_depend_on_the_call(run):
+    """A kernel's shared-memory limit belongs to the process: calls from two
+    threads that set it to what each of them needs could lower it under each
+    other's launch.  Every call that sets a kernel's limit sets the same, and
+    none launches more than that."""
+    got = run([(entry, {**args, "M": M, "N": N, "K": K, "bits": bits, "gs": gs, **more})
+               for entry, args, more in (("wq_linear_act", FORWARD, {}), ("wq_gated", FORWARD, {}),
+                                         ("wq_linear_act_backward", BACKWARD, {}))
+               for M in (1, 8, 20, 100) for N in (4096, 4128) for K in (1024, 2048, 4096, 8192) for bits in (4, 8)
+               for gs in (32, 128, -1)])
+    limits, most = {}, {}
+    for call in got:
+        assert call["status"] == 0
+        for a in call["attributes"]:
+            limits.setdefault((a["fn"], a["attr"]), set()).add(a["value"])
+        for k in call["launches"]:
+            most[k["fn"]] = max(most.get(k["fn"], 0), k["lds"])
+    assert limits
+    changing = {k: sorted(v) for k, v in limits.items() if len(v) > 1}
+    assert not changing, changing
+    for (fn, _), v in limits.items():
+        assert most.get(fn, 0) <= max(v)

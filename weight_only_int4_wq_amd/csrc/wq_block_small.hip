@@ -417,8 +417,10 @@ wq_status launch_small(const SmallPlan& pl, const SmallArgs& a, hipStream_t s) {
     const int lds = fixed + (WIDE ? 2 * T * pl.meta_tile : 0);
     if (lds > kSmallLds) return launch_small<BITS, false, MF, H, W, GATED>(pl, a, s);
     auto kern = block_small_kernel<BITS, WIDE, MF, H, W, GATED>;
-    const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    // (the limit is the process's, not the call's: one value for every call, or
+    // a thread with a smaller layer could lower it under another's launch)
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
     if (e != hipSuccess) return wqh::hip_status(e);
     hipLaunchKernelGGL(kern, dim3(pl.blocks, pl.splits), dim3(64 * W), lds, s, a);
     return wqh::launch_status();
