@@ -26,8 +26,8 @@
  *    they are;
  *  - with act-order (perm != NULL) x and dx are in original channel order,
  *    as for wq_linear.  perm must be a permutation of 0 .. K-1;
- *  - outputs share no memory with inputs or each other (WQ_ERR_ARG), except
- *    that y may be residual and dx may be dx_add, whole;
+ *  - outputs and the workspace share no memory with inputs or each other
+ *    (WQ_ERR_ARG), except that y may be residual and dx may be dx_add, whole;
  *  - sums run in a fixed order: the same call gives the same bits, whatever
  *    the workspace holds.  A call with less optional workspace, or with
  *    another M, may add in another order;

@@ -146,3 +146,63 @@ def test_kernel_attributes_do_not_depend_on_the_call(run):
     assert not changing, changing
     for (fn, _), v in limits.items():
         assert most.get(fn, 0) <= max(v)
+
+
+# ------------------------------------------------------ overlapping arrays --
+
+M, N, K, GS = 4, 64, 128, 32
+
+
+def sizes(gated):
+    """Bytes of each array of 4 rows, 128 channels in, 64 out."""
+    rows = 2 * N if gated else N
+    g = K // GS
+    return dict(x=M * K * 2, packed=rows * K // 2, scales=rows * g * 2, zeros=rows * g, perm=K * 4, bias=rows * 2,
+                residual=M * N * 2, y=M * N * 2, preact=M * rows * 2, dy=M * N * 2, add=M * K * 2, dx=M * K * 2,
+                dz=M * rows * 2, dbias=rows * 4, ws=1 << 20)
+
+
+ENTRIES = {
+    "wq_linear_act": ("y preact ws", "x packed scales zeros perm bias residual"),
+    "wq_gated": ("y preact ws", "x packed scales zeros perm bias"),
+    "wq_linear_act_backward": ("dx dz dbias ws", "dy preact packed scales zeros perm add"),
+    "wq_gated_backward": ("dx dz dbias ws", "dy preact packed scales zeros perm add"),
+}
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_what_is_written_lies_apart(run, entry):
+    """Every array that a call writes, the workspace among them, against every
+    other array: one on top of the other, its last 16 bytes in the other and
+    its first 16 in the other are refused before anything is launched; right
+    behind the other and right before it is fine."""
+    written, read = (s.split() for s in ENTRIES[entry])
+    n = sizes(entry.startswith("wq_gated"))
+    apart = {a: at(i) for i, a in enumerate(written + read)}
+    apart.update(wsb=n["ws"], M=M, N=N, K=K, gs=GS, act=1)
+    names, bad, good = [], [], []
+    for i, w in enumerate(written):
+        for other in written[i + 1:] + read:
+            base = apart[other]
+            for where in (base, base + n[other] - 16, base - n[w] + 16):
+                names.append((w, other, where - base))
+                bad.append((entry, {**apart, w: where}))
+            good += [(entry, {**apart, w: base + n[other]}), (entry, {**apart, w: base - n[w]})]
+    whole = {("y", "residual", 0), ("dx", "add", 0)}       # updates in place
+    got = run(bad)
+    for name, call, r in zip(names, bad, got):
+        if name in whole:
+            assert r["status"] == 0 and r["launches"], name
+        else:
+            assert r["status"] == 1 and not r["launches"], (name, call, r)
+    for call, r in zip(good, run(good)):
+        assert r["status"] == 0 and r["launches"], (call, r)
+
+
+def test_empty_sums_lie_apart_too(run):
+    """No weight rows: dx is dx_add, copied; half on top of it would be read
+    after it was written."""
+    size = M * K * 2
+    for where, status in ((0, 0), (size, 0), (size - 16, 1), (16 - size, 1)):
+        r, = run([("wq_linear_act_backward", dict(M=M, N=0, K=K, gs=GS, dx=at(0) + where, add=at(0)))])
+        assert r["status"] == status, where

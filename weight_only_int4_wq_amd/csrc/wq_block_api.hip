@@ -1,5 +1,7 @@
 // Entry points of wq_block.h: argument checks, workspace sizes, and the
 // choice between the decode-batch and the tiled forward kernels.
+#include <initializer_list>
+
 #include "wq_block_common.h"
 
 namespace wqh {
@@ -30,11 +32,33 @@ bool query_ok(int M, long long rows, int K, int bits) {
     return sizes_ok(M, rows, K) && M > 0 && rows > 0 && wqh::bits_ok(bits);
 }
 
-// Whether two fp16 arrays share memory.
-bool overlap(const uint16_t* a, size_t na, const uint16_t* b, size_t nb) {
-    const uintptr_t ia = reinterpret_cast<uintptr_t>(a), ib = reinterpret_cast<uintptr_t>(b);
-    return a && b && ia < ib + 2 * nb && ib < ia + 2 * na;
+// An array of the caller's, empty when it is null.
+struct Bytes {
+    uintptr_t at;
+    size_t n;
+    Bytes(const void* p, size_t bytes) : at(reinterpret_cast<uintptr_t>(p)), n(p ? bytes : 0) {}
+    bool overlaps(const Bytes& o) const { return n && o.n && (at <= o.at ? o.at - at < n : at - o.at < o.n); }
+};
+
+// Whether something that a call writes shares memory with something that it
+// reads or with something else that it writes.
+bool clash(std::initializer_list<Bytes> written, std::initializer_list<Bytes> read) {
+    for (auto w = written.begin(); w != written.end(); ++w) {
+        for (const Bytes& r : read)
+            if (w->overlaps(r)) return true;
+        for (auto o = w + 1; o != written.end(); ++o)
+            if (w->overlaps(*o)) return true;
+    }
+    return false;
 }
+
+// Bytes of a layer's codes, scales and zero-points.
+struct WeightBytes {
+    size_t codes, scales, zeros;
+    WeightBytes(int rows, int K, int bits, int gs)
+        : codes(size_t(rows) * (K / 32) * bits * 4), scales(size_t(rows) * (K / gs) * 2),
+          zeros(size_t(rows) * (K / gs)) {}
+};
 
 size_t fwd_workspace(int M, int rows, int K, int bits, bool has_perm, bool gated) {
     const size_t part = M <= wqh::kBlockSmallM ? wqh::block_small_part_bytes(M, rows, K, bits, gated)
@@ -56,9 +80,11 @@ wq_status forward(const uint16_t* x, const uint32_t* packed, const uint16_t* sca
                           static_cast<const void*>(workspace)})
         if (!wqh::aligned16(p)) return WQ_ERR_ARG;
     if (M == 0 || N == 0) return WQ_OK;
-    const size_t nx = size_t(M) * K, ny = size_t(M) * N, nz = size_t(M) * rows;
-    if (overlap(y, ny, x, nx) || overlap(preact, nz, x, nx) || overlap(preact, nz, y, ny) ||
-        overlap(preact, nz, residual, ny) || (residual != y && overlap(residual, ny, y, ny)))
+    const size_t ny = size_t(M) * N * 2;
+    const WeightBytes wb(rows, K, bits, gs);
+    if (clash({{y, ny}, {preact, size_t(M) * rows * 2}, {workspace, workspace_bytes}},
+              {{x, size_t(M) * K * 2}, {packed, wb.codes}, {scales, wb.scales}, {zeros, wb.zeros},
+               {perm, size_t(K) * 4}, {bias, size_t(rows) * 2}, {residual == y ? nullptr : residual, ny}}))
         return WQ_ERR_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
@@ -100,12 +126,14 @@ wq_status backward(const uint16_t* dy, const uint16_t* preact, int act, const ui
         if (!wqh::aligned16(p)) return WQ_ERR_ARG;
     const bool needs_z = gated || act != WQ_ACT_NONE;
     if (M > 0 && !dx) return WQ_ERR_ARG;
-    if (M > 0 && N > 0) {
-        if (!dy || !packed || !scales || (needs_z && !preact)) return WQ_ERR_ARG;
-        const size_t nx = size_t(M) * K, ny = size_t(M) * N, nz = gated ? 2 * ny : ny;
-        const uint16_t* z = needs_z ? preact : nullptr;
-        if (overlap(dx, nx, dy, ny) || overlap(dx, nx, z, nz) || overlap(dz, nz, dy, ny) || overlap(dz, nz, z, nz) ||
-            overlap(dz, nz, dx, nx) || overlap(dz, nz, dx_add, nx) || (dx_add != dx && overlap(dx_add, nx, dx, nx)))
+    if (M > 0) {
+        if (N > 0 && (!dy || !packed || !scales || (needs_z && !preact))) return WQ_ERR_ARG;
+        const int rows = gated ? 2 * N : N;
+        const size_t nx = size_t(M) * K * 2, nz = size_t(M) * rows * 2;
+        const WeightBytes wb(rows, K, bits, gs);
+        if (clash({{dx, nx}, {dz, nz}, {dbias, size_t(rows) * 4}, {workspace, workspace_bytes}},
+                  {{dy, size_t(M) * N * 2}, {needs_z ? preact : nullptr, nz}, {packed, wb.codes}, {scales, wb.scales},
+                   {zeros, wb.zeros}, {perm, size_t(K) * 4}, {dx_add == dx ? nullptr : dx_add, nx}}))
             return WQ_ERR_ARG;
     }
     return wqh::block_bwd(dy, preact, act, gated, packed, scales, zeros, perm, dx_add, dx, dz, dbias, M, N, K, bits, gs,
