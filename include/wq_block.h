@@ -18,8 +18,9 @@
  *
  * Conventions beyond wq.h's:
  *  - every array is 16-byte aligned, except scales and zeros;
- *  - K and the number of weight rows are at most 2^22, M at most 2^30
- *    (WQ_ERR_ARG past that);
+ *  - K and the number of weight rows are at most 2^22, M at most 2^30, and
+ *    the outputs fewer than 2^24 tiles of 256 rows by 256 weight rows
+ *    (backward: by 256 channels) (WQ_ERR_ARG past that);
  *  - zero-points are below 2^bits (8-bit: any byte);
  *  - rows are independent: row m of an output depends on row m of the inputs
  *    only, so rows that hold padding, infinities or NaN leave the others as

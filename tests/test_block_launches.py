@@ -206,3 +206,35 @@ def test_empty_sums_lie_apart_too(run):
     for where, status in ((0, 0), (size, 0), (size - 16, 1), (16 - size, 1)):
         r, = run([("wq_linear_act_backward", dict(M=M, N=0, K=K, gs=GS, dx=at(0) + where, add=at(0)))])
         assert r["status"] == status, where
+
+
+# --------------------------------------------------------------- launches --
+
+def test_launches_stay_within_the_runtimes_limits(run):
+    """Fewer than 2^32 threads in x and 2^16 blocks in y, up to the largest
+    sizes: what a launch past them leaves undone, earlier kernels have begun."""
+    big = [(1 << 20, 8, 16384), (1 << 21, 16, 16384), ((1 << 30) - 5, 16, 32), (1 << 30, 1, 32), (1 << 26, 1030, 64),
+           (70000, 32768, 64), (33, 1 << 21, 4096), (257, 2048, 1 << 22), (1, 1 << 21, 1 << 22), (32, 1 << 21, 32)]
+    calls = [(entry, {**(BACKWARD if entry.endswith("backward") else FORWARD), **more, "M": m, "N": n, "K": k,
+                      "perm": at(7) if perm else None})
+             for entry in ENTRIES for m, n, k in big for perm in (False, True)
+             for more in ([dict(act=1, preact=at(8), dbias=at(9)), dict(act=1, preact=at(8))]
+                          if entry.endswith("backward") else [{}])]
+    far = {a: (i + 1) << 56 for i, a in enumerate("x dy packed scales y dx ws perm preact dbias".split())}
+    calls = [(e, {k: far[k] if k in far and v is not None else v for k, v in a.items()}) for e, a in calls]
+    for call, r in zip(calls, run(calls)):
+        assert r["status"] == 0 and r["launches"], call
+        for k in r["launches"]:
+            assert 0 < k["gx"] * k["bx"] < 1 << 32 and 0 < k["gy"] < 1 << 16 and k["gz"] == 1, (call, k)
+
+
+def test_what_no_launch_covers_is_refused_first(run):
+    """More tiles than a launch holds: refused before the first kernel."""
+    calls = [("wq_linear_act", {**FORWARD, "perm": (9 << 56), "M": 1 << 30, "N": 1 << 22, "K": 32}),
+             ("wq_gated", {**FORWARD, "perm": (9 << 56), "M": 1 << 30, "N": 1 << 21, "K": 32}),
+             ("wq_linear_act_backward", {**BACKWARD, "act": 1, "preact": 9 << 56, "M": 1 << 30, "N": 8, "K": 1 << 22})]
+    far = {a: (i + 1) << 56 for i, a in enumerate("x dy packed scales y dx".split())}
+    for e, a in calls:
+        a.update({k: v for k, v in far.items() if k in a}, ws=8 << 56, wsb=1 << 52)
+    for call, r in zip(calls, run(calls)):
+        assert r["status"] == 1 and not r["launches"], (call, r["status"], len(r["launches"]))

@@ -86,6 +86,7 @@ wq_status forward(const uint16_t* x, const uint32_t* packed, const uint16_t* sca
               {{x, size_t(M) * K * 2}, {packed, wb.codes}, {scales, wb.scales}, {zeros, wb.zeros},
                {perm, size_t(K) * 4}, {bias, size_t(rows) * 2}, {residual == y ? nullptr : residual, ny}}))
         return WQ_ERR_ARG;
+    if (!wqh::block_fwd_fits(M, N, gated)) return WQ_ERR_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     size_t left = workspace ? workspace_bytes : 0;

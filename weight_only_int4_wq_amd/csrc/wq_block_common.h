@@ -336,6 +336,9 @@ __device__ __forceinline__ void sum_ranges(const float* __restrict__ src, const 
 
 namespace wqh {
 
+// A launch holds fewer than 2^32 threads in x: blocks of 256 threads.
+constexpr long long kMaxBlocks = (1LL << 24) - 1;
+
 // Time of a tile kernel's block, in us on MI355X: `idle` + `load` * (share of
 // the compute units that work) per 64-deep stage, plus `fixed` per tile (the
 // clock falls as more units feed their matrix cores).  `overlap`: two blocks
@@ -370,14 +373,15 @@ struct TilePlan {
 // 1024 x 2048 to 4096 x 11008, three widths and group sizes, all heights, 1 ..
 // 32 ranges, with and without whole rounds): over each kernel's timings the
 // choice is 0.3 .. 2.2 % slower than the fastest on average, 17 % at worst.
-// all_part: every product goes through the second kernel.
+// all_part: every product goes through the second kernel.  No tiles: what
+// has to be cut does not fit part_bytes, or no height fits a launch.
 inline TilePlan plan_tiles(int M, int n_tiles, int stages, const TileCosts& costs, int align, size_t part_bytes,
                            int units, bool all_part) {
     TilePlan best;
     double best_us = 1e300;
     for (const TileCost& c : costs.height) {
         const long long tiles_ll = (long long)((M + c.BM - 1) / c.BM) * n_tiles;
-        if (tiles_ll > (1LL << 30)) continue;
+        if (tiles_ll > kMaxBlocks) continue;
         const int tiles = int(tiles_ll);
         auto round_us = [&](int st, double share) { return st * (c.idle + c.load * share) + c.fixed; };
         // `blocks` of st stages in rounds
@@ -395,6 +399,7 @@ inline TilePlan plan_tiles(int M, int n_tiles, int stages, const TileCosts& cost
                 const int sps = ((stages + S - 1) / S + align - 1) / align * align;
                 if ((stages + sps - 1) / sps != S || (S == 1 && pass == 1)) continue;
                 TilePlan p{c.BM, S, sps, tiles, S == 1 && !all_part ? tiles : head};
+                if (p.head + (long long)p.tail() * S > kMaxBlocks) continue;
                 const double bytes = double(p.part_bytes());
                 if (p.tail() > 0 && bytes > double(part_bytes)) continue;
                 if (S > 1 && sps < 4) continue;
@@ -424,6 +429,7 @@ struct BlockFwd {
 
 // Bytes of fp32 partial sums the product would like.
 size_t block_fwd_part_bytes(int M, int rows, int K, bool gated);  // for any group size
+bool block_fwd_fits(int M, int out, bool gated);                  // whether a launch covers the tiles
 wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
 // Small M (decode batches).

@@ -384,23 +384,29 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
     }
 }
 
-// The same for tiles cut in ranges: one piece of a tail tile per thread, the
+// The same for tiles cut in ranges: one piece of a tail tile per thread (of
+// more than one tile where there are more pieces than a launch holds), the
 // ranges' partial products added in order.  Bound by reading them: 67 MB in
 // 16 us, two ranges of 2048 x 4096.
 template <int BM>
 __global__ void __launch_bounds__(256) block_tail_kernel(const FwdArgs p, int splits) {
     const bool gated = p.gated != 0, wide = p.e.out % 8 == 0;
     const int oc_tile = gated ? 128 : 256, per_row = oc_tile / 8, rows = 256 / per_row;
-    const int tail = p.tiles - p.head, per_tile = BM / rows, i = blockIdx.x / per_tile;
-    int m_t, n_t;
-    tile_place(p.head + i, p.m_tiles, p.n_tiles, m_t, n_t);
-    const int rr = (blockIdx.x % per_tile) * rows + threadIdx.x / per_row, oc = (threadIdx.x % per_row) * 8;
-    const int row = m_t * BM + rr;
-    if (row >= p.M) return;
-    const float* src = p.part + (size_t(i) * BM + rr) * 256;
-    finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](const auto& at, auto& v) {
-        sum_ranges(src, at, size_t(tail) * (BM * 256), splits, v);
-    });
+    const int tail = p.tiles - p.head, per_tile = BM / rows;
+    const int rr0 = threadIdx.x / per_row, oc = (threadIdx.x % per_row) * 8;
+#pragma unroll 1
+    for (int b = blockIdx.x; b < tail * per_tile; b += int(gridDim.x)) {
+        const int i = b / per_tile;
+        int m_t, n_t;
+        tile_place(p.head + i, p.m_tiles, p.n_tiles, m_t, n_t);
+        const int rr = (b % per_tile) * rows + rr0;
+        const int row = m_t * BM + rr;
+        if (row >= p.M) continue;
+        const float* src = p.part + (size_t(i) * BM + rr) * 256;
+        finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](const auto& at, auto& v) {
+            sum_ranges(src, at, size_t(tail) * (BM * 256), splits, v);
+        });
+    }
 }
 
 // Epilogue of a split product: V outputs of one row per thread, the ranges'
@@ -454,7 +460,8 @@ wq_status launch_fwd(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
     const wq_status st = wqh::launch_status();
     if (st != WQ_OK || pl.tail() == 0) return st;
     const unsigned per_tile = BM / (a.gated ? 16 : 8);
-    hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(unsigned(pl.tail()) * per_tile), dim3(256), 0, s, a, pl.splits);
+    const unsigned blocks = unsigned(std::min(pl.tail() * (long long)per_tile, wqh::kMaxBlocks));
+    hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(blocks), dim3(256), 0, s, a, pl.splits);
     return wqh::launch_status();
 }
 
@@ -476,6 +483,11 @@ wq_status launch_fwd_bits(int gs, const wqh::TilePlan& pl, const FwdArgs& a, hip
 
 namespace wqh {
 
+bool block_fwd_fits(int M, int out, bool gated) {
+    const int oc = gated ? 128 : 256;
+    return (M + 255LL) / 256 * ((out + oc - 1LL) / oc) <= kMaxBlocks;
+}
+
 size_t block_fwd_part_bytes(int M, int rows, int K, bool gated) {
     return std::max(fwd_plan(M, rows, K, gated, false, ~size_t(0)).part_bytes(),
                     fwd_plan(M, rows, K, gated, true, ~size_t(0)).part_bytes());
@@ -483,7 +495,7 @@ size_t block_fwd_part_bytes(int M, int rows, int K, bool gated) {
 
 wq_status block_fwd(const BlockFwd& f, float* part, size_t part_bytes, hipStream_t s) {
     const TilePlan pl = fwd_plan(f.M, f.rows, f.K, f.gated, fast_groups(f.gs), part ? part_bytes : 0);
-    if (pl.tiles == 0) return WQ_ERR_ARG;  // more tiles than a grid holds
+    if (pl.tiles == 0) return WQ_ERR_ARG;
     const int oc = f.gated ? 128 : 256;
     const int m_tiles = (f.M + pl.BM - 1) / pl.BM, n_tiles = (f.e.out + oc - 1) / oc;
     const FwdArgs a{f.x, f.packed, f.scales, f.zeros, part, f.M, f.rows, f.K, group_magic(f.gs), m_tiles, n_tiles,
