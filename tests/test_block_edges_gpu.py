@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import weight_only_int4_wq_amd as wq  # noqa: E402
-from test_block_gpu import check_backward, make_layer, randn  # noqa: E402
+from test_block_gpu import check_backward, check_gated, check_linear, make_layer, randn  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,14 @@ def test_more_pieces_than_a_launch_holds():
     check_backward("linear", L, dy[rows], None, "none", None, dx[rows], dy[rows], None, "far pieces")
     del dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,K", [(20, 262144 + 4096), (2, 524288 + 4096)])
+def test_decode_batches_of_very_long_rows(M, K):
+    """Rows longer than the decode kernel's ranges hold."""
+    N = 17
+    L = make_layer(311, 2 * N, K, 4, 128)
+    x = randn(312, M, K)
+    y = wq.linear_act(x, *L["args"], act="relu")
+    check_linear(L, x, None, None, "relu", y, None, "long rows")
+    check_gated(L, x, None, "silu", wq.gated(x, *L["args"]), None, "long rows")

@@ -238,3 +238,19 @@ def test_what_no_launch_covers_is_refused_first(run):
         a.update({k: v for k, v in far.items() if k in a}, ws=8 << 56, wsb=1 << 52)
     for call, r in zip(calls, run(calls)):
         assert r["status"] == 1 and not r["launches"], (call, r["status"], len(r["launches"]))
+
+
+@pytest.mark.parametrize("entry", ["wq_linear_act", "wq_gated"])
+def test_decode_batches_of_very_long_rows_are_cut(run, entry):
+    """Rows too long for the decode kernel's 64 ranges take the tile kernel;
+    with exactly the workspace that was asked for it cuts them."""
+    shapes = [(20, 262144 + 4096), (32, 1 << 20), (1, 524288 + 4096), (16, 1 << 22)]
+    got = run([(entry, {**FORWARD, "M": m, "N": 48, "K": k, "gs": 128, "perm": perm}) for m, k in shapes
+               for perm in (None, at(7))])
+    for (m, k), r in zip([s for s in shapes for _ in range(2)], got):
+        assert r["status"] == 0
+        assert max(launch["gx"] for launch in r["launches"][-2:]) >= 8, (m, k, r)
+    # one channel block less and the decode kernel takes them, in 64 ranges
+    for m, k in ((20, 262144), (1, 524288)):
+        r, = run([(entry, {**FORWARD, "M": m, "N": 48, "K": k, "gs": 128})])
+        assert r["status"] == 0 and r["launches"][0]["gy"] == 64

@@ -432,7 +432,8 @@ size_t block_fwd_part_bytes(int M, int rows, int K, bool gated);  // for any gro
 bool block_fwd_fits(int M, int out, bool gated);                  // whether a launch covers the tiles
 wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
-// Small M (decode batches).
+// Small M (decode batches).  K of more than 64 ranges of what a block's
+// registers hold of x is the tile kernel's, and so are its bytes.
 constexpr int kBlockSmallM = 32;
 size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated);
 // WQ_ERR_UNSUPPORTED when K has to be split and `part` has no room for it.

@@ -448,6 +448,7 @@ namespace wqh {
 
 size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated) {
     const SmallPlan p = small_plan(M, rows, K, bits, gated, ~size_t(0));
+    if (!p.ok) return block_fwd_part_bytes(M, rows, K, gated);  // the tile kernel takes the call
     return p.splits > 1 ? size_t(p.splits) * M * rows * 4 : 0;
 }
 
