@@ -360,11 +360,7 @@ __global__ void __launch_bounds__(64 * W) block_small_kernel(const SmallArgs p) 
         if constexpr (S > 1) if (1 < mine) work(std::integral_constant<int, HALVES>{}, par);
         if constexpr (S > 2) if (2 < mine) work(std::integral_constant<int, 2 * HALVES>{}, par);
         if constexpr (S > 3) if (3 < mine) work(std::integral_constant<int, 3 * HALVES>{}, par);
-        if constexpr (S > 4) if (4 < mine) work(std::integral_constant<int, 4 * HALVES>{}, par);
-        if constexpr (S > 5) if (5 < mine) work(std::integral_constant<int, 5 * HALVES>{}, par);
-        if constexpr (S > 6) if (6 < mine) work(std::integral_constant<int, 6 * HALVES>{}, par);
-        if constexpr (S > 7) if (7 < mine) work(std::integral_constant<int, 7 * HALVES>{}, par);
-        static_assert(S <= 8, "steps of a wavefront");
+        static_assert(S <= 4, "steps of a wavefront");
         // (the next tile's scales have landed: an item's wait came after their
         // copies)
         if (WIDE && mine == 0) copies_landed<0>();
