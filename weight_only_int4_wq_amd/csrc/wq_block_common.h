@@ -89,7 +89,8 @@ __device__ __forceinline__ TileWork tile_work(int b, int tiles, int head, int m_
 //    are complete) comes before the barrier that publishes them;
 //  - a kernel that leaves copies in flight across its waits (N > 0) has no
 //    other memory loads there, or waits for them too.
-// m0 (the target's LDS address) holds nothing else in these kernels.
+// m0, the target's LDS address, is an operand: the compiler sets it and keeps
+// its own uses of it apart.
 
 // Buffer resource over `bytes` bytes at p (at most 2 GiB of them): accesses
 // add a 32-bit offset to it, and those past its end read zeros.
@@ -114,13 +115,13 @@ template <int B>
 __device__ __forceinline__ void copy_to_lds(u4 src, uint32_t off, uint32_t lds) {
     const uint32_t l = __builtin_amdgcn_readfirstlane(lds);
     if constexpr (B == 16)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+        asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(l), "v"(off), "s"(src));
     else if constexpr (B == 12)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+        asm volatile("s_nop 0\n\tbuffer_load_dwordx3 %1, %2, 0 offen lds" : : "{m0}"(l), "v"(off), "s"(src));
     else if constexpr (B == 2)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+        asm volatile("s_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds" : : "{m0}"(l), "v"(off), "s"(src));
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" : : "s"(l), "v"(off), "s"(src));
+        asm volatile("s_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" : : "{m0}"(l), "v"(off), "s"(src));
 }
 
 template <int N>
