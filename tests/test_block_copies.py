@@ -2,7 +2,8 @@
 in the code that the compiler generates for gfx950.
 
 The copies are asm statements, of which the compiler knows only what they
-declare."""
+declare, and the forward tile kernel ends a stage with a wait that leaves the
+newest copies in flight."""
 
 import concurrent.futures as cf
 import os
@@ -25,6 +26,11 @@ def code(tmp_path_factory):
         return dict(zip(SOURCES, ex.map(lambda s: _assembly(os.path.join(CSRC, s), where), SOURCES)))
 
 
+def kernels(asm, pattern):
+    for name in re.findall(r"^(_ZN\S*" + pattern + r"\S*):", asm, re.M):
+        yield name, asm.split(name + ":", 1)[1].split(".Lfunc_end", 1)[0]
+
+
 def test_copies_write_only_what_they_declare(code):
     """m0 holds a copy's target: it comes as the statement's operand, so that
     the compiler, which puts values of its own there, knows of it.  A write
@@ -37,3 +43,32 @@ def test_copies_write_only_what_they_declare(code):
             bad = [line for line in lines if re.match(r"\S+\s+m0\b", line)]
             assert not bad, (src, bad)
     assert copies > 1000
+
+
+def test_a_stage_leaves_only_the_newest_rows_in_flight(code):
+    """At the barriers of the forward tile kernel's loop the copies still in
+    flight are those of one stage's rows of x, as many as a wavefront issues:
+    the packed words, scales and zero-points that the next stage reads, and
+    its rows, were copied before them."""
+    seen = 0
+    for name, body in kernels(code["wq_block_fwd.hip"], "16block_fwd_kernel"):
+        seen += 1
+        rows = int(re.search(r"ELi(\d+)EEEv", name).group(1))
+        flight, barriers = [], []
+        for line in body.splitlines():
+            line = line.split(";")[0].strip()
+            if re.match(r"(global|buffer|flat|scratch)_", line):
+                src = re.search(r"s\[\d+:\d+\]", line)
+                flight.append((src and src.group(0), line.endswith(" lds")))
+                continue
+            wait = re.match(r"s_waitcnt\s.*vmcnt\((\d+)\)", line)
+            if wait:
+                flight = flight[max(0, len(flight) - int(wait.group(1))):]
+            elif line.startswith("s_barrier"):
+                barriers.append(list(flight))
+        # the first stage's, the loop's; those behind the loop leave none
+        first, loop, rest = barriers[0], barriers[1], barriers[2:]
+        assert len(first) == len(loop) == rows // 32, (name, first, loop)
+        assert all(f == loop[0] and f[1] for f in first + loop), (name, first, loop)
+        assert rest and not rest[0], (name, rest)
+    assert seen == 24
