@@ -509,7 +509,15 @@ def block_workspace_size(entry: str, M: int, N: int, K: int, bits: int, has_perm
     """Bytes of workspace of `entry` ("linear_act", "gated",
     "linear_act_backward" or "gated_backward"); N counts one projection's
     columns for the gated ones."""
+    _sizes(M, N, K)
     return int(getattr(lib(), f"wq_{entry}_workspace_size")(M, N, K, bits, int(bool(has_perm))))
+
+
+def _sizes(M, rows, K):
+    """The library takes sizes in 32 bits and checks them itself: what those
+    would cut off must not become another size."""
+    if M > 0x7FFFFFFF or rows > 0x7FFFFFFF or K > 0x7FFFFFFF:
+        raise ValueError(f"sizes must be below 2^31, got {M} rows, {rows} weight rows, {K} channels")
 
 
 def _act(act) -> int:
@@ -604,6 +612,7 @@ def _forward(entry, x, packed, scales, zeros, bits, group_size, perm, bias, resi
     M, cols = x.shape
     if cols != K:
         raise ValueError(f"x must have {K} columns, got {cols}")
+    _sizes(M, rows, K)
     code = _act(act)
     if workspace is not None:
         workspace = _workspace_arg(workspace, d)
@@ -658,6 +667,7 @@ def _backward(entry, dy, preact, packed, scales, zeros, bits, group_size, perm, 
     M, cols = dy.shape
     if cols != N:
         raise ValueError(f"dy must have {N} columns, got {cols}")
+    _sizes(M, rows, K)
     code = _act(act)
     if workspace is not None:
         workspace = _workspace_arg(workspace, d)
