@@ -44,3 +44,53 @@ def test_workspace_of_sizes_that_a_32_bit_integer_would_wrap(entry):
     for M, N, K in ((WIDE + 33, 64, 4096), (33, WIDE + 64, 4096), (33, 64, WIDE + 4096)):
         with pytest.raises(ValueError, match="2\\^31"):
             wq.block_workspace_size(entry, M, N, K, 4, True)
+
+
+def needs(t):
+    return t.requires_grad_()
+
+
+@pytest.mark.parametrize("fn", FORWARD + BACKWARD)
+def test_a_lost_gradient_is_said(fn, recwarn):
+    """The functions record nothing for autograd: a tensor that requires a
+    gradient is accepted with a warning, and without one where no graph is
+    recorded.  (The calls end at the check for GPU tensors.)"""
+    rows = 4 if fn in (wq.gated, wq.gated_backward) else 2
+    layer = (meta(rows, 4, dtype=torch.int32), meta(rows, 1), None, 2, -1)
+    if fn in FORWARD:
+        cases = [((needs(meta(3, 64)), *layer), {}), ((meta(3, 64), *layer), dict(bias=needs(meta(rows))))]
+        if fn is wq.linear_act:
+            cases.append(((meta(3, 64), *layer), dict(residual=needs(meta(3, 2)))))
+        plain = (meta(3, 64), *layer)
+    else:
+        z = meta(3, rows)
+        cases = [((needs(meta(3, 2)), z, *layer), {}), ((meta(3, 2), needs(meta(3, rows)), *layer), {}),
+                 ((meta(3, 2), z, *layer), dict(dx_add=needs(meta(3, 64))))]
+        plain = (meta(3, 2), z, *layer)
+    for args, more in cases:
+        more.update(act="silu")
+        with pytest.warns(UserWarning, match="no gradient"), pytest.raises(ValueError, match="GPU tensors"):
+            fn(*args, **more)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU tensors"):
+            fn(*args, **more)
+    with pytest.raises(ValueError, match="GPU tensors"):
+        fn(*plain, act="silu")
+    assert len(recwarn) == 0
+
+
+def test_a_gradient_lost_at_the_awq_scale_is_said():
+    """Where the AWQ scale is applied first, its result would hide that x
+    requires a gradient."""
+    layer = wq.QuantizedLinear(meta(4, 4, dtype=torch.int32), meta(4, 1), None, 2, -1, 64, act_scale=meta(64))
+    for f in (layer.forward_act, wq.QuantizedGatedMLP(layer, wq.QuantizedLinear(
+            meta(5, 2, dtype=torch.int32), meta(5, 1), None, 32, -1, 2))):
+        with pytest.warns(UserWarning, match="no gradient"), pytest.raises(ValueError, match="GPU tensors"):
+            f(needs(meta(3, 64)))
+
+
+def test_wrong_types_are_still_named():
+    layer = (meta(2, 4, dtype=torch.int32), meta(2, 1), None, 2, -1)
+    with pytest.raises(ValueError, match="bias must be a torch tensor"):
+        wq.linear_act(meta(3, 64), *layer, bias=[0.0, 0.0])
+    with pytest.raises(ValueError, match="dx_add must be a torch tensor"):
+        wq.linear_act_backward(meta(3, 2), None, *layer, dx_add=1.0)

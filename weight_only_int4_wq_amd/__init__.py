@@ -520,6 +520,18 @@ def _sizes(M, rows, K):
         raise ValueError(f"sizes must be below 2^31, got {M} rows, {rows} weight rows, {K} channels")
 
 
+def _needs_gradient(t) -> bool:
+    return getattr(t, "requires_grad", False)  # (None and wrong types: checked elsewhere)
+
+
+def _say_detached(name):
+    """These functions record nothing for autograd; where a graph is being
+    recorded, a tensor that requires a gradient gets none through them."""
+    import warnings
+    warnings.warn(f"{name} requires a gradient, but the result carries no gradient: call the matching backward "
+                  "function, from a torch.autograd.Function for instance, or torch.no_grad()", stacklevel=4)
+
+
 def _act(act) -> int:
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
@@ -614,6 +626,8 @@ def _forward(entry, x, packed, scales, zeros, bits, group_size, perm, bias, resi
         raise ValueError(f"x must have {K} columns, got {cols}")
     _sizes(M, rows, K)
     code = _act(act)
+    if torch.is_grad_enabled() and (x.requires_grad or _needs_gradient(bias) or _needs_gradient(residual)):
+        _say_detached("x, bias or residual")
     if workspace is not None:
         workspace = _workspace_arg(workspace, d)
     bias = _opt(bias, half, "bias", (rows,), d)
@@ -640,7 +654,8 @@ def linear_act(x, packed, scales, zeros, bits: int, group_size: int, perm=None, 
     """y fp16 [M][N] = act(x . W^T + bias) + residual, any M, rounded once.
     `out` may be `residual` (update in place).  With save_preact (or a
     `preact` tensor to fill) returns (y, preact), preact = fp16(x . W^T + bias)
-    for linear_act_backward."""
+    for linear_act_backward.  Nothing is recorded for autograd; where that
+    loses a gradient, this and the three functions below warn."""
     return _forward("wq_linear_act", x, packed, scales, zeros, bits, group_size, perm, bias, residual, act, save_preact,
                     out, preact, workspace)
 
@@ -671,6 +686,8 @@ def _backward(entry, dy, preact, packed, scales, zeros, bits, group_size, perm, 
     code = _act(act)
     if workspace is not None:
         workspace = _workspace_arg(workspace, d)
+    if torch.is_grad_enabled() and (dy.requires_grad or _needs_gradient(preact) or _needs_gradient(dx_add)):
+        _say_detached("dy, preact or dx_add")
     needs_z = is_gated or act != "none"
     if needs_z and preact is None:
         raise ValueError("preact is required")
@@ -753,7 +770,11 @@ class QuantizedLinear:
         return fn(x, self.packed, self.scales, self.zeros, self.bits, self.group_size, self.perm, out, workspace)
 
     def _scaled(self, x):
-        return x if self.act_scale is None else scale_act(x, self.act_scale)
+        if self.act_scale is None:
+            return x
+        if _needs_gradient(x) and _torch().is_grad_enabled():
+            _say_detached("x")
+        return scale_act(x, self.act_scale)
 
     def forward_act(self, x, bias=None, residual=None, act: str = "none", save_preact: bool = False, out=None,
                     workspace=None):
