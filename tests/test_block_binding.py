@@ -94,3 +94,36 @@ def test_wrong_types_are_still_named():
         wq.linear_act(meta(3, 64), *layer, bias=[0.0, 0.0])
     with pytest.raises(ValueError, match="dx_add must be a torch tensor"):
         wq.linear_act_backward(meta(3, 2), None, *layer, dx_add=1.0)
+
+
+class OnDevice:
+    """Stands for a tensor on GPU `index`."""
+    requires_grad = False
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_the_awq_scale_runs_on_the_tensors_device(index, monkeypatch):
+    """Like the products themselves: the tensors' device is the current one
+    while the library is called, whichever was current before."""
+    current = [0]
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(wq, "scale_act", lambda x, s: seen.append(current[0]))
+    layer = wq.QuantizedLinear(meta(4, 4, dtype=torch.int32), meta(4, 1), None, 2, -1, 64, act_scale=meta(64))
+    layer._scaled(OnDevice(index))
+    assert seen == [index] and current == [0]

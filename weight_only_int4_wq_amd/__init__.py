@@ -772,8 +772,13 @@ class QuantizedLinear:
     def _scaled(self, x):
         if self.act_scale is None:
             return x
-        if _needs_gradient(x) and _torch().is_grad_enabled():
+        torch = _torch()
+        if _needs_gradient(x) and torch.is_grad_enabled():
             _say_detached("x")
+        d = getattr(x, "device", None)
+        if d is not None and d.type == "cuda" and torch.cuda.current_device() != d.index:
+            with torch.cuda.device(d):
+                return scale_act(x, self.act_scale)
         return scale_act(x, self.act_scale)
 
     def forward_act(self, x, bias=None, residual=None, act: str = "none", save_preact: bool = False, out=None,
