@@ -463,27 +463,22 @@ __global__ void __launch_bounds__(256) block_dx_kernel(const DxArgs p) {
 }
 
 // The same for tiles cut in ranges (with act-order, for every tile): block b
-// takes 4 rows of a tail tile, four columns per thread (and more such pieces
-// where there are more than a launch holds); the ranges' partial products are
-// added in order.
+// takes 4 rows of a tail tile, four columns per thread; the ranges' partial
+// products are added in order.  A launch's blocks count from `first`.
 template <int BM>
 __global__ void __launch_bounds__(256) block_dx_tail_kernel(const DxArgs p, int splits,
-                                                            const int32_t* __restrict__ perm) {
-    const int tail = p.tiles - p.head, lc = (threadIdx.x & 63) * 4;
-#pragma unroll 1
-    for (int b = blockIdx.x; b < tail * (BM / 4); b += int(gridDim.x)) {
-        const int i = b / (BM / 4);
-        int m_t, k_t;
-        tile_place(p.head + i, p.m_tiles, p.k_tiles, m_t, k_t);
-        const int rr = (b % (BM / 4)) * 4 + threadIdx.x / 64;
-        const int row = m_t * BM + rr, col = k_t * 256 + lc;
-        if (row >= p.M || col >= p.K) continue;
-        const int at[1] = {lc};
-        f4 w[1];
-        sum_ranges(p.part + (size_t(i) * BM + rr) * 256, at, size_t(tail) * (BM * 256), splits, w);
-        float v[4] = {w[0][0], w[0][1], w[0][2], w[0][3]};
-        finish_dx(p.add, p.dx, perm, size_t(row) * p.K, col, v);
-    }
+                                                            const int32_t* __restrict__ perm, int first) {
+    const int tail = p.tiles - p.head, b = first + int(blockIdx.x), i = b / (BM / 4);
+    int m_t, k_t;
+    tile_place(p.head + i, p.m_tiles, p.k_tiles, m_t, k_t);
+    const int rr = (b % (BM / 4)) * 4 + threadIdx.x / 64, lc = (threadIdx.x & 63) * 4;
+    const int row = m_t * BM + rr, col = k_t * 256 + lc;
+    if (row >= p.M || col >= p.K) return;
+    const int at[1] = {lc};
+    f4 w[1];
+    sum_ranges(p.part + (size_t(i) * BM + rr) * 256, at, size_t(tail) * (BM * 256), splits, w);
+    float v[4] = {w[0][0], w[0][1], w[0][2], w[0][3]};
+    finish_dx(p.add, p.dx, perm, size_t(row) * p.K, col, v);
 }
 
 // dx of an empty sum: dx_add, or zero.
@@ -515,9 +510,9 @@ wq_status launch_dx(const wqh::TilePlan& pl, const int32_t* perm, const DxArgs& 
     hipLaunchKernelGGL(kern, dim3(pl.blocks()), dim3(256), lds, s, a);
     const wq_status st = wqh::launch_status();
     if (st != WQ_OK || pl.tail() == 0) return st;
-    const unsigned blocks = unsigned(std::min(pl.tail() * (BM / 4LL), wqh::kMaxBlocks));
-    hipLaunchKernelGGL((block_dx_tail_kernel<BM>), dim3(blocks), dim3(256), 0, s, a, pl.splits, perm);
-    return wqh::launch_status();
+    return wqh::launch_pieces(pl.tail() * (BM / 4LL), [&](unsigned blocks, int first) {
+        hipLaunchKernelGGL((block_dx_tail_kernel<BM>), dim3(blocks), dim3(256), 0, s, a, pl.splits, perm, first);
+    });
 }
 
 template <int BITS>

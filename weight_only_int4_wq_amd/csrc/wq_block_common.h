@@ -2,6 +2,8 @@
 // and their derivatives, the forward epilogue, fp16 vector accesses.
 #pragma once
 
+#include <algorithm>
+
 #include "../../include/wq_block.h"
 #include "wq_gemm_common.h"
 
@@ -339,6 +341,18 @@ namespace wqh {
 
 // A launch holds fewer than 2^32 threads in x: blocks of 256 threads.
 constexpr long long kMaxBlocks = (1LL << 24) - 1;
+
+// launch(blocks, first) for blocks 0 .. total - 1 (total below 2^31), in as
+// many launches as that takes.
+template <class Launch>
+wq_status launch_pieces(long long total, const Launch& launch) {
+    for (long long first = 0; first < total; first += kMaxBlocks) {
+        launch(unsigned(std::min(total - first, kMaxBlocks)), int(first));
+        const wq_status st = launch_status();
+        if (st != WQ_OK) return st;
+    }
+    return WQ_OK;
+}
 
 // Time of a tile kernel's block, in us on MI355X: `idle` + `load` * (share of
 // the compute units that work) per 64-deep stage, plus `fixed` per tile (the

@@ -384,29 +384,24 @@ __global__ void __launch_bounds__(256, 1) block_fwd_kernel(const FwdArgs p) {
     }
 }
 
-// The same for tiles cut in ranges: one piece of a tail tile per thread (of
-// more than one tile where there are more pieces than a launch holds), the
-// ranges' partial products added in order.  Bound by reading them: 67 MB in
-// 16 us, two ranges of 2048 x 4096.
+// The same for tiles cut in ranges: one piece of a tail tile per thread, the
+// ranges' partial products added in order; a launch's blocks count from
+// `first`.  Bound by reading them: 67 MB in 16 us, two ranges of 2048 x 4096.
+// (With a capped grid that loops over the pieces instead: 18.)
 template <int BM>
-__global__ void __launch_bounds__(256) block_tail_kernel(const FwdArgs p, int splits) {
+__global__ void __launch_bounds__(256) block_tail_kernel(const FwdArgs p, int splits, int first) {
     const bool gated = p.gated != 0, wide = p.e.out % 8 == 0;
     const int oc_tile = gated ? 128 : 256, per_row = oc_tile / 8, rows = 256 / per_row;
-    const int tail = p.tiles - p.head, per_tile = BM / rows;
-    const int rr0 = threadIdx.x / per_row, oc = (threadIdx.x % per_row) * 8;
-#pragma unroll 1
-    for (int b = blockIdx.x; b < tail * per_tile; b += int(gridDim.x)) {
-        const int i = b / per_tile;
-        int m_t, n_t;
-        tile_place(p.head + i, p.m_tiles, p.n_tiles, m_t, n_t);
-        const int rr = (b % per_tile) * rows + rr0;
-        const int row = m_t * BM + rr;
-        if (row >= p.M) continue;
-        const float* src = p.part + (size_t(i) * BM + rr) * 256;
-        finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](const auto& at, auto& v) {
-            sum_ranges(src, at, size_t(tail) * (BM * 256), splits, v);
-        });
-    }
+    const int tail = p.tiles - p.head, per_tile = BM / rows, b = first + int(blockIdx.x), i = b / per_tile;
+    int m_t, n_t;
+    tile_place(p.head + i, p.m_tiles, p.n_tiles, m_t, n_t);
+    const int rr = (b % per_tile) * rows + threadIdx.x / per_row, oc = (threadIdx.x % per_row) * 8;
+    const int row = m_t * BM + rr;
+    if (row >= p.M) return;
+    const float* src = p.part + (size_t(i) * BM + rr) * 256;
+    finish_piece(p.e, gated, wide, row, n_t * oc_tile, oc, [&](const auto& at, auto& v) {
+        sum_ranges(src, at, size_t(tail) * (BM * 256), splits, v);
+    });
 }
 
 // Epilogue of a split product: V outputs of one row per thread, the ranges'
@@ -459,10 +454,9 @@ wq_status launch_fwd(const wqh::TilePlan& pl, const FwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((block_fwd_kernel<BITS, FAST, BM>), dim3(pl.blocks()), dim3(256), 0, s, a);
     const wq_status st = wqh::launch_status();
     if (st != WQ_OK || pl.tail() == 0) return st;
-    const unsigned per_tile = BM / (a.gated ? 16 : 8);
-    const unsigned blocks = unsigned(std::min(pl.tail() * (long long)per_tile, wqh::kMaxBlocks));
-    hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(blocks), dim3(256), 0, s, a, pl.splits);
-    return wqh::launch_status();
+    return wqh::launch_pieces(pl.tail() * (BM / (a.gated ? 16LL : 8LL)), [&](unsigned blocks, int first) {
+        hipLaunchKernelGGL((block_tail_kernel<BM>), dim3(blocks), dim3(256), 0, s, a, pl.splits, first);
+    });
 }
 
 template <int BITS, bool FAST>
