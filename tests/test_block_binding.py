@@ -127,3 +127,11 @@ def test_the_awq_scale_runs_on_the_tensors_device(index, monkeypatch):
     layer = wq.QuantizedLinear(meta(4, 4, dtype=torch.int32), meta(4, 1), None, 2, -1, 64, act_scale=meta(64))
     layer._scaled(OnDevice(index))
     assert seen == [index] and current == [0]
+
+
+def test_sizes_whose_sum_alone_is_large():
+    """Large sizes that each fit in 32 bits go to the library's own checks."""
+    with pytest.raises(ValueError, match="GPU tensors"):
+        call(wq.linear_act, 1 << 30, 1 << 21, 1 << 22)
+    with pytest.raises(ValueError, match="GPU tensors"):
+        call(wq.linear_act, (1 << 31) - 1, 1 << 21, 1 << 22)

@@ -521,7 +521,7 @@ def _sizes(M, rows, K):
 
 
 def _needs_gradient(t) -> bool:
-    return getattr(t, "requires_grad", False)  # (None and wrong types: checked elsewhere)
+    return getattr(t, "requires_grad", False)  # (wrong types are named elsewhere)
 
 
 def _say_detached(name):
@@ -624,9 +624,11 @@ def _forward(entry, x, packed, scales, zeros, bits, group_size, perm, bias, resi
     M, cols = x.shape
     if cols != K:
         raise ValueError(f"x must have {K} columns, got {cols}")
-    _sizes(M, rows, K)
+    if M + rows + K > 0x7FFFFFFF:
+        _sizes(M, rows, K)
     code = _act(act)
-    if torch.is_grad_enabled() and (x.requires_grad or _needs_gradient(bias) or _needs_gradient(residual)):
+    if (x.requires_grad or bias is not None and _needs_gradient(bias)
+            or residual is not None and _needs_gradient(residual)) and torch.is_grad_enabled():
         _say_detached("x, bias or residual")
     if workspace is not None:
         workspace = _workspace_arg(workspace, d)
@@ -682,11 +684,13 @@ def _backward(entry, dy, preact, packed, scales, zeros, bits, group_size, perm, 
     M, cols = dy.shape
     if cols != N:
         raise ValueError(f"dy must have {N} columns, got {cols}")
-    _sizes(M, rows, K)
+    if M + rows + K > 0x7FFFFFFF:
+        _sizes(M, rows, K)
     code = _act(act)
     if workspace is not None:
         workspace = _workspace_arg(workspace, d)
-    if torch.is_grad_enabled() and (dy.requires_grad or _needs_gradient(preact) or _needs_gradient(dx_add)):
+    if (dy.requires_grad or preact is not None and _needs_gradient(preact)
+            or dx_add is not None and _needs_gradient(dx_add)) and torch.is_grad_enabled():
         _say_detached("dy, preact or dx_add")
     needs_z = is_gated or act != "none"
     if needs_z and preact is None:
