@@ -95,7 +95,8 @@ size_t wq_gated_workspace_size(int32_t M, int32_t I, int32_t K, int32_t bits, in
  * gradient that adapters on this layer take); dbias fp32
  * [N] (nullable; fp32 because a sum over thousands of rows leaves fp16's
  * range).  The residual's gradient is dy.  dz enters the product in fp16, as
- * the matrix cores take it.  With M = 0 dbias is zero; with N = 0 dx is
+ * the matrix cores take it: where it leaves fp16's range it is infinite, and
+ * that row of dx infinite or NaN.  With M = 0 dbias is zero; with N = 0 dx is
  * dx_add or zero.
  * The workspace part that cannot be left out: dz rows padded to a multiple of
  * 8 when dz is NULL and the activation is not WQ_ACT_NONE, or when N is no

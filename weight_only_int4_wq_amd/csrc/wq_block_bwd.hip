@@ -27,11 +27,17 @@
 // tile's groups) pass through LDS one stage earlier.  Tiles that would fill a
 // last round only partly are cut along the weight rows.
 //
-// Measured: dz [2048 x 4096] . W [4096 x 11008] at 4 bits 200 us (923
+// dz enters the product in fp16, the matrix instruction's operand: half a step
+// (2^-11) of each value, which puts as much error into dx as dx's own rounding
+// does (relative to dx, root mean square: 2.1e-4 each, 2.9e-4 together), and an
+// infinity past 65504, which takes its row of dx along.  Two operands (the
+// value and what its rounding left) would take twice the matrix instructions.
+//
+// Measured: dz [2048 x 4096] . W [4096 x 11008] at 4 bits 198 us a pass (934
 // TFLOP/s), of which the cut tiles' sums take 10; [2048 x 22016] . [22016 x
-// 4096] 355 us (1040 TFLOP/s).  Bound by the matrix units at the clock that
-// power leaves them (busy 51 % of the counted cycles) and by the LDS writes of
-// the decoded weights, which hold a wavefront up by 25 cycles each.
+// 4096] 348 us (1063 TFLOP/s) of its pass's 401, and 17 for its sums.  Bound by the matrix units at
+// the clock that power leaves them (busy 51 % of the counted cycles) and by the
+// LDS writes of the decoded weights, which hold a wavefront up by 25 cycles each.
 #include <algorithm>
 
 #include "wq_block_common.h"
@@ -57,8 +63,8 @@ constexpr int kDzRowLanes = 4;  // rows a block works on at once
 // dbias's sums stay in registers, cross the four row lanes through LDS and
 // leave as one partial row per block row.  V = 8 needs N to be a multiple of
 // 8.  Bound by memory: each of dy, preact and dz is touched once (gated, 2048
-// x 11008, 225 MB in 46 us).  Columns that are not 8-byte groups take V = 1,
-// bound by the activation's arithmetic (311 x 5001, gelu, 8.6 us).
+// x 11008, 225 MB in 45 us).  Columns that are not 8-byte groups take V = 1,
+// bound by the activation's arithmetic (311 x 5001, gelu, 7.1 us).
 template <bool GATED, int V>
 __global__ void __launch_bounds__(64 * kDzRowLanes) block_dz_kernel(const DzArgs p) {
     constexpr int P = GATED ? 2 : 1;
@@ -489,8 +495,10 @@ __global__ void __launch_bounds__(256) block_dx_empty_kernel(size_t n4, const ui
     }
 }
 
-// [3 bits]: codes that straddle bytes take longer to decode, taller tiles
-// decode them fewer times.
+// [3 bits]: codes that straddle bytes take longer to decode (taller tiles
+// decode them fewer times), and the loop waits for all of its loads, its next
+// stage's among them, before each decoding.  At 256 rows it also moves 128
+// accumulators a stage to make room in registers (8 bits: 96; 2 and 4: none).
 constexpr wqh::TileCosts kDxCosts[2] = {
     {{{64, 0.55, 0.36, 8.01, false}, {128, 1.09, 0.14, 6.7, false}, {256, 1.44, 0.48, 6.29, false}}, 0.17, 0.314},
     {{{64, 1.35, 0.29, 0.02, false}, {128, 2.24, 0.17, 0.0, false}, {256, 2.75, 0.0, 0.0, false}}, 7.27, 0.259}};
@@ -526,8 +534,9 @@ wq_status launch_dx_bits(const wqh::TilePlan& pl, const int32_t* perm, bool g8, 
 
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// dbias's row ranges: enough blocks to fill the machine, at least 16 rows
-// each (a partial row costs 4 bytes per column to write and read).
+// dbias's row ranges: enough blocks to fill the machine, of about 16 rows or
+// more (17 rows make two, of 9 and 8; the last takes what is left): a partial
+// row costs 4 bytes per column to write and read.
 int dbias_ranges(int M, int R) {
     const int col_blocks = (R + 511) / 512;
     const int want = (4 * wqh::gemm_slots(1) + col_blocks - 1) / col_blocks;

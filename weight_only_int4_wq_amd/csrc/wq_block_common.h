@@ -447,7 +447,11 @@ size_t block_fwd_part_bytes(int M, int rows, int K, bool gated);  // for any gro
 bool block_fwd_fits(int M, int out, bool gated);                  // whether a launch covers the tiles
 wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream_t s);
 
-// Small M (decode batches).  K of more than 64 ranges of what a block's
+// Small M (decode batches): as far as two 16-row fragments of x fit the
+// registers.  Up to there the decode kernel is the faster one at every width:
+// at 32 rows, 4 bits, groups of 128, 11.9 us against the tile kernel's 16.8 for
+// 4096 x 4096, 20.5 against 21.1 for 4096 x 11008 (the closest; 25.2 and 26.7
+// at 8 bits), 22.8 against 33.3 for gated 11008 x 4096.  K of more than 64 ranges of what a block's
 // registers hold of x is the tile kernel's, and so are its bytes.
 constexpr int kBlockSmallM = 32;
 size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated);

@@ -33,9 +33,9 @@
 //    partly filled round of tiles leaves idle is used by cutting those tiles
 //    along K: 2048 x 11008 x 4096, 128 tiles, in two ranges 178 us, whole
 //    204 us.
-//  Measured: 2048 x 4096 x 2 x 11008 at 4 bits, gated, 364 us (1015 TFLOP/s;
-//  the card's matrix units are held back by power there: the loop's matrix
-//  instructions alone reach 1470).
+//  Measured: 2048 x 4096 x 2 x 11008 at 4 bits, gated, 364-369 us a pass (1000
+//  TFLOP/s; the card's matrix units are held back by power there: the loop's
+//  matrix instructions alone reach 1470).
 #include <algorithm>
 #include <type_traits>
 

@@ -31,12 +31,15 @@
 //    take that way.
 //  - At the end of a tile the wavefronts' partial products meet in LDS in a
 //    fixed order (two buffers: one barrier per tile).
-// Measured (kernel time): one row of 2 x 11008 x 4096 13.7 us (3.3 TB/s of
-// packed words), 8 rows of 2 x 14336 x 8192 31 us (3.9 TB/s), 16 rows of 4096
-// x 11008 13.4 us and 3.8 for its sums, one row of 4096 x 4096 6.0 us.  Start
-// and end take some 5 us of each; in between the decoder's vector instructions
-// (13 for 8 codes at 4 bits) bound it, then the copies' latency.  Placing the
-// scales so that their reads do not share banks changed no time.
+// Measured (a pass in a captured graph, three sets of inputs in turn): one row
+// of 2 x 11008 x 4096 13.8 us (3.3 TB/s of packed words), 8 rows of 2 x 14336
+// x 8192 34.8 us (3.4 TB/s; 31 when the same weights come again, from the
+// Infinity Cache), 16 rows of 4096 x 11008 16.1 us with its sums, one row of
+// 4096 x 4096 6.0 us.  Start and end take some 5 us of each; in between the
+// decoder's vector instructions (13 for 8 codes at 4 bits) bound it, then the
+// copies' latency, and tiles that do not fill whole rounds (896 of 2 x 14336
+// columns are 3.5 rounds of 256 blocks and take 4).  Placing the scales so that
+// their reads do not share banks changed no time.
 // (With the stream through double-buffered registers instead, one token
 // through 2 x 11008 x 4096 took 27 us, 16 tokens through 4096 x 11008 25 us.)
 #include <algorithm>
@@ -392,7 +395,10 @@ SmallPlan small_plan(int M, int rows, int K, int bits, bool gated, size_t part_b
     const size_t copy = size_t(M) * rows * 4;
     const int afford = copy ? int(std::min<size_t>(part_bytes / copy, 64)) : 1;
     int S = (steps * halves + most - 1) / most;
-    // a split pays for its second launch with at least two rounds of steps saved
+    // A range takes at least 16 steps, which suits one row: 1024 x 8192 7.4 us
+    // in the two ranges of this rule, 7.6 whole; 1024 x 4096 5.1 whole, 6.0 in
+    // two; 2048 x 8192 8.2 in two, 7.9 whole.  More rows would take more ranges
+    // (1024 x 8192 at 32 rows: 14.0 us in two, 10.5 in four).
     while (S < afford && p.tiles * (S + 1) <= cus && steps >= 16 * (S + 1)) ++S;
     if (S > 1 && S > afford) return p;
     p.sps = (steps + S - 1) / S;
