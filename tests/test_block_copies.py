@@ -72,3 +72,60 @@ def test_a_stage_leaves_only_the_newest_rows_in_flight(code):
         assert all(f == loop[0] and f[1] for f in first + loop), (name, first, loop)
         assert rest and not rest[0], (name, rest)
     assert seen == 24
+
+
+def _sgprs(operand):
+    m = re.fullmatch(r"s\[(\d+):(\d+)\]", operand)
+    if m:
+        return set(range(int(m.group(1)), int(m.group(2)) + 1))
+    return {int(operand[1:])} if re.fullmatch(r"s\d+", operand) else set()
+
+
+def _written(op, operands):
+    """Scalar registers that an instruction writes (a few vector ones have a
+    second result, a carry)."""
+    regs = set(_sgprs(operands[0])) if operands else set()
+    if re.match(r"v_(mad_[iu]64|add_co|sub_co|subrev_co|addc|subb|div_scale)", op) and len(operands) > 1:
+        regs |= _sgprs(operands[1])
+    return regs
+
+
+def _too_early(body):
+    """Copies whose resource the vector ALU wrote fewer than five wait states
+    before, in code order: the compiler adds those waits before loads of its
+    own, not inside an asm statement."""
+    at, last, bad = 0, {}, []
+    for line in body.splitlines():
+        line = line.split(";")[0].strip()
+        if not line or line.startswith(".") or line.endswith(":"):
+            continue
+        op, *operands = re.split(r"[\s,]+", line)
+        if op == "s_nop":
+            at += int(operands[0], 0) + 1
+            continue
+        if line.endswith(" lds"):
+            read = set().union(*(_sgprs(o) for o in operands))
+            bad += [(line, last[r][1]) for r in read if r in last and at - last[r][0] - 1 < 5]
+        for r in _written(op, operands):
+            if op.startswith("v_"):
+                last[r] = (at, line)
+            else:
+                last.pop(r, None)
+        at += 1
+    return bad
+
+
+def test_the_walk_sees_an_early_copy():
+    copy = "\ts_nop 0\n\tbuffer_load_dwordx4 v1, s[8:11], 0 offen lds\n"
+    write = "\tv_readfirstlane_b32 s9, v0\n"
+    assert _too_early(write + copy)
+    assert _too_early(write + "\ts_mov_b32 m0, s3\n\tv_mov_b32 v2, v3\n\tv_mov_b32 v2, v3\n" + copy)
+    assert not _too_early(write + "\ts_nop 3\n" + copy)
+    assert not _too_early(write + "\ts_mov_b32 s9, s4\n" + copy)
+    assert _too_early("\tv_mad_u64_u32 v[2:3], s[10:11], v2, s1, 0\n" + copy)
+
+
+def test_resources_are_ready_when_a_copy_reads_them(code):
+    for src, asm in code.items():
+        for name, body in kernels(asm, r"block_\w+_kernel"):
+            assert not _too_early(body), (src, name, _too_early(body)[:3])
