@@ -674,9 +674,11 @@ wq_status skinny_gemv(const uint16_t* x, const uint32_t* packed, const uint16_t*
     float* part = split ? static_cast<float*>(workspace) : nullptr;
     constexpr int D = WQ_SKINNY_D;
     auto go = [&](auto kern) {
+        // (one value for every call: the limit is the process's, and another
+        // thread's smaller layer must not lower it under this launch)
         if (plan.lds > 64 * 1024)
             (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                      int(plan.lds));
+                                      lds_max);
         hipLaunchKernelGGL(kern, dim3(plan.blocks), dim3(64 * kSkinnyWaves), plan.lds, s, x, packed, scales, zeros, y,
                            M, N, K, gd, plan.tpb, plan.geo, act_scale, bias, part);
         wq_status st = launch_status();
