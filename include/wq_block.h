@@ -92,8 +92,8 @@ size_t wq_gated_workspace_size(int32_t M, int32_t I, int32_t K, int32_t bits, in
  *   dx = fp16(dz . W + dx_add),    dbias[n] = sum over m of dy * act'(preact).
  * preact fp16 [M][N], required unless act is WQ_ACT_NONE; dx_add fp16 [M][K]
  * (nullable, may be dx itself); dx fp16 [M][K]; dz fp16 [M][N] (nullable: the
- * gradient that adapters on this layer take); dbias fp32
- * [N] (nullable; fp32 because a sum over thousands of rows leaves fp16's
+ * gradient that adapters on this layer take); dbias fp32 [N]
+ * (nullable; fp32 because a sum over thousands of rows leaves fp16's
  * range).  The residual's gradient is dy.  dz enters the product in fp16, as
  * the matrix cores take it: where it leaves fp16's range it is infinite, and
  * that row of dx infinite or NaN.  With M = 0 dbias is zero; with N = 0 dx is

@@ -35,9 +35,10 @@
 //
 // Measured: dz [2048 x 4096] . W [4096 x 11008] at 4 bits 198 us a pass (934
 // TFLOP/s), of which the cut tiles' sums take 10; [2048 x 22016] . [22016 x
-// 4096] 348 us (1063 TFLOP/s) of its pass's 401, and 17 for its sums.  Bound by the matrix units at
-// the clock that power leaves them (busy 51 % of the counted cycles) and by the
-// LDS writes of the decoded weights, which hold a wavefront up by 25 cycles each.
+// 4096] 348 us (1063 TFLOP/s) of its pass's 401, and 17 for its sums.  Bound by
+// the matrix units at the clock that power leaves them (busy 51 % of the counted
+// cycles) and by the LDS writes of the decoded weights, which hold a wavefront
+// up by 25 cycles each.
 #include <algorithm>
 
 #include "wq_block_common.h"

@@ -451,8 +451,9 @@ wq_status block_fwd(const BlockFwd& p, float* part, size_t part_bytes, hipStream
 // registers.  Up to there the decode kernel is the faster one at every width:
 // at 32 rows, 4 bits, groups of 128, 11.9 us against the tile kernel's 16.8 for
 // 4096 x 4096, 20.5 against 21.1 for 4096 x 11008 (the closest; 25.2 and 26.7
-// at 8 bits), 22.8 against 33.3 for gated 11008 x 4096.  K of more than 64 ranges of what a block's
-// registers hold of x is the tile kernel's, and so are its bytes.
+// at 8 bits), 22.8 against 33.3 for gated 11008 x 4096.  K of more than 64
+// ranges of what a block's registers hold of x is the tile kernel's, and so are
+// its bytes.
 constexpr int kBlockSmallM = 32;
 size_t block_small_part_bytes(int M, int rows, int K, int bits, bool gated);
 // WQ_ERR_UNSUPPORTED when K has to be split and `part` has no room for it.
