@@ -27,3 +27,5 @@ from .wq_oracle import (  # noqa: F401
     quantize_linear_layer,
     f64_to_f16_nearest,
 )
+
+from .wq_dropout_oracle import drop_halves, drop_keep, philox4x32  # noqa: F401,E402

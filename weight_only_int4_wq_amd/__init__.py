@@ -1,8 +1,9 @@
 """Weight-only quantized linear layers on AMD gfx950 (MI355X).
 
 Thin Python binding over libwq.so, the HIP library whose C ABI is declared in
-include/wq.h and, for the products of a feed-forward block and their backward
-passes, include/wq_block.h.  Every function here only checks and marshals arguments (torch
+include/wq.h, for the products of a feed-forward block and their backward
+passes include/wq_block.h, and for low-rank adapters and dropout
+include/wq_adapter.h.  Every function here only checks and marshals arguments (torch
 tensors for device memory, torch's current HIP stream) and calls the entry
 point of the same name; all computation runs in the library's kernels.
 There is no fallback: if libwq.so is missing or cannot be loaded, every call
@@ -21,7 +22,8 @@ __all__ = [
     "dequant", "scale_act", "workspace_size", "gemv", "gemm", "linear", "gemv_silu_mul", "gemv_ex", "gemv_max_m",
     "linear_noalloc", "noalloc_scratch_bytes", "stream_read",
     "ACTIVATIONS", "linear_act", "linear_act_backward", "gated", "gated_backward", "block_workspace_size",
-    "status_str", "version", "QuantizedLinear", "QuantizedGatedMLP",
+    "adapters", "adapters_backward", "adapters_workspace_size", "dropout", "dropout_backward",
+    "status_str", "version", "QuantizedLinear", "QuantizedGatedMLP", "AdaptedLinear",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -66,6 +68,12 @@ _SIG["wq_gated"] = (ctypes.c_int, [_VP] * 6 + [_I32, _VP, _VP] + [_I32] * 5 + [_
 for _name in ("wq_linear_act_backward", "wq_gated_backward"):
     _SIG[_name] = (ctypes.c_int, [_VP, _VP, _I32] + [_VP] * 8 + [_I32] * 5 + [_VP, _SIZE, _VP])
 for _name in ("wq_linear_act", "wq_gated", "wq_linear_act_backward", "wq_gated_backward"):
+    _SIG[_name + "_workspace_size"] = (_SIZE, [_I32] * 5)
+_DROP = [ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _VP]
+_SIG["wq_adapters"] = (ctypes.c_int, [_VP] * 6 + _DROP + [_VP, _VP] + [_I32] * 5 + [_VP, _SIZE, _VP])
+_SIG["wq_adapters_backward"] = (ctypes.c_int, [_VP] * 7 + _DROP + [_VP] * 4 + [_I32] * 5 + [_VP, _SIZE, _VP])
+_SIG["wq_dropout"] = (ctypes.c_int, [_VP, _VP] + _DROP + [_VP, ctypes.c_int64, _VP])
+for _name in ("wq_adapters", "wq_adapters_backward"):
     _SIG[_name + "_workspace_size"] = (_SIZE, [_I32] * 5)
 
 # Activations of the block's products, by the numbers of wq_act.
@@ -532,6 +540,10 @@ def _say_detached(name):
                   "function, from a torch.autograd.Function for instance, or torch.no_grad()", stacklevel=4)
 
 
+def _say_detached_call(name):
+    _say_detached(name)  # (one frame more, as in the block's functions)
+
+
 def _act(act) -> int:
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
@@ -731,6 +743,197 @@ def gated_backward(dh, preact, packed, scales, zeros, bits: int, group_size: int
                      need_dbias, out, workspace)
 
 
+# -------------------------------------------- adapters and dropout ----
+
+def adapters_workspace_size(entry: str, M: int, N: int, K: int, rank: int, adapters: int) -> int:
+    """Bytes of workspace of `entry` ("adapters" or "adapters_backward")."""
+    _sizes(M, N, K)
+    _sizes(rank, adapters, 0)
+    return int(getattr(lib(), f"wq_{entry}_workspace_size")(M, N, K, rank, adapters))
+
+
+def _on_device(entry, device, args):
+    """wq_<entry> on the tensors' device (made current for the call) and its
+    current stream."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensor arguments must be GPU tensors, got one on {device}")
+    fn = getattr(lib(), entry)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            code = fn(*args, stream)
+    else:
+        code = fn(*args, stream)
+    if code:
+        _check(code, entry)
+
+
+def _drop_args(p, seed, offset, step, device):
+    """p, seed, offset and step's address; p = 0 drops nothing."""
+    if not 0 <= p < 1 or p * 65536 + 0.5 >= 65536:
+        raise ValueError(f"p must be in [0, 1) and not round to 1 in steps of 2^-16, got {p!r}")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"seed and offset must be in 0 .. 2^64 - 1, got {seed!r} and {offset!r}")
+    return p, seed, offset, None if step is None else _arg(step, _torch().int64, "step", (1,), device)
+
+
+def _pool_args(down, up, scales, slots, M, N, K, device):
+    """Check a pool of adapters; returns (rank, adapters, the addresses of
+    down, up, scales and slots)."""
+    torch = _torch()
+    if down.__class__ is not torch.Tensor or down.dim() != 3:
+        _dev(down, torch.float16, "down", 3, device=device)
+    count, rank, _ = down.shape
+    if not 1 <= rank <= 128:
+        raise ValueError(f"ranks of 1 to 128 are supported, got {rank}")
+    if count < 1 or N < 1 or K < 32 or K % 32:
+        raise ValueError(f"at least one adapter and one column, and a multiple of 32 channels are needed, got {count}, "
+                         f"{N} and {K}")
+    if M + N + K > 0x7FFFFFFF or count > 0x7FFFFFFF:
+        _sizes(M, N, K)
+        _sizes(count, 0, 0)
+    return rank, count, _arg(down, torch.float16, "down", (count, rank, K), device), \
+        _arg(up, torch.float16, "up", (count, rank, N), device), _arg(scales, torch.float32, "scales", (count,), device), \
+        _opt(slots, torch.int32, "slots", (M,), device)
+
+
+def _room(entry, workspace, M, N, K, rank, count, device):
+    """Address and bytes of the workspace, allocated where none is given."""
+    torch = _torch()
+    if workspace is not None:
+        workspace = _workspace_arg(workspace, device)
+    elif M and device.type == "cuda":
+        need = getattr(lib(), entry)(M, N, K, rank, count)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+    # (the tensor is returned to live until the call is enqueued)
+    return workspace, (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+
+
+def adapters(x, down, up, scales, slots=None, base=None, p: float = 0.0, seed: int = 0, offset: int = 0, step=None,
+             save_hidden: bool = False, out=None, hidden=None, workspace=None):
+    """y fp16 [M][N] = base + s[a] * (dropout(x) . down[a]^T) . up[a], row m
+    with adapter a = slots[m] (int32 [M] in any order; None: adapter 0; a
+    number that is no adapter's: none, y is base or zero).  x fp16 [M][K]; the
+    pool: down fp16 [L][rank][K], up fp16 [L][rank][N] (the second factor
+    transposed), scales fp32 [L]; rank at most 128.  base fp16 [M][N]: a
+    projection's output; `out` may be `base`.  With save_hidden (or a
+    `hidden` tensor to fill) returns (y, hidden fp32 [M][rank]) for
+    adapters_backward.  p, seed, offset, step: dropout of x, the mask that
+    dropout() makes of them.  Nothing is recorded for autograd; where that
+    loses a gradient, this and the three functions below warn."""
+    torch = _torch()
+    half = torch.float16
+    x = _first(x, "x")
+    d = x.device
+    M, K = x.shape
+    if up.__class__ is not torch.Tensor or up.dim() != 3:
+        _dev(up, half, "up", 3, device=d)
+    N = up.shape[2]
+    rank, count, down_at, up_at, scales_at, slots_at = _pool_args(down, up, scales, slots, M, N, K, d)
+    drop = _drop_args(p, seed, offset, step, d)
+    if (x.requires_grad or down.requires_grad or up.requires_grad or _needs_gradient(scales)
+            or base is not None and _needs_gradient(base)) and torch.is_grad_enabled():
+        _say_detached_call("x, down, up, scales or base")
+    base_at = _opt(base, half, "base", (M, N), d)
+    if out is None:
+        out = torch.empty((M, N), dtype=half, device=d)
+        y = out.data_ptr()
+    else:
+        y = _arg(out, half, "out", (M, N), d)
+    h = None
+    if hidden is not None:
+        h = _arg(hidden, torch.float32, "hidden", (M, rank), d)
+    elif save_hidden:
+        hidden = torch.empty((M, rank), dtype=torch.float32, device=d)
+        h = hidden.data_ptr()
+    workspace, room = _room("wq_adapters_workspace_size", workspace, M, N, K, rank, count, d)
+    _on_device("wq_adapters", d, (x.data_ptr(), down_at, up_at, scales_at, slots_at, base_at, *drop, y, h, M, N, K, rank,
+                                  count, *room))
+    return out if hidden is None else (out, hidden)
+
+
+def adapters_backward(dy, x, hidden, down, up, scales, slots=None, p: float = 0.0, seed: int = 0, offset: int = 0,
+                      step=None, dx_add=None, need_dx: bool = True, need_weights: bool = True, out=None,
+                      workspace=None):
+    """Backward of adapters for dy fp16 [M][N], the x and dropout numbers of
+    the forward call and the hidden it kept -> (dx fp16 [M][K] + dx_add, or
+    None; ddown fp32 [L][rank][K] and dup fp32 [L][rank][N], or None).  With
+    need_weights=False x and hidden may be None.  base's gradient is dy.
+    `out` may be `dx_add`."""
+    torch = _torch()
+    half = torch.float16
+    dy = _first(dy, "dy")
+    d = dy.device
+    M, N = dy.shape
+    if down.__class__ is not torch.Tensor or down.dim() != 3:
+        _dev(down, half, "down", 3, device=d)
+    K = down.shape[2]
+    rank, count, down_at, up_at, scales_at, slots_at = _pool_args(down, up, scales, slots, M, N, K, d)
+    drop = _drop_args(p, seed, offset, step, d)
+    if (dy.requires_grad or down.requires_grad or up.requires_grad or _needs_gradient(scales)
+            or x is not None and _needs_gradient(x) or dx_add is not None and _needs_gradient(dx_add)) \
+            and torch.is_grad_enabled():
+        _say_detached_call("dy, x, down, up, scales or dx_add")
+    x_at = h = dx = ddown = dup = None
+    add_at = _opt(dx_add, half, "dx_add", (M, K), d)
+    if not need_dx:
+        if out is not None or dx_add is not None:
+            raise ValueError("out and dx_add are for a call that needs dx")
+    elif out is None:
+        out = torch.empty((M, K), dtype=half, device=d)
+        dx = out.data_ptr()
+    else:
+        dx = _arg(out, half, "out", (M, K), d)
+    if need_weights:
+        x_at = _arg(x, half, "x", (M, K), d)
+        h = _arg(hidden, torch.float32, "hidden", (M, rank), d)
+        ddown = torch.empty((count, rank, K), dtype=torch.float32, device=d)
+        dup = torch.empty((count, rank, N), dtype=torch.float32, device=d)
+    workspace, room = _room("wq_adapters_backward_workspace_size", workspace, M, N, K, rank, count, d)
+    _on_device("wq_adapters_backward", d,
+               (dy.data_ptr(), x_at, h, down_at, up_at, scales_at, slots_at, *drop, add_at, dx,
+                None if ddown is None else ddown.data_ptr(), None if dup is None else dup.data_ptr(), M, N, K, rank,
+                count, *room))
+    return out, ddown, dup
+
+
+def _dropout(x, name, p, seed, offset, step, residual, out):
+    torch = _torch()
+    half = torch.float16
+    if x.__class__ is not torch.Tensor or x.dtype is not half or not x.is_contiguous():
+        _dev(x, half, name)
+    d, shape = x.device, x.shape
+    drop = _drop_args(p, seed, offset, step, d)
+    if (x.requires_grad or residual is not None and _needs_gradient(residual)) and torch.is_grad_enabled():
+        _say_detached(f"{name} or residual")
+    r = _opt(residual, half, "residual", shape, d)
+    if out is None:
+        out = torch.empty_like(x)
+        y = out.data_ptr()
+    else:
+        y = _arg(out, half, "out", shape, d)
+    _on_device("wq_dropout", d, (x.data_ptr(), r, *drop, y, x.numel()))
+    return out
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None, out=None):
+    """(kept ? x / (1 - p) : 0) + residual for fp16 x of any shape.  Which
+    elements are kept follows from (seed, offset + step, the element's number)
+    by a counter-based generator: no mask is stored, and the same numbers make
+    the same mask in dropout_backward, adapters and adapters_backward.  Give
+    every call of a training run another offset.  step: int64 [1] on the
+    device, added to offset, for captured graphs (advance it between replays).
+    p is taken in steps of 2^-16.  `out` may be x or residual."""
+    return _dropout(x, "x", p, seed, offset, step, residual, out)
+
+
+def dropout_backward(dy, p: float, seed: int, offset: int = 0, step=None, out=None):
+    """Gradient of dropout's x: kept ? dy / (1 - p) : 0, for the forward
+    call's p, seed, offset and step.  The residual's gradient is dy."""
+    return _dropout(dy, "dy", p, seed, offset, step, None, out)
+
+
 class QuantizedLinear:
     """A quantized linear layer held in device memory: packed weights, group
     scales and zero-points, optional act-order perm and AWQ input scale.
@@ -839,3 +1042,36 @@ class QuantizedGatedMLP:
         dx, dz, _ = gated_backward(dh, preact, g.packed, g.scales, g.zeros, g.bits, g.group_size, perm=g.perm,
                                    act=self.act, dx_add=dx_add)
         return g._scaled(dx), dz, dh
+
+
+class AdaptedLinear:
+    """A frozen quantized layer and a pool of low-rank adapters on it:
+    y = x . W^T + bias + s[a] * (dropout(x) . down[a]^T) . up[a], row m with
+    adapter a = slots[m] (see adapters).  base: a QuantizedLinear; down fp16
+    [L][rank][K], up fp16 [L][rank][N], scales fp32 [L].  backward returns the
+    gradients of x and of the pool."""
+
+    def __init__(self, base: QuantizedLinear, down, up, scales):
+        if down.dim() != 3 or up.dim() != 3 or down.shape[:2] != up.shape[:2]:
+            raise ValueError("down and up must be [L][rank][K] and [L][rank][N]")
+        if down.shape[2] != base.K or up.shape[2] != base.N:
+            raise ValueError(f"the base layer is [{base.N}][{base.K}], the adapters' is "
+                             f"[{up.shape[2]}][{down.shape[2]}]")
+        self.base, self.down, self.up, self.scales = base, down, up, scales
+
+    def __call__(self, x, slots=None, bias=None, residual=None, p: float = 0.0, seed: int = 0, offset: int = 0,
+                 step=None, save_hidden: bool = False):
+        """y, or with save_hidden (y, hidden) where hidden is what backward
+        takes.  The layer's output (with bias and residual) is rounded to
+        fp16 before the adapters' is added."""
+        y = self.base.forward_act(x, bias=bias, residual=residual)
+        return adapters(x, self.down, self.up, self.scales, slots, base=y, p=p, seed=seed, offset=offset, step=step,
+                        save_hidden=save_hidden, out=y)
+
+    def backward(self, dy, x, hidden, slots=None, p: float = 0.0, seed: int = 0, offset: int = 0, step=None,
+                 need_weights: bool = True):
+        """(dx, ddown, dup) for dy fp16 [M][N] and the forward call's x, slots
+        and dropout numbers."""
+        dx, _, _ = self.base.backward(dy, need_dz=False)
+        return adapters_backward(dy, x, hidden, self.down, self.up, self.scales, slots, p=p, seed=seed, offset=offset,
+                                 step=step, dx_add=dx, need_weights=need_weights, out=dx)

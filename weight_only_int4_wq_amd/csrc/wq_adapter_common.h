@@ -1,0 +1,66 @@
+// Shared parts of the adapters' and dropout's kernels (wq_adapter.h).
+#pragma once
+
+#include "../../include/wq_adapter.h"
+#include "wq_block_common.h"
+
+namespace wq {
+
+// Which elements dropout keeps.  t = 0: all of them.
+struct Drop {
+    uint32_t t;            // a half word below it drops the element
+    float keep;            // 65536 / (65536 - t)
+    uint32_t key0, key1;   // the seed
+    uint64_t offset;
+    const int64_t* step;   // added to offset; nullable
+};
+
+// The second half of the generator's counter: offset + *step.
+__device__ __forceinline__ uint64_t drop_stream(const Drop& d) {
+    return d.offset + (d.step ? uint64_t(*d.step) : 0u);
+}
+
+// Philox4x32-10's output for the counter (n, stream).
+__device__ __forceinline__ u4 philox(uint64_t n, uint64_t stream, uint32_t k0, uint32_t k1) {
+    uint32_t c0 = uint32_t(n), c1 = uint32_t(n >> 32), c2 = uint32_t(stream), c3 = uint32_t(stream >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
+        c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+        c1 = uint32_t(b);
+        c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+        c3 = uint32_t(a);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u4{c0, c1, c2, c3};
+}
+
+// Whether element i of a block's eight is kept.
+__device__ __forceinline__ bool kept(u4 w, int i, uint32_t t) {
+    return (i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu) >= t;
+}
+
+}  // namespace wq
+
+namespace wqh {
+
+// Sizes and operands of both adapter passes: src [M][C] . w[a]^T -> [M][R].
+struct Adapters {
+    const float* scales;
+    const int32_t* slots;
+    int M, R, L;
+    wq::Drop drop;
+};
+
+size_t adapters_workspace(int M, int N, int K, int R, int L);
+wq_status adapters_forward(const Adapters& a, const uint16_t* x, const uint16_t* down, const uint16_t* up,
+                           const uint16_t* base, uint16_t* y, float* hidden, int N, int K, void* ws, hipStream_t s);
+size_t adapters_backward_workspace(int M, int N, int K, int R, int L);
+wq_status adapters_backward(const Adapters& a, const uint16_t* dy, const uint16_t* x, const float* hidden,
+                            const uint16_t* down, const uint16_t* up, const uint16_t* dx_add, uint16_t* dx,
+                            float* ddown, float* dup, int N, int K, void* ws, hipStream_t s);
+wq_status dropout(const uint16_t* x, const uint16_t* residual, const wq::Drop& d, uint16_t* y, int64_t n,
+                  hipStream_t s);
+
+}  // namespace wqh
