@@ -25,7 +25,8 @@ using wq::h8;
 using wq::u4;
 
 constexpr int kWindow = 64;   // rows a block looks at: a wavefront's lanes
-constexpr int kChunk = 128;   // columns of src that a wavefront takes at a time
+constexpr int kChunk = 128;   // columns of src by which a shrink is split into ranges
+constexpr int kShrinkWaves = 8;
 constexpr int kCols = 128;    // columns of out and dw of a wavefront: 16 lanes of 8
 
 // Eight fp16 values at p, which need not be aligned to more than one of them
@@ -35,15 +36,27 @@ __device__ __forceinline__ u4 load8(const uint16_t* p) {
     __builtin_memcpy(&v, p, 16);
     return v;
 }
-// The first n of them (n <= 0: none), zeros behind.
-__device__ __forceinline__ u4 load8_part(const uint16_t* p, int n) {
-    if (n >= 8) return load8(p);
-    u4 v{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) v[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+// Within a window or an adapter, element numbers fit 32 bits (64 rows, or 128
+// of the rank, of at most 2^22 columns): a uniform base and a 32-bit offset,
+// which the loads take as they are.
+__device__ __forceinline__ const uint16_t* off(const uint16_t* base, uint32_t n) {
+    return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + n * 2u);
+}
+// The last columns of a row of C (at least 8): where a load of eight from
+// column c on would pass the row's end it is taken from C - 8 on, and what comes
+// before c is shifted out.
+__device__ __forceinline__ int held(int c, int C) { return min(c, C - 8); }
+__device__ __forceinline__ u4 shifted(u4 v, int c, int C) {
+    const int s = c - held(c, C);
+    if (s & 1)
+        v = u4{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+               __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
+    if (s & 2) v = u4{v[1], v[2], v[3], 0};
+    if (s & 4) v = u4{v[2], v[3], 0, 0};
+    if (s >= 8) v = u4{0, 0, 0, 0};
     return v;
 }
+// The first n of eight values.
 __device__ __forceinline__ void store8_part(uint16_t* p, u4 v, int n) {
     if (n >= 8) {
         __builtin_memcpy(p, &v, 16);
@@ -196,96 +209,100 @@ __device__ __forceinline__ void list_rows(const Shrink& p, int64_t a) {
 }
 
 // One adapter's rows of a window against 16 NRT of its rank's rows, over the
-// block's range of columns; the four wavefronts take its chunks in turn.
+// block's range of columns; the wavefronts take pieces of it in turn, the
+// next one's loads in flight.  Rows past the adapter's repeat its last one, and rows past
+// the rank likewise: they cost no traffic, and what they give is not kept.
 template <int MT, int NRT, bool DROP>
-__device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, int cnt, int order, int r0, int split, f4* sum) {
-    // columns a wavefront loads at a time: 32 to a matrix step
-    constexpr int STEPS = MT + NRT > 5 ? 2 : 4, COLS = 32 * STEPS;
+__device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, int cnt, int order, int r0, int split,
+                                            f4* sum) {
+    constexpr int STEPS = MT * NRT > 8 ? 1 : 2, COLS = 32 * STEPS;   // 128 bytes of a row, or what the registers hold
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
     f4 acc[MT][NRT];
-    const uint16_t* xr[MT];
-    uint64_t eight[MT];
-    bool on[MT];
+    const uint16_t* const xb = p.src + m0 * p.C;
+    const uint16_t* const wb = p.w + int64_t(a) * p.R * p.C;
+    const uint64_t eight = uint64_t(m0) * (p.C / 8);
+    uint32_t xr[MT], wr[NRT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t m = m0 + __shfl(order, 16 * t + c16);
-        on[t] = 16 * t + c16 < cnt;
-        xr[t] = p.src + m * p.C + 8 * g;
-        eight[t] = uint64_t(m) * (p.C / 8) + g;
+        xr[t] = uint32_t(__shfl(order, min(16 * t + c16, cnt - 1))) * p.C;
 #pragma unroll
         for (int n = 0; n < NRT; ++n) acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
     }
-    const uint16_t* wr[NRT];   // (rows past the rank repeat the last one: their columns of h become zeros)
 #pragma unroll
-    for (int n = 0; n < NRT; ++n) wr[n] = p.w + (int64_t(a) * p.R + min(r0 + 16 * n + c16, p.R - 1)) * p.C + 8 * g;
+    for (int n = 0; n < NRT; ++n) wr[n] = uint32_t(min(r0 + 16 * n + c16, p.R - 1)) * p.C;
     const uint64_t stream = DROP ? wq::drop_stream(p.drop) : 0;
 
-    u4 x[2][MT][STEPS], w[2][NRT][STEPS];
-    auto load = [&](int64_t c0, u4 (&xs)[MT][STEPS], u4 (&ws)[NRT][STEPS]) {
-        if (c0 + COLS <= p.C) {
+    struct Part {
+        u4 x[MT][STEPS], w[NRT][STEPS];
+    };
+    auto load = [&](int c0, Part& v) {
 #pragma unroll
-            for (int n = 0; n < NRT; ++n)
+        for (int i = 0; i < STEPS; ++i) {
+            const int c = held(c0 + 32 * i + 8 * g, p.C);
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) ws[n][i] = load8(wr[n] + c0 + 32 * i);
+            for (int n = 0; n < NRT; ++n) v.w[n][i] = load8(off(wb, wr[n] + c));
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    xs[t][i] = u4{0, 0, 0, 0};
-                    if (on[t]) xs[t][i] = load8(xr[t] + c0 + 32 * i);
-                }
-        } else {
-            const int left = int(p.C - c0) - 8 * g;
-#pragma unroll
-            for (int n = 0; n < NRT; ++n)
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) ws[n][i] = load8_part(wr[n] + c0 + 32 * i, left - 32 * i);
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i)
-                    xs[t][i] = load8_part(xr[t] + c0 + 32 * i, on[t] ? left - 32 * i : 0);
+            for (int t = 0; t < MT; ++t) v.x[t][i] = load8(off(xb, xr[t] + c));
         }
     };
-    auto multiply = [&](int64_t c0, u4 (&xs)[MT][STEPS], u4 (&ws)[NRT][STEPS]) {
+    auto multiply = [&](int c0, Part& v) {
+        if (c0 + COLS > p.C)
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int c = c0 + 32 * i + 8 * g;
+#pragma unroll
+                for (int n = 0; n < NRT; ++n) v.w[n][i] = shifted(v.w[n][i], c, p.C);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) v.x[t][i] = shifted(v.x[t][i], c, p.C);
+            }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i)
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                if constexpr (DROP) xs[t][i] = drop8(xs[t][i], eight[t] + uint64_t(c0 / 8 + 4 * i), p.drop, stream);
+                if constexpr (DROP) v.x[t][i] = drop8(v.x[t][i], eight + ((xr[t] + c0 + 32 * i + 8 * g) >> 3), p.drop, stream);
 #pragma unroll
-                for (int n = 0; n < NRT; ++n) acc[t][n] = mfma(xs[t][i], ws[n][i], acc[t][n]);
+                for (int n = 0; n < NRT; ++n) acc[t][n] = mfma(v.x[t][i], v.w[n][i], acc[t][n]);
             }
     };
-    const int64_t end = min(int64_t(split + 1) * p.cps * kChunk, int64_t(p.C));
-    int64_t c0 = int64_t(split) * p.cps * kChunk + wave * COLS;
-    if (c0 < end) load(c0, x[0], w[0]);
-    for (; c0 < end; c0 += 8 * COLS) {
-        const int64_t c1 = c0 + 4 * COLS, c2 = c1 + 4 * COLS;
-        if (c1 < end) load(c1, x[1], w[1]);
-        multiply(c0, x[0], w[0]);
-        if (c2 < end) load(c2, x[0], w[0]);
-        if (c1 < end) multiply(c1, x[1], w[1]);
+    const int end = int(min(int64_t(split + 1) * p.cps * kChunk, int64_t(p.C)));
+    constexpr int NEXT = kShrinkWaves * COLS;
+    int c0 = split * p.cps * kChunk + wave * COLS;
+    Part v[2];
+    if (c0 < end) load(c0, v[0]);
+    for (; c0 < end; c0 += 2 * NEXT) {
+        if (c0 + NEXT < end) load(c0 + NEXT, v[1]);
+        multiply(c0, v[0]);
+        if (c0 + 2 * NEXT < end) load(c0 + 2 * NEXT, v[0]);
+        if (c0 + NEXT < end) multiply(c0 + NEXT, v[1]);
     }
 
-    // the four wavefronts' sums, in order
+    // the wavefronts' sums: w and w + 4, then the four in order
+    constexpr int HALF = kShrinkWaves / 2;
+    auto at = [&](int t, int n, int w) { return ((t * NRT + n) * HALF + w) * 64 + lane; };
+    if (wave >= HALF)
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int n = 0; n < NRT; ++n) sum[((t * NRT + n) * 4 + wave) * 64 + lane] = acc[t][n];
+            for (int n = 0; n < NRT; ++n) sum[at(t, n, wave - HALF)] = acc[t][n];
+    __syncthreads();
+    if (wave < HALF)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < NRT; ++n) sum[at(t, n, wave)] += acc[t][n];
     __syncthreads();
     const int RP = NRT * 16 * p.rchunks;
-    for (int e = wave; e < MT * NRT; e += 4) {
+    for (int e = wave; e < MT * NRT; e += kShrinkWaves) {
         const int t = e / NRT, n = e % NRT, r = r0 + 16 * n + c16;
-        f4 v = sum[e * 256 + lane];
+        f4 v = sum[at(t, n, 0)];
 #pragma unroll
-        for (int i = 1; i < 4; ++i) v += sum[e * 256 + 64 * i + lane];
-        const float f = r < p.R ? DROP ? p.drop.keep : 1.f : 0.f;
+        for (int i = 1; i < HALF; ++i) v += sum[at(t, n, i)];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 16 * t + 4 * g + i;
             const int64_t m = m0 + __shfl(order, row);
-            if (row < cnt) p.part[(int64_t(split) * p.M + m) * RP + r] = r < p.R ? v[i] * f : 0.f;
+            if (row < cnt)
+                p.part[(int64_t(split) * p.M + m) * RP + r] = r < p.R ? DROP ? v[i] * p.drop.keep : v[i] : 0.f;
         }
     }
     __syncthreads();
@@ -295,11 +312,11 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
 // take them in turn, so that each holds its own range of every adapter in L2),
 // the rank's 64s, and Z shares of its adapters.
 template <int NRT, bool DROP>
-__global__ __launch_bounds__(256) void shrink_kernel(const Shrink p, int64_t first) {
-    __shared__ f4 sum[4 * NRT * 256];
+__global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(const Shrink p, int64_t first) {
+    __shared__ f4 sum[4 * NRT * 64 * (kShrinkWaves / 2)];
     int64_t b = first + blockIdx.x;
     if (b >= p.blocks) {
-        list_rows(p, (b - p.blocks) * 4 + (threadIdx.x >> 6));
+        list_rows(p, (b - p.blocks) * kShrinkWaves + (threadIdx.x >> 6));
         return;
     }
     const int split = int(b % p.splits);
@@ -343,12 +360,185 @@ struct ExpandTile {
     static constexpr int STRIDE = 2 * RP + 8;       // halves to a row in LDS, 16-byte aligned
 };
 
-template <int RP, bool DROP>
-__global__ __launch_bounds__(256) void expand_kernel(const Expand p, int64_t total, int64_t first) {
+// h of an adapter's rows, four threads to a row: summed over the ranges, scaled
+// into fp16's range row by row and split in two.
+template <int RP>
+__device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cnt, int order, bool keep_sum,
+                                             uint16_t* parts, float* back) {
     typedef ExpandTile<RP> T;
-    __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * T::STRIDE];
-    __shared__ __attribute__((aligned(16))) float back[kWindow];
+    const int row = threadIdx.x >> 2, q = threadIdx.x & 3;
+    const int64_t m = m0 + __shfl(order, min(row, cnt - 1));
+    if (row >= (cnt + 15) / 16 * 16) return;   // (whole wavefronts)
+    f4 v[RP / 16];
+#pragma unroll
+    for (int i = 0; i < RP / 16; ++i) v[i] = f4{0.f, 0.f, 0.f, 0.f};
+    const float* h = p.part + m * RP + q * (RP / 4);
+    const int64_t next = int64_t(p.M) * RP;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s, h += next)
+#pragma unroll
+        for (int i = 0; i < RP / 16; ++i) v[i] += *reinterpret_cast<const f4*>(h + 4 * i);
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < RP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = __builtin_fmaxf(most, finite_magnitude(v[i][j]));
+    most = __builtin_fmaxf(most, __shfl_xor(most, 1));
+    most = __builtin_fmaxf(most, __shfl_xor(most, 2));
+    float inverse;
+    const float scale = to_range(most, 13, inverse);
+    if (q == 0) back[row] = inverse;
+    uint16_t* to = parts + row * T::STRIDE + q * (RP / 4);
+#pragma unroll
+    for (int i = 0; i < RP / 16; ++i) {
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split_h(v[i][j] * scale, hi[j], lo[j]);
+        __builtin_memcpy(__builtin_assume_aligned(to + 4 * i, 8), hi, 8);
+        __builtin_memcpy(__builtin_assume_aligned(to + RP + 4 * i, 8), lo, 8);
+    }
+    if (keep_sum && row < cnt)
+#pragma unroll
+        for (int i = 0; i < RP / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = q * (RP / 4) + 4 * i + j;
+                if (r < p.R) p.sum[m * p.R + r] = v[i][j];
+            }
+}
+
+// One adapter's rows, up to 16 MT, against the block's columns.
+template <int RP, int MT, bool DROP>
+__device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, int cnt, int order, int cb,
+                                            uint16_t* parts, float* back) {
+    typedef ExpandTile<RP> T;
+    constexpr int G = MT > 2 ? 2 : MT;   // 16-row tiles whose old values are loaded at a time
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int wave0 = (cb * p.span * 4 + wave) * kCols;   // the wavefront's first column
+    const uint64_t stream = DROP ? wq::drop_stream(p.drop) : 0, eight = uint64_t(m0) * (p.C / 8);
+    const uint16_t* const wb = p.w + int64_t(a) * p.R * p.C;
+    const uint16_t* const ab = p.add + m0 * p.C;
+    uint16_t* const ob = p.out + m0 * p.C;
+    uint32_t row[MT * 4];   // where the lane's rows begin, from the window's first on
+#pragma unroll
+    for (int i = 0; i < MT * 4; ++i)
+        row[i] = uint32_t(__shfl(order, min(16 * (i >> 2) + 4 * g + (i & 3), cnt - 1))) * p.C;
+    constexpr bool AHEAD = RP <= 32;   // w is loaded before h is ready, and a column tile ahead
+    u4 raw[AHEAD ? T::KB : 1][8], old[G * 4];
+    auto load_piece = [&](u4 (&v)[8], int k, int c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i;
+            v[i] = load8(off(wb, uint32_t(min(r, p.R - 1)) * p.C + held(c, p.C)));
+        }
+    };
+    auto load_w = [&](int c) {
+        if constexpr (AHEAD)
+#pragma unroll
+            for (int k = 0; k < T::KB; ++k) load_piece(raw[k], k, c);
+    };
+    auto load_old = [&](int t0, int c) {
+        if (!p.add) return;
+#pragma unroll
+        for (int i = 0; i < G * 4; ++i) old[i] = load8(off(ab, row[t0 * 4 + i] + held(c, p.C)));
+    };
+    // one column tile of the wavefront: its loads are in flight
+    auto tile = [&](int c, bool full, float s, auto&& next) {
+        u4 w[T::KB][8];
+#pragma unroll
+        for (int k = 0; k < T::KB; ++k) {
+            u4(&v)[8] = raw[AHEAD ? k : 0];
+            if constexpr (!AHEAD) load_piece(v, k, c);
+            if (p.R < RP) {   // rows past the rank: zeros, as h is there
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if ((T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i) >= p.R) v[i] = u4{0, 0, 0, 0};
+            }
+            if (!full)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = shifted(v[i], c, p.C);
+            transpose8(v, w[k]);
+        }
+        next();
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if (t > 0 && t % G == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                load_old(t, c);
+            }
+            f4 acc[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+            const uint16_t* h = parts + (16 * t + c16) * T::STRIDE + 8 * g;
+#pragma unroll
+            for (int k = 0; k < T::KB; ++k) {
+                const u4 hi = *reinterpret_cast<const u4*>(h + 32 * k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] = mfma(hi, w[k][j], acc[j]);
+                if constexpr (!T::BOTH) {
+                    const u4 lo = *reinterpret_cast<const u4*>(h + RP + 32 * k);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
+                }
+            }
+            const f4 inverse = *reinterpret_cast<const f4*>(back + 16 * t + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = acc[j][i] * inverse[i] * s;
+                if constexpr (DROP) {
+                    const u4 d = wq::philox(eight + ((row[t * 4 + i] + c) >> 3), stream, p.drop.key0, p.drop.key1);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = wq::kept(d, j, p.drop.t) ? f[j] : 0.f;
+                }
+                if (p.add) {
+                    u4 o = old[t % G * 4 + i];
+                    if (!full) o = shifted(o, c, p.C);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] += wq::h2f(uint16_t(o[j >> 1] >> (16 * (j & 1))));
+                }
+                u4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = wq::f2h(f[2 * j]) | uint32_t(wq::f2h(f[2 * j + 1])) << 16;
+                if (16 * t + 4 * g + i < cnt) {
+                    uint16_t* to = const_cast<uint16_t*>(off(ob, row[t * 4 + i] + c));
+                    if (full)
+                        __builtin_memcpy(to, &v, 16);
+                    else
+                        store8_part(to, v, p.C - c);
+                }
+            }
+        }
+    };
+
+    const bool any = p.out && wave0 < p.C;
+    if (any) {
+        load_w(wave0 + 8 * c16);
+        load_old(0, wave0 + 8 * c16);
+    }
+    expand_parts<RP>(p, m0, cnt, order, p.sum && cb == 0, parts, back);
+    __syncthreads();
+    if (any) {
+        const float s = p.scales[a] * (DROP ? p.drop.keep : 1.f);
+        for (int ct = 0; ct < p.span; ++ct) {
+            const int c0 = wave0 + ct * 4 * kCols, c = c0 + 8 * c16;
+            if (c0 >= p.C) break;
+            const int n0 = c0 + 4 * kCols;
+            if (ct) load_old(0, c);
+            tile(c, c0 + kCols <= p.C, s, [&] {
+                if (ct + 1 < p.span && n0 < p.C) load_w(n0 + 8 * c16);
+            });
+        }
+    }
+    __syncthreads();
+}
+
+template <int RP, bool DROP>
+__global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p, int64_t total, int64_t first) {
+    __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * ExpandTile<RP>::STRIDE];
+    __shared__ __attribute__((aligned(16))) float back[kWindow];
+    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
     // contiguous tiles to an XCD: a window's column blocks share its h
     int64_t b = first + blockIdx.x;
     {
@@ -360,136 +550,31 @@ __global__ __launch_bounds__(256) void expand_kernel(const Expand p, int64_t tot
     const int z = int(b % p.Z);
     const int64_t m0 = b / p.Z * kWindow;
     const int slot = slot_of(p.slots, m0 + lane, p.M, p.L);
-    const int64_t col0 = (int64_t(cb) * p.span * 4 + wave) * kCols + 8 * c16;   // the lane's first column
-    const uint64_t stream = DROP ? wq::drop_stream(p.drop) : 0;
 
     each_adapter(slot, z, p.Z, [&](int a, int cnt, int order) {
-        // h of the adapter's rows, four threads to a row: summed over the
-        // ranges, scaled into fp16's range row by row and split in two
-        {
-            const int row = threadIdx.x >> 2, q = threadIdx.x & 3;
-            const int64_t m = m0 + __shfl(order, row);
-            f4 v[RP / 16];
-#pragma unroll
-            for (int i = 0; i < RP / 16; ++i) v[i] = f4{0.f, 0.f, 0.f, 0.f};
-            if (row < cnt)
-                for (int s = 0; s < p.splits; ++s) {
-                    const float* h = p.part + (int64_t(s) * p.M + m) * RP + q * (RP / 4);
-#pragma unroll
-                    for (int i = 0; i < RP / 16; ++i) v[i] += *reinterpret_cast<const f4*>(h + 4 * i);
-                }
-            float most = 0.f;
-#pragma unroll
-            for (int i = 0; i < RP / 16; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) most = __builtin_fmaxf(most, finite_magnitude(v[i][j]));
-            most = __builtin_fmaxf(most, __shfl_xor(most, 1));
-            most = __builtin_fmaxf(most, __shfl_xor(most, 2));
-            float inverse;
-            const float scale = to_range(most, 13, inverse);
-            if (q == 0) back[row] = inverse;
-            uint16_t* to = parts + row * T::STRIDE + q * (RP / 4);
-#pragma unroll
-            for (int i = 0; i < RP / 16; ++i) {
-                uint16_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) split_h(v[i][j] * scale, hi[j], lo[j]);
-                __builtin_memcpy(__builtin_assume_aligned(to + 4 * i, 8), hi, 8);
-                __builtin_memcpy(__builtin_assume_aligned(to + RP + 4 * i, 8), lo, 8);
-            }
-            if (p.sum && cb == 0 && row < cnt)
-#pragma unroll
-                for (int i = 0; i < RP / 16; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = q * (RP / 4) + 4 * i + j;
-                        if (r < p.R) p.sum[m * p.R + r] = v[i][j];
-                    }
-        }
-        __syncthreads();
-        const float s = p.scales[a] * (DROP ? p.drop.keep : 1.f);
-        const int tiles = (cnt + 15) / 16;
-        for (int ct = 0; ct < p.span; ++ct) {
-            const int64_t c = col0 + int64_t(ct) * 4 * kCols;
-            if (!p.out || c - 8 * c16 >= p.C) break;
-            const int left = int(p.C - c);
-            u4 w[T::KB][8];
-#pragma unroll
-            for (int k = 0; k < T::KB; ++k) {
-                u4 raw[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // (rows past the rank are zeros, not the next adapter's)
-                    const int r = T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i;
-                    raw[i] = load8_part(p.w + (int64_t(a) * p.R + r) * p.C + c, r < p.R ? left : 0);
-                }
-                transpose8(raw, w[k]);
-            }
-            for (int t = 0; t < tiles; ++t) {
-                int64_t m[4];
-                u4 old[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * t + 4 * g + i;
-                    m[i] = m0 + __shfl(order, row);
-                    old[i] = u4{0, 0, 0, 0};
-                    if (p.add && row < cnt) old[i] = load8_part(p.add + m[i] * p.C + c, left);
-                }
-                f4 acc[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
-                const uint16_t* h = parts + (16 * t + c16) * T::STRIDE + 8 * g;
-#pragma unroll
-                for (int k = 0; k < T::KB; ++k) {
-                    const u4 hi = *reinterpret_cast<const u4*>(h + 32 * k);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] = mfma(hi, w[k][j], acc[j]);
-                    if constexpr (!T::BOTH) {
-                        const u4 lo = *reinterpret_cast<const u4*>(h + RP + 32 * k);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
-                    }
-                }
-                const f4 inverse = *reinterpret_cast<const f4*>(back + 16 * t + 4 * g);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (16 * t + 4 * g + i >= cnt) continue;
-                    float f[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = acc[j][i] * inverse[i] * s;
-                    if constexpr (DROP) {
-                        const u4 d = wq::philox((uint64_t(m[i]) * p.C + c) >> 3, stream, p.drop.key0, p.drop.key1);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = wq::kept(d, j, p.drop.t) ? f[j] : 0.f;
-                    }
-                    uint16_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float before = wq::h2f(uint16_t(old[i][j >> 1] >> (16 * (j & 1))));
-                        o[j] = wq::f2h(p.add ? before + f[j] : f[j]);
-                    }
-                    u4 v;
-                    __builtin_memcpy(&v, o, 16);
-                    store8_part(p.out + m[i] * p.C + c, v, left);
-                }
-            }
-        }
-        __syncthreads();
+        if (cnt <= 16)
+            expand_rows<RP, 1, DROP>(p, m0, a, cnt, order, cb, parts, back);
+        else if (cnt <= 32)
+            expand_rows<RP, 2, DROP>(p, m0, a, cnt, order, cb, parts, back);
+        else
+            expand_rows<RP, 4, DROP>(p, m0, a, cnt, order, cb, parts, back);
     });
 
+    const int col0 = (cb * p.span * 4 + int(threadIdx.x >> 6)) * kCols + 8 * c16;
     // rows without an adapter
     const uint64_t none = z == 0 ? __ballot(slot < 0 && m0 + lane < p.M) : 0;
     if (!none) return;
     const int cnt = __builtin_popcountll(none), order = compact(none);
     if (p.out && p.out != p.add)
         for (int ct = 0; ct < p.span; ++ct) {
-            const int64_t c = col0 + int64_t(ct) * 4 * kCols;
+            const int c = col0 + ct * 4 * kCols;
             if (c - 8 * c16 >= p.C) break;
-            const int left = int(p.C - c);
             for (int row = 0; row < cnt; row += 4) {
                 const int64_t m = m0 + __shfl(order, row + g);
                 if (row + g >= cnt) continue;
-                store8_part(p.out + m * p.C + c, p.add ? load8_part(p.add + m * p.C + c, left) : u4{0, 0, 0, 0}, left);
+                u4 v{0, 0, 0, 0};
+                if (p.add) v = shifted(load8(p.add + m * p.C + held(c, p.C)), c, p.C);
+                store8_part(p.out + m * p.C + c, v, p.C - c);
             }
         }
     if (p.sum && cb == 0)
@@ -539,13 +624,14 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
     const int r0 = int(b % p.rchunks) * 64;
     const int a = int(b / p.rchunks);
     const int at = p.start ? p.start[a] : 0, cnt = p.start ? p.start[a + 1] - at : a == 0 ? p.M : 0;
-    const int64_t c = int64_t(tile) * kCols + 8 * c16;
-    const int left = int(j.C - c);
-    const bool drop = j.drop.t != 0;
+    const int c = tile * kCols + 8 * c16, left = j.C - c;
+    const bool full = (tile + 1) * kCols <= j.C, drop = j.drop.t != 0;
     const uint64_t stream = drop ? wq::drop_stream(j.drop) : 0;
     const int steps = (cnt + 31) / 32;
     const int end = int(int64_t(split + 1) * steps / p.splits);
-    const int rl = r0 + NRT * c16;       // the lane's first r; fragment t holds r0 + NRT (l % 16) + t
+    // fragment t holds r0 + NRT (l % 16) + t, a lane's r side by side; for those past
+    // the rank others are taken: what they give is not kept
+    const int held_r = min(r0 + NRT * c16, p.R - NRT);
     f4 acc[NRT][8];
     float mul[NRT];
 #pragma unroll
@@ -559,23 +645,46 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
         const int i0 = st * 32 + 8 * g;
         u4 x[8];
         float h[8][NRT];
+        int64_t m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // (rows past the adapter's repeat its last one)
+            const int n = min(i0 + i, cnt - 1);
+            m[i] = p.list ? p.list[at + n] : n;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool on = i0 + i < cnt;
-            const int64_t m = !on ? 0 : p.list ? p.list[at + i0 + i] : i0 + i;
-            x[i] = load8_part(j.src + m * j.C + c, on ? left : 0);
-            const float* hp = j.h + m * p.R + rl;
-#pragma unroll
-            for (int t = 0; t < NRT; ++t) h[i][t] = 0.f;
-            if (on && rl + NRT <= p.R) {
-                __builtin_memcpy(h[i], hp, 4 * NRT);
-            } else if (on) {
-#pragma unroll
-                for (int t = 0; t < NRT; ++t)
-                    if (rl + t < p.R) h[i][t] = hp[t];
-            }
-            if (drop) x[i] = drop8(x[i], (uint64_t(m) * j.C + c) >> 3, j.drop, stream);
+            x[i] = load8(j.src + m[i] * j.C + held(c, j.C));
+            __builtin_memcpy(h[i], j.h + m[i] * p.R + held_r, 4 * NRT);
         }
+        if (p.R % NRT) {   // a lane whose r's end inside NRT of them took the rank's last NRT
+            const int by = r0 + NRT * c16 - held_r;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v[NRT];
+#pragma unroll
+                for (int t = 0; t < NRT; ++t) {
+                    v[t] = h[i][t];
+#pragma unroll
+                    for (int k = 1; t + k < NRT; ++k) v[t] = by == k ? h[i][t + k] : v[t];
+                }
+#pragma unroll
+                for (int t = 0; t < NRT; ++t) h[i][t] = v[t];
+            }
+        }
+        if (!full)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = shifted(x[i], c, j.C);
+        if (drop)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = drop8(x[i], (uint64_t(m[i]) * j.C + c) >> 3, j.drop, stream);
+        if (st * 32 + 32 > cnt)   // they count as zeros
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i >= cnt) {
+                    x[i] = u4{0, 0, 0, 0};
+#pragma unroll
+                    for (int t = 0; t < NRT; ++t) h[i][t] = 0.f;
+                }
         float most[NRT];
         bool grow = false;
 #pragma unroll
@@ -685,7 +794,7 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(const Outer p, int64_t n
     if (second) q -= n0;
     const OuterJob& j = p.job[second];
     const int64_t size = int64_t(p.L) * p.R * j.C;
-    if (q >= size) return;
+    if (q >= size || (second && j.C < 8)) return;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     const int k = int(min(size - q, int64_t(4)));
     for (int s = 0; s < p.splits; ++s)
@@ -695,6 +804,61 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(const Outer p, int64_t n
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (i < k) j.dw[q + i] = v[i];
+}
+
+// ------------------------------------------------------- narrow projections ----
+//
+// With fewer than eight columns rows are shorter than a load.  One thread to an
+// element; the products have at most seven columns.
+
+// part[0][m][r], columns past R zero, of src [M][C].
+__global__ __launch_bounds__(256) void narrow_shrink_kernel(const Shrink p, int RP, int64_t first) {
+    const int64_t q = (first + blockIdx.x) * 256 + threadIdx.x, m = q / RP;
+    const int r = int(q % RP);
+    if (m >= p.M) return;
+    const int a = slot_of(p.slots, m, p.M, p.L);
+    float v = 0.f;
+    if (a >= 0 && r < p.R)
+        for (int c = 0; c < p.C; ++c)
+            v += wq::h2f(p.src[m * p.C + c]) * wq::h2f(p.w[(int64_t(a) * p.R + r) * p.C + c]);
+    p.part[q] = v;
+}
+__global__ __launch_bounds__(64 * kShrinkWaves) void list_kernel(const Shrink p, int64_t first) {
+    list_rows(p, (first + blockIdx.x) * kShrinkWaves + (threadIdx.x >> 6));
+}
+
+// out of C columns; thread 0 of a row's columns also leaves the row's sums.
+__global__ __launch_bounds__(256) void narrow_expand_kernel(const Expand p, int RP, int64_t first) {
+    const int64_t q = (first + blockIdx.x) * 256 + threadIdx.x, m = q / p.C;
+    const int c = int(q % p.C);
+    if (m >= p.M) return;
+    const int a = slot_of(p.slots, m, p.M, p.L);
+    float v = 0.f;
+    for (int r = 0; r < p.R; ++r) {
+        float h = 0.f;
+        if (a >= 0) {
+            for (int s = 0; s < p.splits; ++s) h += p.part[(int64_t(s) * p.M + m) * RP + r];
+            v += h * wq::h2f(p.w[(int64_t(a) * p.R + r) * p.C + c]);
+        }
+        if (p.sum && c == 0) p.sum[m * p.R + r] = h;
+    }
+    if (a >= 0) v *= p.scales[a];
+    p.out[q] = p.add ? a >= 0 ? wq::f2h(wq::h2f(p.add[q]) + v) : p.add[q] : wq::f2h(v);
+}
+
+// One gradient of C columns, a wavefront to an element.
+__global__ __launch_bounds__(64) void narrow_outer_kernel(const Outer p, int64_t first) {
+    const OuterJob& j = p.job[1];
+    const int64_t q = first + blockIdx.x, ar = q / j.C;
+    const int c = int(q % j.C), a = int(ar / p.R), r = int(ar % p.R);
+    const int at = p.start ? p.start[a] : 0, cnt = p.start ? p.start[a + 1] - at : a == 0 ? p.M : 0;
+    float v = 0.f;
+    for (int i = threadIdx.x; i < cnt; i += 64) {
+        const int64_t m = p.list ? p.list[at + i] : i;
+        v += j.h[m * p.R + r] * wq::h2f(j.src[m * j.C + c]);
+    }
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+    if (threadIdx.x == 0) j.dw[q] = cnt ? v * p.scales[a] : 0.f;
 }
 
 // -------------------------------------------------------------- launches ----
@@ -736,13 +900,23 @@ wq_status shrink(const wqh::Adapters& a, const uint16_t* src, const uint16_t* w,
     const int RP = padded_rank(a.R);
     Shrink p{src, w, a.slots, part, d, a.M, a.R, a.L, C, plan.splits, plan.cps, plan.Z, RP > 64 ? 2 : 1, start, list, 0};
     p.blocks = int64_t(div_up(a.M, kWindow)) * p.splits * p.Z * p.rchunks;
-    const int64_t all = p.blocks + (start ? div_up(a.L, 4) : 0);
+    const int lists = start ? div_up(a.L, kShrinkWaves) : 0;
+    if (C < 8) {   // (N: K is 32 at least, so nothing is dropped)
+        const wq_status st = pieces((int64_t(a.M) * RP + 255) / 256, [&](unsigned blocks, int64_t first) {
+            narrow_shrink_kernel<<<blocks, 256, 0, s>>>(p, RP, first);
+        });
+        if (st != WQ_OK) return st;
+        return pieces(lists, [&](unsigned blocks, int64_t first) {
+            list_kernel<<<blocks, 64 * kShrinkWaves, 0, s>>>(p, first);
+        });
+    }
+    const int64_t all = p.blocks + lists;
     return pieces(all, [&](unsigned blocks, int64_t first) {
         auto go = [&](auto n) {
             if (d.t)
-                shrink_kernel<decltype(n)::value, true><<<blocks, 256, 0, s>>>(p, first);
+                shrink_kernel<decltype(n)::value, true><<<blocks, 64 * kShrinkWaves, 0, s>>>(p, first);
             else
-                shrink_kernel<decltype(n)::value, false><<<blocks, 256, 0, s>>>(p, first);
+                shrink_kernel<decltype(n)::value, false><<<blocks, 64 * kShrinkWaves, 0, s>>>(p, first);
         };
         if (RP == 16)
             go(std::integral_constant<int, 1>{});
@@ -761,6 +935,10 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), windows * wide / 768)));
     p.cblocks = div_up(wide, p.span);
     p.Z = int(std::max<int64_t>(1, std::min<int64_t>(std::min(std::min(a.L, a.M), kWindow), 512 / (windows * p.cblocks))));
+    if (out && C < 8)
+        return pieces((int64_t(a.M) * C + 255) / 256, [&](unsigned blocks, int64_t first) {
+            narrow_expand_kernel<<<blocks, 256, 0, s>>>(p, padded_rank(a.R), first);
+        });
     const int64_t all = windows * p.cblocks * p.Z;
     return pieces(all, [&](unsigned blocks, int64_t first) {
         auto go = [&](auto n) {
@@ -790,7 +968,14 @@ wq_status outer(const wqh::Adapters& a, Outer& p, hipStream_t s) {
     const int64_t per = int64_t(a.L) * p.rchunks * p.splits;
     for (OuterJob& j : p.job) j.tiles = div_up(j.C, kCols);
     p.blocks0 = per * p.job[0].tiles;
-    wq_status st = pieces(p.blocks0 + per * p.job[1].tiles, [&](unsigned blocks, int64_t first) {
+    const bool narrow = p.job[1].C < 8;
+    if (narrow) {
+        const wq_status st = pieces(int64_t(a.L) * a.R * p.job[1].C, [&](unsigned blocks, int64_t first) {
+            narrow_outer_kernel<<<blocks, 64, 0, s>>>(p, first);
+        });
+        if (st != WQ_OK) return st;
+    }
+    wq_status st = pieces(p.blocks0 + (narrow ? 0 : per * p.job[1].tiles), [&](unsigned blocks, int64_t first) {
         if (RP == 16)
             outer_kernel<1><<<blocks, 256, 0, s>>>(p, first);
         else if (RP == 32)
@@ -799,7 +984,7 @@ wq_status outer(const wqh::Adapters& a, Outer& p, hipStream_t s) {
             outer_kernel<4><<<blocks, 256, 0, s>>>(p, first);
     });
     if (st != WQ_OK || p.splits == 1) return st;
-    const int64_t n0 = (int64_t(a.L) * a.R * p.job[0].C + 3) / 4 * 4, n1 = int64_t(a.L) * a.R * p.job[1].C;
+    const int64_t n0 = (int64_t(a.L) * a.R * p.job[0].C + 3) / 4 * 4, n1 = narrow ? 0 : int64_t(a.L) * a.R * p.job[1].C;
     return pieces((n0 + n1 + 1023) / 1024, [&](unsigned blocks, int64_t first) {
         outer_sum_kernel<<<blocks, 256, 0, s>>>(p, n0, first * 256);
     });
