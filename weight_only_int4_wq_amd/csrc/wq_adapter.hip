@@ -36,36 +36,22 @@ __device__ __forceinline__ u4 load8(const uint16_t* p) {
     __builtin_memcpy(&v, p, 16);
     return v;
 }
+__device__ __forceinline__ void store8(uint16_t* p, u4 v) { __builtin_memcpy(p, &v, 16); }
+
 // Within a window or an adapter, element numbers fit 32 bits (64 rows, or 128
 // of the rank, of at most 2^22 columns): a uniform base and a 32-bit offset,
 // which the loads take as they are.
 __device__ __forceinline__ const uint16_t* off(const uint16_t* base, uint32_t n) {
     return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + n * 2u);
 }
-// The last columns of a row of C (at least 8): where a load of eight from
-// column c on would pass the row's end it is taken from C - 8 on, and what comes
-// before c is shifted out.
+__device__ __forceinline__ uint16_t* off(uint16_t* base, uint32_t n) {
+    return reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(base) + n * 2u);
+}
+
+// Where the eight columns of a lane begin that nominally begin at c: the last
+// eight of a row of C (at least 8) take the place of any that would pass its
+// end.  Columns held twice are written twice, the same value, or masked.
 __device__ __forceinline__ int held(int c, int C) { return min(c, C - 8); }
-__device__ __forceinline__ u4 shifted(u4 v, int c, int C) {
-    const int s = c - held(c, C);
-    if (s & 1)
-        v = u4{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
-               __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
-    if (s & 2) v = u4{v[1], v[2], v[3], 0};
-    if (s & 4) v = u4{v[2], v[3], 0, 0};
-    if (s >= 8) v = u4{0, 0, 0, 0};
-    return v;
-}
-// The first n of eight values.
-__device__ __forceinline__ void store8_part(uint16_t* p, u4 v, int n) {
-    if (n >= 8) {
-        __builtin_memcpy(p, &v, 16);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) p[i] = uint16_t(v[i >> 1] >> (16 * (i & 1)));
-}
 
 __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
@@ -73,8 +59,7 @@ __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
 
 // Rows 8 g + i of a fragment's k dimension as 8 loads of 8 neighbouring
 // columns, to the fragments of those columns: fragment j holds column j of the
-// lane's eight (matrix column 8 (l % 16) + j), so a lane ends up with eight
-// neighbouring columns of the result.
+// lane's eight, so a lane ends up with eight neighbouring columns of the result.
 __device__ __forceinline__ void transpose8(const u4 (&row)[8], u4 (&frag)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -84,33 +69,18 @@ __device__ __forceinline__ void transpose8(const u4 (&row)[8], u4 (&frag)[8]) {
                                                j & 1 ? 0x07060302u : 0x05040100u);
 }
 
-typedef uint16_t us2 __attribute__((ext_vector_type(2)));
-
-// All ones in the halves of w that are at least t (t > 0).
-__device__ __forceinline__ uint32_t keep_mask(uint32_t w, us2 below) {
-    const us2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(us2, w), below);  // w - (t - 1), 0 at least
-    const us2 one = __builtin_elementwise_min(over, us2{1, 1});
-    return __builtin_bit_cast(uint32_t, us2{0, 0} - one);
-}
-// Eight values with the dropped ones zeroed; n: the eight's number.
-__device__ __forceinline__ u4 drop8(u4 v, uint64_t n, const Drop& d, uint64_t stream) {
-    const u4 w = wq::philox(n, stream, d.key0, d.key1);
-    const us2 below{uint16_t(d.t - 1), uint16_t(d.t - 1)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] &= keep_mask(w[i], below);
-    return v;
-}
-
 // Lane l's row of a window: its slot, -1 for one without an adapter.
 __device__ __forceinline__ int slot_of(const int32_t* slots, int64_t m, int M, int L) {
     if (m >= M) return -1;
     const int s = slots ? slots[m] : 0;
     return unsigned(s) < unsigned(L) ? s : -1;
 }
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
+}
 // The lanes in `mask` first, in order, then the others: lane i gets the i-th's number.
 __device__ __forceinline__ int compact(uint64_t mask) {
-    const int lane = threadIdx.x & 63;
-    const int below = __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
+    const int lane = threadIdx.x & 63, below = lanes_below(mask);
     const int to = mask >> lane & 1 ? below : __builtin_popcountll(mask) + lane - below;
     return __builtin_amdgcn_ds_permute(to * 4, lane);
 }
@@ -120,11 +90,11 @@ __device__ __forceinline__ int compact(uint64_t mask) {
 template <class Work>
 __device__ __forceinline__ void each_adapter(int slot, int z, int Z, const Work& work) {
     uint64_t todo = __ballot(slot >= 0);
-    for (int n = 0; todo; ++n) {
+    for (int n = 0; todo; n = n + 1 == Z ? 0 : n + 1) {
         const int a = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
         const uint64_t mine = __ballot(slot == a);
         todo &= ~mine;
-        if (n % Z == z) work(a, __builtin_popcountll(mine), compact(mine));
+        if (n == z) work(a, __builtin_popcountll(mine), compact(mine));
     }
 }
 
@@ -140,12 +110,16 @@ __device__ __forceinline__ float finite_magnitude(float v) {
     const float a = __builtin_fabsf(v);
     return a <= 3.402823466e38f ? a : 0.f;
 }
-// v as a sum of two fp16 numbers (an infinity: itself and zero).
-__device__ __forceinline__ void split_h(float v, uint16_t& hi, uint16_t& lo) {
-    const _Float16 h = (_Float16)v;
-    const float f = float(h);
-    hi = __builtin_bit_cast(uint16_t, h);
-    lo = wq::f2h(v == f ? 0.f : v - f);
+typedef float f2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_h(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, wq::h2));
+}
+// a and b as sums of two fp16 numbers each (an infinity: itself and zero).
+__device__ __forceinline__ void split_h(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_h(a, b);
+    const wq::h2 h = wq::as_h2(hi);
+    const float fa = float(h[0]), fb = float(h[1]);
+    lo = pack_h(a == fa ? 0.f : a - fa, b == fb ? 0.f : b - fb);
 }
 
 // --------------------------------------------------------------- shrink ----
@@ -162,7 +136,7 @@ struct Shrink {
     // rows by adapter, for the gradients (null: not wanted)
     int32_t* start;        // [L + 1]
     int32_t* list;         // [M]
-    int64_t blocks;        // of the product; those behind them make the lists
+    int window0;           // of this launch
 };
 
 // Lists of rows by adapter: a wavefront per adapter counts the rows of lower
@@ -200,18 +174,17 @@ __device__ __forceinline__ void list_rows(const Shrink& p, int64_t a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint64_t mask = __ballot(s[u] == a);
-            const int at = less + __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32),
-                                                            __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
-            if (s[u] == a) p.list[at] = int(m + 64 * u + lane);
+            if (s[u] == a) p.list[less + lanes_below(mask)] = int(m + 64 * u + lane);
             less += __builtin_popcountll(mask);
         }
     }
 }
 
-// One adapter's rows of a window against 16 NRT of its rank's rows, over the
-// block's range of columns; the wavefronts take pieces of it in turn, the
-// next one's loads in flight.  Rows past the adapter's repeat its last one, and rows past
-// the rank likewise: they cost no traffic, and what they give is not kept.
+// One adapter's rows of a window, up to 16 MT, against 16 NRT of its rank's
+// rows, over the block's range of columns; the wavefronts take pieces of it in
+// turn, the next one's loads in flight.  Rows past the adapter's repeat its
+// last one, and rows past the rank likewise: they cost no traffic, and what
+// they give is not kept.
 template <int MT, int NRT, bool DROP>
 __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, int cnt, int order, int r0, int split,
                                             f4* sum) {
@@ -245,35 +218,37 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
             for (int t = 0; t < MT; ++t) v.x[t][i] = load8(off(xb, xr[t] + c));
         }
     };
-    auto multiply = [&](int c0, Part& v) {
-        if (c0 + COLS > p.C)
+    const int end = int(min(int64_t(split + 1) * p.cps * kChunk, int64_t(p.C)));
+    constexpr int NEXT = kShrinkWaves * COLS;
+    int c0 = split * p.cps * kChunk + wave * COLS;
+    Part v, next;
+    if (c0 < end) load(c0, v);
+#pragma unroll 1
+    for (; c0 < end; c0 += NEXT) {
+        if (c0 + NEXT < end) load(c0 + NEXT, next);
+        if (c0 + COLS > p.C)   // columns that other lanes hold too: zeros on both sides
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                const int c = c0 + 32 * i + 8 * g;
+                const int twice = c0 + 32 * i + 8 * g - held(c0 + 32 * i + 8 * g, p.C);
+                u4 mask;
 #pragma unroll
-                for (int n = 0; n < NRT; ++n) v.w[n][i] = shifted(v.w[n][i], c, p.C);
+                for (int q = 0; q < 4; ++q)
+                    mask[q] = (twice <= 2 * q ? 0xFFFFu : 0u) | (twice <= 2 * q + 1 ? 0xFFFF0000u : 0u);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) v.x[t][i] = shifted(v.x[t][i], c, p.C);
+                for (int n = 0; n < NRT; ++n) v.w[n][i] &= mask;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) v.x[t][i] &= mask;
             }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i)
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                if constexpr (DROP) v.x[t][i] = drop8(v.x[t][i], eight + ((xr[t] + c0 + 32 * i + 8 * g) >> 3), p.drop, stream);
+                if constexpr (DROP)
+                    v.x[t][i] = wq::drop8(v.x[t][i], eight + ((xr[t] + c0 + 32 * i + 8 * g) >> 3), p.drop, stream);
 #pragma unroll
                 for (int n = 0; n < NRT; ++n) acc[t][n] = mfma(v.x[t][i], v.w[n][i], acc[t][n]);
             }
-    };
-    const int end = int(min(int64_t(split + 1) * p.cps * kChunk, int64_t(p.C)));
-    constexpr int NEXT = kShrinkWaves * COLS;
-    int c0 = split * p.cps * kChunk + wave * COLS;
-    Part v[2];
-    if (c0 < end) load(c0, v[0]);
-    for (; c0 < end; c0 += 2 * NEXT) {
-        if (c0 + NEXT < end) load(c0 + NEXT, v[1]);
-        multiply(c0, v[0]);
-        if (c0 + 2 * NEXT < end) load(c0 + 2 * NEXT, v[0]);
-        if (c0 + NEXT < end) multiply(c0 + NEXT, v[1]);
+        v = next;
     }
 
     // the wavefronts' sums: w and w + 4, then the four in order
@@ -292,47 +267,47 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
             for (int n = 0; n < NRT; ++n) sum[at(t, n, wave)] += acc[t][n];
     __syncthreads();
     const int RP = NRT * 16 * p.rchunks;
+#pragma unroll 1
     for (int e = wave; e < MT * NRT; e += kShrinkWaves) {
         const int t = e / NRT, n = e % NRT, r = r0 + 16 * n + c16;
         f4 v = sum[at(t, n, 0)];
 #pragma unroll
         for (int i = 1; i < HALF; ++i) v += sum[at(t, n, i)];
+        float* to = p.part + (int64_t(split) * p.M + m0) * RP + r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = 16 * t + 4 * g + i;
-            const int64_t m = m0 + __shfl(order, row);
-            if (row < cnt)
-                p.part[(int64_t(split) * p.M + m) * RP + r] = r < p.R ? DROP ? v[i] * p.drop.keep : v[i] : 0.f;
+            const int row = 16 * t + 4 * g + i, m = __shfl(order, row & 63);
+            if (row < cnt) to[m * RP] = r < p.R ? DROP ? v[i] * p.drop.keep : v[i] : 0.f;
         }
     }
     __syncthreads();
 }
 
-// Blocks: for a window, its ranges of columns (neighbouring blocks: the XCDs
-// take them in turn, so that each holds its own range of every adapter in L2),
-// the rank's 64s, and Z shares of its adapters.
-template <int NRT, bool DROP>
-__global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(const Shrink p, int64_t first) {
-    __shared__ f4 sum[4 * NRT * 64 * (kShrinkWaves / 2)];
-    int64_t b = first + blockIdx.x;
-    if (b >= p.blocks) {
-        list_rows(p, (b - p.blocks) * kShrinkWaves + (threadIdx.x >> 6));
+// Blocks: x the ranges of columns (the XCDs take neighbours in turn, so that
+// each holds its own range of every adapter in L2), y the window, z the rank's
+// 64s and Z shares of the window's adapters; behind those the lists' blocks.
+//
+// ONE: the 16-row form alone, for decode batches of many adapters: it leaves
+// registers for more wavefronts, and those blocks wait for a few short loads.
+template <int NRT, bool DROP, bool ONE>
+__global__ __launch_bounds__(64 * kShrinkWaves, NRT > 2 || !ONE ? 2 : 4) void shrink_kernel(const Shrink p) {
+    constexpr int MT = ONE ? 1 : 4;
+    __shared__ f4 sum[MT * NRT * 64 * (kShrinkWaves / 2)];
+    const int zs = p.Z * p.rchunks, bz = blockIdx.z;
+    if (bz >= zs) {
+        const int64_t b = (int64_t(bz - zs) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+        list_rows(p, b * kShrinkWaves + (threadIdx.x >> 6));
         return;
     }
-    const int split = int(b % p.splits);
-    b /= p.splits;
-    const int r0 = int(b % p.rchunks) * 64;
-    b /= p.rchunks;
-    const int z = int(b % p.Z);
-    const int64_t m0 = b / p.Z * kWindow;
+    const int split = blockIdx.x, r0 = p.rchunks > 1 ? (bz & 1) * 64 : 0, z = p.rchunks > 1 ? bz >> 1 : bz;
+    const int64_t m0 = int64_t(p.window0 + int(blockIdx.y)) * kWindow;
     const int slot = slot_of(p.slots, m0 + (threadIdx.x & 63), p.M, p.L);
     each_adapter(slot, z, p.Z, [&](int a, int cnt, int order) {
-        if (cnt <= 16)
-            shrink_rows<1, NRT, DROP>(p, m0, a, cnt, order, r0, split, sum);
-        else if (cnt <= 32)
-            shrink_rows<2, NRT, DROP>(p, m0, a, cnt, order, r0, split, sum);
-        else
-            shrink_rows<4, NRT, DROP>(p, m0, a, cnt, order, r0, split, sum);
+#pragma unroll 1
+        for (; cnt > 0; cnt -= 16 * MT) {
+            shrink_rows<MT, NRT, DROP>(p, m0, a, min(cnt, 16 * MT), order, r0, split, sum);
+            order = __shfl(order, (threadIdx.x + 16 * MT) & 63);
+        }
     });
 }
 
@@ -348,7 +323,9 @@ struct Expand {
     float* sum;            // h [M][R], nullable
     Drop drop;
     int M, R, L, C, splits;
-    int Z, span, cblocks;  // a block's columns: span * 512
+    int Z, halves;         // blocks that share a window's adapters; and an adapter's rows
+    int span;              // a block's columns: span * 512
+    int window0;           // of this launch
 };
 
 template <int RP>
@@ -367,14 +344,15 @@ __device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cn
                                              uint16_t* parts, float* back) {
     typedef ExpandTile<RP> T;
     const int row = threadIdx.x >> 2, q = threadIdx.x & 3;
-    const int64_t m = m0 + __shfl(order, min(row, cnt - 1));
     if (row >= (cnt + 15) / 16 * 16) return;   // (whole wavefronts)
+    const int64_t m = m0 + __shfl(order, min(row, cnt - 1));
     f4 v[RP / 16];
 #pragma unroll
     for (int i = 0; i < RP / 16; ++i) v[i] = f4{0.f, 0.f, 0.f, 0.f};
     const float* h = p.part + m * RP + q * (RP / 4);
     const int64_t next = int64_t(p.M) * RP;
-#pragma unroll 4
+    constexpr int U = RP > 32 ? 2 : 4;
+#pragma unroll U
     for (int s = 0; s < p.splits; ++s, h += next)
 #pragma unroll
         for (int i = 0; i < RP / 16; ++i) v[i] += *reinterpret_cast<const f4*>(h + 4 * i);
@@ -388,48 +366,45 @@ __device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cn
     float inverse;
     const float scale = to_range(most, 13, inverse);
     if (q == 0) back[row] = inverse;
-    uint16_t* to = parts + row * T::STRIDE + q * (RP / 4);
+    uint32_t* to = reinterpret_cast<uint32_t*>(parts + row * T::STRIDE + q * (RP / 4));
 #pragma unroll
-    for (int i = 0; i < RP / 16; ++i) {
-        uint16_t hi[4], lo[4];
+    for (int i = 0; i < RP / 16; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split_h(v[i][j] * scale, hi[j], lo[j]);
-        __builtin_memcpy(__builtin_assume_aligned(to + 4 * i, 8), hi, 8);
-        __builtin_memcpy(__builtin_assume_aligned(to + RP + 4 * i, 8), lo, 8);
-    }
-    if (keep_sum && row < cnt)
+        for (int j = 0; j < 2; ++j)
+            split_h(v[i][2 * j] * scale, v[i][2 * j + 1] * scale, to[2 * i + j], to[RP / 2 + 2 * i + j]);
+    if (keep_sum && row < cnt) {
+        float* at = p.sum + m * p.R;
 #pragma unroll
         for (int i = 0; i < RP / 16; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = q * (RP / 4) + 4 * i + j;
-                if (r < p.R) p.sum[m * p.R + r] = v[i][j];
+                if (r < p.R) at[r] = v[i][j];
             }
+    }
 }
 
-// One adapter's rows, up to 16 MT, against the block's columns.
-template <int RP, int MT, bool DROP>
-__device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, int cnt, int order, int cb,
-                                            uint16_t* parts, float* back) {
+// One adapter's rows against the block's columns.
+template <int RP, bool DROP>
+__device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, int cnt, int order, uint16_t* parts,
+                                            float* back) {
     typedef ExpandTile<RP> T;
-    constexpr int G = MT > 2 ? 2 : MT;   // 16-row tiles whose old values are loaded at a time
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
-    const int wave0 = (cb * p.span * 4 + wave) * kCols;   // the wavefront's first column
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4, cb = blockIdx.y;
     const uint64_t stream = DROP ? wq::drop_stream(p.drop) : 0, eight = uint64_t(m0) * (p.C / 8);
     const uint16_t* const wb = p.w + int64_t(a) * p.R * p.C;
     const uint16_t* const ab = p.add + m0 * p.C;
     uint16_t* const ob = p.out + m0 * p.C;
-    uint32_t row[MT * 4];   // where the lane's rows begin, from the window's first on
+    const int wave0 = (cb * p.span * 4 + wave) * kCols;   // the wavefront's first column
+    const int tiles = (cnt + 15) / 16;
+    constexpr bool AHEAD = RP <= 32;   // w and the first old values are loaded before h is ready
+    u4 raw[AHEAD ? T::KB : 1][8], old[4], fetched[4];
 #pragma unroll
-    for (int i = 0; i < MT * 4; ++i)
-        row[i] = uint32_t(__shfl(order, min(16 * (i >> 2) + 4 * g + (i & 3), cnt - 1))) * p.C;
-    constexpr bool AHEAD = RP <= 32;   // w is loaded before h is ready, and a column tile ahead
-    u4 raw[AHEAD ? T::KB : 1][8], old[G * 4];
+    for (int i = 0; i < 4; ++i) old[i] = u4{0, 0, 0, 0};
     auto load_piece = [&](u4 (&v)[8], int k, int c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i;
-            v[i] = load8(off(wb, uint32_t(min(r, p.R - 1)) * p.C + held(c, p.C)));
+            v[i] = load8(off(wb, uint32_t(min(r, p.R - 1)) * p.C + c));
         }
     };
     auto load_w = [&](int c) {
@@ -437,147 +412,133 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
 #pragma unroll
             for (int k = 0; k < T::KB; ++k) load_piece(raw[k], k, c);
     };
-    auto load_old = [&](int t0, int c) {
-        if (!p.add) return;
+    // where row 16 t + 4 g + i begins, from the window's first on
+    auto row_at = [&](int t, int i) { return uint32_t(__shfl(order, min(16 * t + 4 * g + i, cnt - 1))) * p.C; };
+    auto load_old = [&](u4 (&v)[4], int t, int c) {
+        if (p.add)
 #pragma unroll
-        for (int i = 0; i < G * 4; ++i) old[i] = load8(off(ab, row[t0 * 4 + i] + held(c, p.C)));
-    };
-    // one column tile of the wavefront: its loads are in flight
-    auto tile = [&](int c, bool full, float s, auto&& next) {
-        u4 w[T::KB][8];
-#pragma unroll
-        for (int k = 0; k < T::KB; ++k) {
-            u4(&v)[8] = raw[AHEAD ? k : 0];
-            if constexpr (!AHEAD) load_piece(v, k, c);
-            if (p.R < RP) {   // rows past the rank: zeros, as h is there
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if ((T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i) >= p.R) v[i] = u4{0, 0, 0, 0};
-            }
-            if (!full)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = shifted(v[i], c, p.C);
-            transpose8(v, w[k]);
-        }
-        next();
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if (t > 0 && t % G == 0) {
-                __builtin_amdgcn_sched_barrier(0);
-                load_old(t, c);
-            }
-            f4 acc[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
-            const uint16_t* h = parts + (16 * t + c16) * T::STRIDE + 8 * g;
-#pragma unroll
-            for (int k = 0; k < T::KB; ++k) {
-                const u4 hi = *reinterpret_cast<const u4*>(h + 32 * k);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] = mfma(hi, w[k][j], acc[j]);
-                if constexpr (!T::BOTH) {
-                    const u4 lo = *reinterpret_cast<const u4*>(h + RP + 32 * k);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
-                }
-            }
-            const f4 inverse = *reinterpret_cast<const f4*>(back + 16 * t + 4 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = acc[j][i] * inverse[i] * s;
-                if constexpr (DROP) {
-                    const u4 d = wq::philox(eight + ((row[t * 4 + i] + c) >> 3), stream, p.drop.key0, p.drop.key1);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = wq::kept(d, j, p.drop.t) ? f[j] : 0.f;
-                }
-                if (p.add) {
-                    u4 o = old[t % G * 4 + i];
-                    if (!full) o = shifted(o, c, p.C);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] += wq::h2f(uint16_t(o[j >> 1] >> (16 * (j & 1))));
-                }
-                u4 v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = wq::f2h(f[2 * j]) | uint32_t(wq::f2h(f[2 * j + 1])) << 16;
-                if (16 * t + 4 * g + i < cnt) {
-                    uint16_t* to = const_cast<uint16_t*>(off(ob, row[t * 4 + i] + c));
-                    if (full)
-                        __builtin_memcpy(to, &v, 16);
-                    else
-                        store8_part(to, v, p.C - c);
-                }
-            }
-        }
+            for (int i = 0; i < 4; ++i) v[i] = load8(off(ab, row_at(t, i) + c));
     };
 
     const bool any = p.out && wave0 < p.C;
     if (any) {
-        load_w(wave0 + 8 * c16);
-        load_old(0, wave0 + 8 * c16);
+        const int c = held(wave0 + 8 * c16, p.C);
+        load_w(c);
+        load_old(old, 0, c);
     }
     expand_parts<RP>(p, m0, cnt, order, p.sum && cb == 0, parts, back);
     __syncthreads();
     if (any) {
         const float s = p.scales[a] * (DROP ? p.drop.keep : 1.f);
+#pragma unroll 1
         for (int ct = 0; ct < p.span; ++ct) {
-            const int c0 = wave0 + ct * 4 * kCols, c = c0 + 8 * c16;
+            const int c0 = wave0 + ct * 4 * kCols, c = held(c0 + 8 * c16, p.C);
             if (c0 >= p.C) break;
-            const int n0 = c0 + 4 * kCols;
-            if (ct) load_old(0, c);
-            tile(c, c0 + kCols <= p.C, s, [&] {
-                if (ct + 1 < p.span && n0 < p.C) load_w(n0 + 8 * c16);
-            });
+            if (ct) {
+                load_w(c);
+                load_old(old, 0, c);
+            }
+            u4 w[T::KB][8];
+#pragma unroll
+            for (int k = 0; k < T::KB; ++k) {
+                u4(&v)[8] = raw[AHEAD ? k : 0];
+                if constexpr (!AHEAD) load_piece(v, k, c);
+                if (p.R < RP) {   // rows past the rank: zeros, as h is there
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if ((T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i) >= p.R) v[i] = u4{0, 0, 0, 0};
+                }
+                transpose8(v, w[k]);
+            }
+#pragma unroll 1
+            for (int t = 0; t < tiles; ++t) {
+                if (t + 1 < tiles) load_old(fetched, t + 1, c);
+                f4 acc[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+                const uint16_t* h = parts + (16 * t + c16) * T::STRIDE + 8 * g;
+#pragma unroll
+                for (int k = 0; k < T::KB; ++k) {
+                    const u4 hi = *reinterpret_cast<const u4*>(h + 32 * k);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] = mfma(hi, w[k][j], acc[j]);
+                    if constexpr (!T::BOTH) {
+                        const u4 lo = *reinterpret_cast<const u4*>(h + RP + 32 * k);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
+                    }
+                }
+                const f4 inverse = *reinterpret_cast<const f4*>(back + 16 * t + 4 * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t at = row_at(t, i) + c;
+                    // (a power of two: exact but where the result is below fp16's numbers anyway)
+                    const float f = inverse[i] * s;
+                    u4 v;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const wq::h2 o = wq::as_h2(old[i][j]);
+                        v[j] = pack_h(__builtin_fmaf(acc[2 * j][i], f, float(o[0])),
+                                      __builtin_fmaf(acc[2 * j + 1][i], f, float(o[1])));
+                    }
+                    if constexpr (DROP) {
+                        const u4 keep = wq::keep8(eight + (at >> 3), p.drop, stream);
+                        v = (v & keep) | (old[i] & ~keep);
+                    }
+                    if (16 * t + 4 * g + i >= cnt) continue;
+                    if (p.C - 8 >= c0) {
+                        store8(off(ob, at), v);
+                    } else {   // the last, fewer than eight columns: those before c0 are another tile's
+#pragma unroll
+                        for (int j = 1; j < 8; ++j)
+                            if (c + j >= c0) off(ob, at)[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) old[i] = p.add ? fetched[i] : u4{0, 0, 0, 0};
+            }
         }
     }
     __syncthreads();
 }
 
+// Blocks: x the window (neighbours on different XCDs, a window's column blocks
+// on one, so that its h comes from memory once), y the column block, z the
+// halves of an adapter's rows and Z shares of the window's adapters.
 template <int RP, bool DROP>
-__global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p, int64_t total, int64_t first) {
+__global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p) {
     __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * ExpandTile<RP>::STRIDE];
     __shared__ __attribute__((aligned(16))) float back[kWindow];
-    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-    // contiguous tiles to an XCD: a window's column blocks share its h
-    int64_t b = first + blockIdx.x;
-    {
-        const int64_t q = total / 8, r = total % 8, x = b % 8, k = b / 8;
-        b = x < r ? x * (q + 1) + k : r * (q + 1) + (x - r) * q + k;
-    }
-    const int cb = int(b % p.cblocks);
-    b /= p.cblocks;
-    const int z = int(b % p.Z);
-    const int64_t m0 = b / p.Z * kWindow;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int half = p.halves > 1 ? blockIdx.z & 1 : 0, z = p.halves > 1 ? blockIdx.z >> 1 : blockIdx.z;
+    const int64_t m0 = int64_t(p.window0 + int(blockIdx.x)) * kWindow;
     const int slot = slot_of(p.slots, m0 + lane, p.M, p.L);
-
+    // the half's rows of what compact gave, at the front
+    auto mine = [&](int& cnt, int& order) {
+        if (p.halves == 1) return;
+        order = __shfl(order, (lane + half * (kWindow / 2)) & 63);
+        cnt = min(cnt - half * (kWindow / 2), kWindow / 2);
+    };
     each_adapter(slot, z, p.Z, [&](int a, int cnt, int order) {
-        if (cnt <= 16)
-            expand_rows<RP, 1, DROP>(p, m0, a, cnt, order, cb, parts, back);
-        else if (cnt <= 32)
-            expand_rows<RP, 2, DROP>(p, m0, a, cnt, order, cb, parts, back);
-        else
-            expand_rows<RP, 4, DROP>(p, m0, a, cnt, order, cb, parts, back);
+        mine(cnt, order);
+        if (cnt > 0) expand_rows<RP, DROP>(p, m0, a, cnt, order, parts, back);
     });
 
-    const int col0 = (cb * p.span * 4 + int(threadIdx.x >> 6)) * kCols + 8 * c16;
     // rows without an adapter
     const uint64_t none = z == 0 ? __ballot(slot < 0 && m0 + lane < p.M) : 0;
     if (!none) return;
-    const int cnt = __builtin_popcountll(none), order = compact(none);
+    int cnt = __builtin_popcountll(none), order = compact(none);
+    mine(cnt, order);
     if (p.out && p.out != p.add)
         for (int ct = 0; ct < p.span; ++ct) {
-            const int c = col0 + ct * 4 * kCols;
-            if (c - 8 * c16 >= p.C) break;
+            const int c0 = ((int(blockIdx.y) * p.span + ct) * 4 + wave) * kCols, c = held(c0 + 8 * c16, p.C);
+            if (c0 >= p.C) break;
             for (int row = 0; row < cnt; row += 4) {
-                const int64_t m = m0 + __shfl(order, row + g);
-                if (row + g >= cnt) continue;
-                u4 v{0, 0, 0, 0};
-                if (p.add) v = shifted(load8(p.add + m * p.C + held(c, p.C)), c, p.C);
-                store8_part(p.out + m * p.C + c, v, p.C - c);
+                const int64_t at = (m0 + __shfl(order, min(row + g, cnt - 1))) * p.C + c;
+                store8(p.out + at, p.add ? load8(p.add + at) : u4{0, 0, 0, 0});
             }
         }
-    if (p.sum && cb == 0)
+    if (p.sum && blockIdx.y == 0)
         for (int i0 = 0; i0 < cnt * p.R; i0 += 256) {
             const int i = i0 + threadIdx.x;
             const int64_t m = m0 + __shfl(order, (i / p.R) & 63);
@@ -594,7 +555,7 @@ struct OuterJob {
     float* dw;
     float* part;           // [splits][L][R][C] where splits > 1
     Drop drop;
-    int C, tiles;  // tiles of 128 columns
+    int C, tiles;          // tiles of 128 columns
 };
 struct Outer {
     OuterJob job[2];
@@ -602,30 +563,27 @@ struct Outer {
     const int32_t* start;  // [L + 1], null: adapter 0 takes every row
     const int32_t* list;
     int M, R, L, splits, rchunks;
-    int64_t blocks0;       // blocks of job 0
+    int adapter0;          // of this launch
 };
 
 // Rows of one adapter, 32 to a matrix step, against 128 columns: a block's
 // wavefronts take steps in turn.  h is brought into fp16's range for each of its
 // columns r, by a power of two that follows the largest magnitude so far, with
 // room for it to grow 2^5 times before the sums are rescaled.
+// Blocks: x the column tiles of both gradients, y the range of rows, z the
+// rank's 64s and the adapter.
 template <int NRT>
-__global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first) {
+__global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     __shared__ f4 sums[2 * NRT * 8 * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
-    int64_t b = first + blockIdx.x;
-    const bool second = b >= p.blocks0;
-    if (second) b -= p.blocks0;
+    const bool second = int(blockIdx.x) >= p.job[0].tiles;
     const OuterJob& j = p.job[second];
-    const int tile = int(b % j.tiles);
-    b /= j.tiles;
-    const int split = int(b % p.splits);
-    b /= p.splits;
-    const int r0 = int(b % p.rchunks) * 64;
-    const int a = int(b / p.rchunks);
+    const int tile = blockIdx.x - (second ? p.job[0].tiles : 0), split = blockIdx.y;
+    const int r0 = p.rchunks > 1 ? (blockIdx.z & 1) * 64 : 0;
+    const int a = p.adapter0 + int(p.rchunks > 1 ? blockIdx.z >> 1 : blockIdx.z);
     const int at = p.start ? p.start[a] : 0, cnt = p.start ? p.start[a + 1] - at : a == 0 ? p.M : 0;
-    const int c = tile * kCols + 8 * c16, left = j.C - c;
-    const bool full = (tile + 1) * kCols <= j.C, drop = j.drop.t != 0;
+    const int c = held(tile * kCols + 8 * c16, j.C);
+    const bool drop = j.drop.t != 0;
     const uint64_t stream = drop ? wq::drop_stream(j.drop) : 0;
     const int steps = (cnt + 31) / 32;
     const int end = int(int64_t(split + 1) * steps / p.splits);
@@ -641,11 +599,12 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
         for (int i = 0; i < 8; ++i) acc[t][i] = f4{0.f, 0.f, 0.f, 0.f};
     }
 
+#pragma unroll 1
     for (int st = int(int64_t(split) * steps / p.splits) + wave; st < end; st += 4) {
         const int i0 = st * 32 + 8 * g;
         u4 x[8];
         float h[8][NRT];
-        int64_t m[8];
+        int m[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {   // (rows past the adapter's repeat its last one)
             const int n = min(i0 + i, cnt - 1);
@@ -653,8 +612,8 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x[i] = load8(j.src + m[i] * j.C + held(c, j.C));
-            __builtin_memcpy(h[i], j.h + m[i] * p.R + held_r, 4 * NRT);
+            x[i] = load8(j.src + int64_t(m[i]) * j.C + c);
+            __builtin_memcpy(h[i], j.h + int64_t(m[i]) * p.R + held_r, 4 * NRT);
         }
         if (p.R % NRT) {   // a lane whose r's end inside NRT of them took the rank's last NRT
             const int by = r0 + NRT * c16 - held_r;
@@ -671,12 +630,9 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
                 for (int t = 0; t < NRT; ++t) h[i][t] = v[t];
             }
         }
-        if (!full)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = shifted(x[i], c, j.C);
         if (drop)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = drop8(x[i], (uint64_t(m[i]) * j.C + c) >> 3, j.drop, stream);
+            for (int i = 0; i < 8; ++i) x[i] &= wq::keep8((uint64_t(m[i]) * j.C + c) >> 3, j.drop, stream);
         if (st * 32 + 32 > cnt)   // they count as zeros
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -719,16 +675,18 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
 #pragma unroll
         for (int t = 0; t < NRT; ++t) {
             const float scale = mul[t] == 0.f ? 1.f : mul[t];
-            uint16_t hi[8], lo[8];
+            u4 hi, lo;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) split_h(h[i][t] * scale, hi[i], lo[i]);
-            u4 vh, vl;
-            __builtin_memcpy(&vh, hi, 16);
-            __builtin_memcpy(&vl, lo, 16);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a, b;
+                split_h(h[2 * i][t] * scale, h[2 * i + 1][t] * scale, a, b);
+                hi[i] = a;
+                lo[i] = b;
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[t][k] = mfma(vh, w[k], acc[t][k]);
+            for (int k = 0; k < 8; ++k) acc[t][k] = mfma(hi, w[k], acc[t][k]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[t][k] = mfma(vl, w[k], acc[t][k]);
+            for (int k = 0; k < 8; ++k) acc[t][k] = mfma(lo, w[k], acc[t][k]);
         }
     }
 
@@ -756,34 +714,27 @@ __global__ __launch_bounds__(256) void outer_kernel(const Outer p, int64_t first
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[t][k] += from[(t * 8 + k) * 64 + lane];
     };
-    f4* const half = sums + NRT * 8 * 64;
-    if (wave >= 2) give(wave == 2 ? sums : half);
+    f4* const other = sums + NRT * 8 * 64;
+    if (wave >= 2) give(wave == 2 ? sums : other);
     __syncthreads();
-    if (wave < 2) take(wave == 0 ? sums : half);
+    if (wave < 2) take(wave == 0 ? sums : other);
     __syncthreads();
     if (wave == 1) give(sums);
     __syncthreads();
     if (wave != 0) return;
     take(sums);
 
-    float* to = p.splits > 1 ? j.part + int64_t(split) * p.L * p.R * j.C : j.dw;
+    float* to = (p.splits > 1 ? j.part + int64_t(split) * p.L * p.R * j.C : j.dw) + int64_t(a) * p.R * j.C + c;
 #pragma unroll
     for (int t = 0; t < NRT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = r0 + NRT * (4 * g + i) + t;
             if (r >= p.R) continue;
-            float* row = to + (int64_t(a) * p.R + r) * j.C + c;
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = acc[t][k][i] * s;
-            if (left >= 8) {
-                __builtin_memcpy(row, v, 32);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 7; ++k)
-                    if (k < left) row[k] = v[k];
-            }
+            __builtin_memcpy(to + int64_t(r) * j.C, v, 32);
         }
 }
 
@@ -795,15 +746,23 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(const Outer p, int64_t n
     const OuterJob& j = p.job[second];
     const int64_t size = int64_t(p.L) * p.R * j.C;
     if (q >= size || (second && j.C < 8)) return;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const int k = int(min(size - q, int64_t(4)));
-    for (int s = 0; s < p.splits; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < k) v[i] += j.part[s * size + q + i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < k) j.dw[q + i] = v[i];
+    f4 v{0.f, 0.f, 0.f, 0.f};
+    if (size - q >= 4) {
+        const float* at = j.part + q;
+#pragma unroll 8
+        for (int s = 0; s < p.splits; ++s, at += size) {
+            f4 w;
+            __builtin_memcpy(&w, at, 16);
+            v += w;
+        }
+        __builtin_memcpy(j.dw + q, &v, 16);
+        return;
+    }
+    for (int64_t i = q; i < size; ++i) {
+        float w = 0.f;
+        for (int s = 0; s < p.splits; ++s) w += j.part[s * size + i];
+        j.dw[i] = w;
+    }
 }
 
 // ------------------------------------------------------- narrow projections ----
@@ -870,14 +829,25 @@ size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// launch(now, first) for 0 .. total - 1, at most `most` at a time.
 template <class Launch>
-wq_status pieces(int64_t blocks, const Launch& launch) {
-    for (int64_t first = 0; first < blocks; first += wqh::kMaxBlocks) {
-        launch(unsigned(std::min<int64_t>(blocks - first, wqh::kMaxBlocks)), first);
+wq_status pieces(int64_t total, int64_t most, const Launch& launch) {
+    for (int64_t first = 0; first < total; first += most) {
+        launch(unsigned(std::min(total - first, most)), first);
         const wq_status st = wqh::launch_status();
         if (st != WQ_OK) return st;
     }
     return WQ_OK;
+}
+constexpr int kMaxY = 65535;   // blocks of a launch in y or z
+
+// How many blocks share the work of a window whose adapters are not known here,
+// where `blocks` alone leave units idle.
+int shares(int M, int L, int64_t blocks, int want) {
+    return int(std::max<int64_t>(1, std::min<int64_t>(std::min(std::min(L, M), kWindow), want / blocks)));
 }
 
 // Ranges of the long side of a shrink, and the blocks that share a window.
@@ -886,10 +856,10 @@ struct ShrinkPlan {
     ShrinkPlan(int M, int R, int L, int C) {
         const int chunks = div_up(C, kChunk), rchunks = padded_rank(R) > 64 ? 2 : 1;
         const int64_t base = int64_t(div_up(M, kWindow)) * rchunks;
-        const int want = int(std::min<int64_t>(std::max<int64_t>(768 / base, 1), 32));
+        const int want = int(std::min<int64_t>(std::max<int64_t>(512 / base, 1), 32));
         cps = div_up(chunks, std::min(want, div_up(chunks, 4)));
         splits = div_up(chunks, cps);
-        Z = int(std::max<int64_t>(1, std::min<int64_t>(std::min(std::min(L, M), kWindow), 768 / (base * splits))));
+        Z = shares(M, L, base * splits, 256);
     }
     size_t bytes(int M, int R) const { return round256(size_t(splits) * M * padded_rank(R) * 4); }
 };
@@ -899,59 +869,70 @@ wq_status shrink(const wqh::Adapters& a, const uint16_t* src, const uint16_t* w,
     const ShrinkPlan plan(a.M, a.R, a.L, C);
     const int RP = padded_rank(a.R);
     Shrink p{src, w, a.slots, part, d, a.M, a.R, a.L, C, plan.splits, plan.cps, plan.Z, RP > 64 ? 2 : 1, start, list, 0};
-    p.blocks = int64_t(div_up(a.M, kWindow)) * p.splits * p.Z * p.rchunks;
     const int lists = start ? div_up(a.L, kShrinkWaves) : 0;
+    constexpr int T = 64 * kShrinkWaves;
     if (C < 8) {   // (N: K is 32 at least, so nothing is dropped)
-        const wq_status st = pieces((int64_t(a.M) * RP + 255) / 256, [&](unsigned blocks, int64_t first) {
-            narrow_shrink_kernel<<<blocks, 256, 0, s>>>(p, RP, first);
+        const wq_status st = pieces((int64_t(a.M) * RP + 255) / 256, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
+            narrow_shrink_kernel<<<now, 256, 0, s>>>(p, RP, first);
         });
         if (st != WQ_OK) return st;
-        return pieces(lists, [&](unsigned blocks, int64_t first) {
-            list_kernel<<<blocks, 64 * kShrinkWaves, 0, s>>>(p, first);
+        return pieces(lists, wqh::kMaxBlocks / 2, [&](unsigned now, int64_t first) {
+            list_kernel<<<now, T, 0, s>>>(p, first);
         });
     }
-    const int64_t all = p.blocks + lists;
-    return pieces(all, [&](unsigned blocks, int64_t first) {
+    const bool one = a.M <= 16 || (a.slots && a.L > 1 && a.M <= 256);
+    return pieces(div_up(a.M, kWindow), kMaxY, [&](unsigned windows, int64_t first) {
+        p.window0 = int(first);
+        dim3 grid(unsigned(p.splits), windows, unsigned(p.Z * p.rchunks));
+        if (first == 0)
+            grid.z += unsigned(div_up(lists, int64_t(p.splits) * windows));
         auto go = [&](auto n) {
-            if (d.t)
-                shrink_kernel<decltype(n)::value, true><<<blocks, 64 * kShrinkWaves, 0, s>>>(p, first);
+            constexpr int NRT = decltype(n)::value;
+            if (one && !d.t)
+                shrink_kernel<NRT, false, true><<<grid, T, 0, s>>>(p);
+            else if (one)
+                shrink_kernel<NRT, true, true><<<grid, T, 0, s>>>(p);
+            else if (!d.t)
+                shrink_kernel<NRT, false, false><<<grid, T, 0, s>>>(p);
             else
-                shrink_kernel<decltype(n)::value, false><<<blocks, 64 * kShrinkWaves, 0, s>>>(p, first);
+                shrink_kernel<NRT, true, false><<<grid, T, 0, s>>>(p);
         };
         if (RP == 16)
-            go(std::integral_constant<int, 1>{});
+            go(Int<1>{});
         else if (RP == 32)
-            go(std::integral_constant<int, 2>{});
+            go(Int<2>{});
         else
-            go(std::integral_constant<int, 4>{});
+            go(Int<4>{});
     });
 }
 
 wq_status expand(const wqh::Adapters& a, const float* part, int splits, const uint16_t* w, const Drop& d,
                  const uint16_t* add, uint16_t* out, float* sum, int C, hipStream_t s) {
+    Expand p{part, w, a.scales, a.slots, add, out, sum, d, a.M, a.R, a.L, C, splits, 1, 1, 1, 0};
+    if (out && C < 8)
+        return pieces((int64_t(a.M) * C + 255) / 256, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
+            narrow_expand_kernel<<<now, 256, 0, s>>>(p, padded_rank(a.R), first);
+        });
     const int64_t windows = div_up(a.M, kWindow);
     const int wide = out ? div_up(C, 4 * kCols) : 1;   // blocks of 512 columns
-    Expand p{part, w, a.scales, a.slots, add, out, sum, d, a.M, a.R, a.L, C, splits, 1, 1, 1};
-    p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), windows * wide / 768)));
-    p.cblocks = div_up(wide, p.span);
-    p.Z = int(std::max<int64_t>(1, std::min<int64_t>(std::min(std::min(a.L, a.M), kWindow), 512 / (windows * p.cblocks))));
-    if (out && C < 8)
-        return pieces((int64_t(a.M) * C + 255) / 256, [&](unsigned blocks, int64_t first) {
-            narrow_expand_kernel<<<blocks, 256, 0, s>>>(p, padded_rank(a.R), first);
-        });
-    const int64_t all = windows * p.cblocks * p.Z;
-    return pieces(all, [&](unsigned blocks, int64_t first) {
+    p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), windows * wide / 1024)));
+    const int cblocks = div_up(wide, p.span);
+    p.halves = a.M > kWindow / 2 && windows * cblocks < 512 ? 2 : 1;
+    p.Z = shares(a.M, a.L, windows * cblocks * p.halves, 512);
+    return pieces(windows, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
+        p.window0 = int(first);
+        const dim3 grid(now, unsigned(cblocks), unsigned(p.Z * p.halves));
         auto go = [&](auto n) {
             if (d.t)
-                expand_kernel<decltype(n)::value, true><<<blocks, 256, 0, s>>>(p, all, first);
+                expand_kernel<decltype(n)::value, true><<<grid, 256, 0, s>>>(p);
             else
-                expand_kernel<decltype(n)::value, false><<<blocks, 256, 0, s>>>(p, all, first);
+                expand_kernel<decltype(n)::value, false><<<grid, 256, 0, s>>>(p);
         };
         switch (padded_rank(a.R)) {
-            case 16: go(std::integral_constant<int, 16>{}); break;
-            case 32: go(std::integral_constant<int, 32>{}); break;
-            case 64: go(std::integral_constant<int, 64>{}); break;
-            default: go(std::integral_constant<int, 128>{});
+            case 16: go(Int<16>{}); break;
+            case 32: go(Int<32>{}); break;
+            case 64: go(Int<64>{}); break;
+            default: go(Int<128>{});
         }
     });
 }
@@ -959,34 +940,36 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
 // Ranges of rows of the gradients.
 int outer_splits(int M, int R, int L, int K, int N) {
     const int64_t blocks = int64_t(L) * (padded_rank(R) > 64 ? 2 : 1) * (div_up(K, kCols) + div_up(N, kCols));
-    return int(std::max<int64_t>(1, std::min<int64_t>(std::min(div_up(M, 128), 32), 768 / blocks)));
+    return int(std::max<int64_t>(1, std::min<int64_t>(std::min(div_up(M, 128), 32), 1024 / blocks)));
 }
 
 wq_status outer(const wqh::Adapters& a, Outer& p, hipStream_t s) {
     const int RP = padded_rank(a.R);
     p.rchunks = RP > 64 ? 2 : 1;
-    const int64_t per = int64_t(a.L) * p.rchunks * p.splits;
-    for (OuterJob& j : p.job) j.tiles = div_up(j.C, kCols);
-    p.blocks0 = per * p.job[0].tiles;
     const bool narrow = p.job[1].C < 8;
+    for (OuterJob& j : p.job) j.tiles = div_up(j.C, kCols);
     if (narrow) {
-        const wq_status st = pieces(int64_t(a.L) * a.R * p.job[1].C, [&](unsigned blocks, int64_t first) {
-            narrow_outer_kernel<<<blocks, 64, 0, s>>>(p, first);
+        const wq_status st = pieces(int64_t(a.L) * a.R * p.job[1].C, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
+            narrow_outer_kernel<<<now, 64, 0, s>>>(p, first);
         });
         if (st != WQ_OK) return st;
     }
-    wq_status st = pieces(p.blocks0 + (narrow ? 0 : per * p.job[1].tiles), [&](unsigned blocks, int64_t first) {
+    const unsigned tiles = unsigned(p.job[0].tiles + (narrow ? 0 : p.job[1].tiles));
+    wq_status st = pieces(a.L, kMaxY / 2, [&](unsigned now, int64_t first) {
+        p.adapter0 = int(first);
+        const dim3 grid(tiles, unsigned(p.splits), now * unsigned(p.rchunks));
         if (RP == 16)
-            outer_kernel<1><<<blocks, 256, 0, s>>>(p, first);
+            outer_kernel<1><<<grid, 256, 0, s>>>(p);
         else if (RP == 32)
-            outer_kernel<2><<<blocks, 256, 0, s>>>(p, first);
+            outer_kernel<2><<<grid, 256, 0, s>>>(p);
         else
-            outer_kernel<4><<<blocks, 256, 0, s>>>(p, first);
+            outer_kernel<4><<<grid, 256, 0, s>>>(p);
     });
     if (st != WQ_OK || p.splits == 1) return st;
-    const int64_t n0 = (int64_t(a.L) * a.R * p.job[0].C + 3) / 4 * 4, n1 = narrow ? 0 : int64_t(a.L) * a.R * p.job[1].C;
-    return pieces((n0 + n1 + 1023) / 1024, [&](unsigned blocks, int64_t first) {
-        outer_sum_kernel<<<blocks, 256, 0, s>>>(p, n0, first * 256);
+    const int64_t n0 = (int64_t(a.L) * a.R * p.job[0].C + 3) / 4 * 4;
+    const int64_t n1 = narrow ? 0 : int64_t(a.L) * a.R * p.job[1].C;
+    return pieces((n0 + n1 + 1023) / 1024, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
+        outer_sum_kernel<<<now, 256, 0, s>>>(p, n0, first * 256);
     });
 }
 
