@@ -136,26 +136,42 @@ struct Shrink {
     // rows by adapter, for the gradients (null: not wanted)
     int32_t* start;        // [L + 1]
     int32_t* list;         // [M]
+    int lists;             // layers of z that make them
     int window0;           // of this launch
 };
 
 // Lists of rows by adapter: a wavefront per adapter counts the rows of lower
-// ones (its start) and writes its own in order.  2 M / 64 loads a wavefront, next to
-// the product's blocks.
+// ones (its start) and writes its own in order.  256 rows to a load, eight
+// loads at a time, twice over the slots, next to the product's blocks.
 __device__ __forceinline__ void list_rows(const Shrink& p, int64_t a) {
     const int lane = threadIdx.x & 63;
     if (a >= p.L) return;
     constexpr int U = 8;
-    int less = 0, mine = 0;
-    for (int64_t m = 0; m < p.M; m += 64 * U) {
-        int s[U];
+    auto load = [&](int64_t m0, int (&s)[U][4]) {   // -1 where there is no adapter
+        if (m0 + 256 * U <= p.M) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) s[u] = slot_of(p.slots, m + 64 * u + lane, p.M, p.L);
+            for (int u = 0; u < U; ++u) __builtin_memcpy(s[u], p.slots + m0 + 256 * u + 4 * lane, 16);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            less += s[u] >= 0 && s[u] < a;
-            mine += s[u] == a;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t m = m0 + 256 * u + 4 * lane + e;
+                    s[u][e] = m < p.M ? p.slots[m] : -1;
+                }
         }
+    };
+    int less = 0, mine = 0;
+    for (int64_t m0 = 0; m0 < p.M; m0 += 256 * U) {
+        int s[U][4];
+        load(m0, s);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                less += unsigned(s[u][e]) < unsigned(a);
+                mine += s[u][e] == a;
+            }
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
@@ -167,15 +183,22 @@ __device__ __forceinline__ void list_rows(const Shrink& p, int64_t a) {
         if (a == p.L - 1) p.start[p.L] = less + mine;
     }
     if (!mine) return;
-    for (int64_t m = 0; m < p.M; m += 64 * U) {
-        int s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) s[u] = slot_of(p.slots, m + 64 * u + lane, p.M, p.L);
+    for (int64_t m0 = 0; m0 < p.M; m0 += 256 * U) {
+        int s[U][4];
+        load(m0, s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint64_t mask = __ballot(s[u] == a);
-            if (s[u] == a) p.list[less + lanes_below(mask)] = int(m + 64 * u + lane);
-            less += __builtin_popcountll(mask);
+            uint64_t mask[4];
+            int at = less;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mask[e] = __ballot(s[u][e] == a);
+                at += lanes_below(mask[e]);
+                less += __builtin_popcountll(mask[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (s[u][e] == a) p.list[at++] = int(m0 + 256 * u + 4 * lane + e);
         }
     }
 }
@@ -240,14 +263,21 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
                 for (int t = 0; t < MT; ++t) v.x[t][i] &= mask;
             }
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
+        for (int i = 0; i < STEPS; ++i) {
+            if constexpr (DROP) {
+                uint64_t at[MT];
+                u4 keep[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if constexpr (DROP)
-                    v.x[t][i] = wq::drop8(v.x[t][i], eight + ((xr[t] + c0 + 32 * i + 8 * g) >> 3), p.drop, stream);
+                for (int t = 0; t < MT; ++t) at[t] = eight + ((xr[t] + c0 + 32 * i + 8 * g) >> 3);
+                wq::keep8(at, p.drop, stream, keep);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) v.x[t][i] &= keep[t];
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int n = 0; n < NRT; ++n) acc[t][n] = mfma(v.x[t][i], v.w[n][i], acc[t][n]);
-            }
+        }
         v = next;
     }
 
@@ -285,7 +315,7 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
 
 // Blocks: x the ranges of columns (the XCDs take neighbours in turn, so that
 // each holds its own range of every adapter in L2), y the window, z the rank's
-// 64s and Z shares of the window's adapters; behind those the lists' blocks.
+// 64s and Z shares of the window's adapters; before those the lists' blocks.
 //
 // ONE: the 16-row form alone, for decode batches of many adapters: it leaves
 // registers for more wavefronts, and those blocks wait for a few short loads.
@@ -293,12 +323,12 @@ template <int NRT, bool DROP, bool ONE>
 __global__ __launch_bounds__(64 * kShrinkWaves, NRT > 2 || !ONE ? 2 : 4) void shrink_kernel(const Shrink p) {
     constexpr int MT = ONE ? 1 : 4;
     __shared__ f4 sum[MT * NRT * 64 * (kShrinkWaves / 2)];
-    const int zs = p.Z * p.rchunks, bz = blockIdx.z;
-    if (bz >= zs) {
-        const int64_t b = (int64_t(bz - zs) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    if (int(blockIdx.z) < p.lists) {
+        const int64_t b = (int64_t(blockIdx.z) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
         list_rows(p, b * kShrinkWaves + (threadIdx.x >> 6));
         return;
     }
+    const int bz = blockIdx.z - p.lists;
     const int split = blockIdx.x, r0 = p.rchunks > 1 ? (bz & 1) * 64 : 0, z = p.rchunks > 1 ? bz >> 1 : bz;
     const int64_t m0 = int64_t(p.window0 + int(blockIdx.y)) * kWindow;
     const int slot = slot_of(p.slots, m0 + (threadIdx.x & 63), p.M, p.L);
@@ -468,10 +498,19 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
                         for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
                     }
                 }
+                uint32_t at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) at[i] = row_at(t, i) + c;
+                u4 keep[4];
+                if constexpr (DROP) {
+                    uint64_t n[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) n[i] = eight + (at[i] >> 3);
+                    wq::keep8(n, p.drop, stream, keep);
+                }
                 const f4 inverse = *reinterpret_cast<const f4*>(back + 16 * t + 4 * g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t at = row_at(t, i) + c;
                     // (a power of two: exact but where the result is below fp16's numbers anyway)
                     const float f = inverse[i] * s;
                     u4 v;
@@ -481,17 +520,14 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
                         v[j] = pack_h(__builtin_fmaf(acc[2 * j][i], f, float(o[0])),
                                       __builtin_fmaf(acc[2 * j + 1][i], f, float(o[1])));
                     }
-                    if constexpr (DROP) {
-                        const u4 keep = wq::keep8(eight + (at >> 3), p.drop, stream);
-                        v = (v & keep) | (old[i] & ~keep);
-                    }
+                    if constexpr (DROP) v = (v & keep[i]) | (old[i] & ~keep[i]);
                     if (16 * t + 4 * g + i >= cnt) continue;
                     if (p.C - 8 >= c0) {
-                        store8(off(ob, at), v);
+                        store8(off(ob, at[i]), v);
                     } else {   // the last, fewer than eight columns: those before c0 are another tile's
 #pragma unroll
                         for (int j = 1; j < 8; ++j)
-                            if (c + j >= c0) off(ob, at)[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
+                            if (c + j >= c0) off(ob, at[i])[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
                     }
                 }
 #pragma unroll
@@ -566,176 +602,168 @@ struct Outer {
     int adapter0;          // of this launch
 };
 
-// Rows of one adapter, 32 to a matrix step, against 128 columns: a block's
-// wavefronts take steps in turn.  h is brought into fp16's range for each of its
-// columns r, by a power of two that follows the largest magnitude so far, with
-// room for it to grow 2^5 times before the sums are rescaled.
+// Rows of one adapter against 128 columns and 16 RW of the rank.  The block's
+// four wavefronts take 32 rows each, a matrix step, from memory through
+// dropout into fragments; the products of a step go to RW wavefronts, 16 of the
+// rank each, over LDS (RW = 1: to itself).  So the rows are read and masked
+// once whatever the rank, and a wavefront's sums take 32 registers.  With
+// RW < 4 groups of RW wavefronts take different rows and meet at the end.
+//
+// h is brought into fp16's range for each of its columns r, by a power of two
+// that follows the largest magnitude so far, with room for it to grow 2^5 times
+// before the sums are rescaled.
 // Blocks: x the column tiles of both gradients, y the range of rows, z the
 // rank's 64s and the adapter.
-template <int NRT>
-__global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
-    __shared__ f4 sums[2 * NRT * 8 * 64];
+template <int RW>
+__global__ __launch_bounds__(256, 3) void outer_kernel(const Outer p) {
+    __shared__ u4 lds[4 * 8 * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int group = wave / RW * RW;   // the first wavefront whose rows this one takes
     const bool second = int(blockIdx.x) >= p.job[0].tiles;
     const OuterJob& j = p.job[second];
     const int tile = blockIdx.x - (second ? p.job[0].tiles : 0), split = blockIdx.y;
-    const int r0 = p.rchunks > 1 ? (blockIdx.z & 1) * 64 : 0;
+    const int r0 = (p.rchunks > 1 ? (blockIdx.z & 1) * 64 : 0) + 16 * (wave - group);
     const int a = p.adapter0 + int(p.rchunks > 1 ? blockIdx.z >> 1 : blockIdx.z);
     const int at = p.start ? p.start[a] : 0, cnt = p.start ? p.start[a + 1] - at : a == 0 ? p.M : 0;
     const int c = held(tile * kCols + 8 * c16, j.C);
     const bool drop = j.drop.t != 0;
     const uint64_t stream = drop ? wq::drop_stream(j.drop) : 0;
-    const int steps = (cnt + 31) / 32;
-    const int end = int(int64_t(split + 1) * steps / p.splits);
-    // fragment t holds r0 + NRT (l % 16) + t, a lane's r side by side; for those past
-    // the rank others are taken: what they give is not kept
-    const int held_r = min(r0 + NRT * c16, p.R - NRT);
-    f4 acc[NRT][8];
-    float mul[NRT];
+    // steps of 32 rows, four at a time
+    const int rounds = (cnt + 127) / 128;
+    const int end = int(int64_t(split + 1) * rounds / p.splits);
+    const float* const hr = j.h + min(r0 + c16, p.R - 1);   // (past the rank: what it gives is not kept)
+    f4 acc[8];
+    float mul = 0.f;
 #pragma unroll
-    for (int t = 0; t < NRT; ++t) {
-        mul[t] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[t][i] = f4{0.f, 0.f, 0.f, 0.f};
-    }
-
-#pragma unroll 1
-    for (int st = int(int64_t(split) * steps / p.splits) + wave; st < end; st += 4) {
-        const int i0 = st * 32 + 8 * g;
-        u4 x[8];
-        float h[8][NRT];
-        int m[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {   // (rows past the adapter's repeat its last one)
-            const int n = min(i0 + i, cnt - 1);
-            m[i] = p.list ? p.list[at + n] : n;
-        }
+    for (int k = 0; k < 8; ++k) acc[k] = f4{0.f, 0.f, 0.f, 0.f};
+    // row 8 g + i of a step (past the adapter's: its last one)
+    auto rows = [&](int step, int (&m)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x[i] = load8(j.src + int64_t(m[i]) * j.C + c);
-            __builtin_memcpy(h[i], j.h + int64_t(m[i]) * p.R + held_r, 4 * NRT);
+            const int n = min(step * 32 + 8 * g + i, cnt - 1);
+            m[i] = p.list ? p.list[at + n] : n;
         }
-        if (p.R % NRT) {   // a lane whose r's end inside NRT of them took the rank's last NRT
-            const int by = r0 + NRT * c16 - held_r;
+    };
+
+#pragma unroll 1
+    for (int round = int(int64_t(split) * rounds / p.splits); round < end; ++round) {
+        const int step = round * 4 + wave;
+        int m[8];
+        u4 x[8], w[8];
+        rows(step, m);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float v[NRT];
+        for (int i = 0; i < 8; ++i) x[i] = load8(j.src + int64_t(m[i]) * j.C + c);
+        float h[RW][8];
 #pragma unroll
-                for (int t = 0; t < NRT; ++t) {
-                    v[t] = h[i][t];
+        for (int q = 0; q < RW; ++q) {
+            int n[8];
+            if (RW > 1) rows(round * 4 + group + q, n);
 #pragma unroll
-                    for (int k = 1; t + k < NRT; ++k) v[t] = by == k ? h[i][t + k] : v[t];
-                }
-#pragma unroll
-                for (int t = 0; t < NRT; ++t) h[i][t] = v[t];
-            }
+            for (int i = 0; i < 8; ++i) h[q][i] = hr[int64_t(RW > 1 ? n[i] : m[i]) * p.R];
         }
         if (drop)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] &= wq::keep8((uint64_t(m[i]) * j.C + c) >> 3, j.drop, stream);
-        if (st * 32 + 32 > cnt)   // they count as zeros
+            for (int i = 0; i < 8; i += 4) {
+                uint64_t n[4];
+                u4 keep[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) n[k] = (uint64_t(m[i + k]) * j.C + c) >> 3;
+                wq::keep8(n, j.drop, stream, keep);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[i + k] &= keep[k];
+            }
+        if (round * 128 + 128 > cnt) {   // rows past the adapter's count as zeros
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i0 + i >= cnt) {
-                    x[i] = u4{0, 0, 0, 0};
+                if (step * 32 + 8 * g + i >= cnt) x[i] = u4{0, 0, 0, 0};
 #pragma unroll
-                    for (int t = 0; t < NRT; ++t) h[i][t] = 0.f;
-                }
-        float most[NRT];
-        bool grow = false;
+            for (int q = 0; q < RW; ++q)
 #pragma unroll
-        for (int t = 0; t < NRT; ++t) {
-            most[t] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) most[t] = __builtin_fmaxf(most[t], finite_magnitude(h[i][t]));
-            most[t] = __builtin_fmaxf(most[t], __shfl_xor(most[t], 16));
-            most[t] = __builtin_fmaxf(most[t], __shfl_xor(most[t], 32));
-            grow |= most[t] * mul[t] >= 32768.f || (mul[t] == 0.f && most[t] > 0.f);
+                for (int i = 0; i < 8; ++i)
+                    if ((round * 4 + group + q) * 32 + 8 * g + i >= cnt) h[q][i] = 0.f;
         }
+        transpose8(x, w);
+        if constexpr (RW > 1) {
+            __syncthreads();   // the round before is read
+#pragma unroll
+            for (int k = 0; k < 8; ++k) lds[(wave * 8 + k) * 64 + lane] = w[k];
+        }
+        float most = 0.f;
+#pragma unroll
+        for (int q = 0; q < RW; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, finite_magnitude(h[q][i]));
+        most = __builtin_fmaxf(most, __shfl_xor(most, 16));
+        most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+        const bool grow = most * mul >= 32768.f || (mul == 0.f && most > 0.f);
         if (__ballot(grow)) {
+            float ratio = 1.f, inverse;
+            if (grow) {
+                const float next = to_range(most, 9, inverse);
+                ratio = mul == 0.f ? 1.f : next / mul;
+                mul = next;
+            }
 #pragma unroll
-            for (int t = 0; t < NRT; ++t) {
-                float ratio = 1.f;
-                if (most[t] * mul[t] >= 32768.f || (mul[t] == 0.f && most[t] > 0.f)) {
-                    float inverse;
-                    const float next = to_range(most[t], 9, inverse);
-                    ratio = mul[t] == 0.f ? 1.f : next / mul[t];
-                    mul[t] = next;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float f = __shfl(ratio, 4 * g + i);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f = __shfl(ratio, 4 * g + i);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[t][k][i] *= f;
-                }
+                for (int k = 0; k < 8; ++k) acc[k][i] *= f;
             }
         }
-        u4 w[8];
-        transpose8(x, w);
+        const float scale = mul == 0.f ? 1.f : mul;
+        if constexpr (RW > 1) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < NRT; ++t) {
-            const float scale = mul[t] == 0.f ? 1.f : mul[t];
+        for (int q = 0; q < RW; ++q) {
             u4 hi, lo;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t a, b;
-                split_h(h[2 * i][t] * scale, h[2 * i + 1][t] * scale, a, b);
+                split_h(h[q][2 * i] * scale, h[q][2 * i + 1] * scale, a, b);
                 hi[i] = a;
                 lo[i] = b;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[t][k] = mfma(hi, w[k], acc[t][k]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[t][k] = mfma(lo, w[k], acc[t][k]);
+            for (int k = 0; k < 8; ++k) {
+                const u4 v = RW > 1 ? lds[((group + q) * 8 + k) * 64 + lane] : w[k];
+                acc[k] = mfma(hi, v, acc[k]);
+                acc[k] = mfma(lo, v, acc[k]);
+            }
         }
     }
 
-    // back from the powers of two, then (0 + 2) + (1 + 3)
+    // back from the powers of two, then the wavefronts of different rows in order
     const float s = (drop ? j.drop.keep : 1.f) * (cnt ? p.scales[a] : 0.f);
+    const float inverse = mul == 0.f ? 1.f : 1.f / mul;   // (a power of two: exact)
 #pragma unroll
-    for (int t = 0; t < NRT; ++t) {
-        const float inverse = mul[t] == 0.f ? 1.f : 1.f / mul[t];   // (a power of two: exact)
+    for (int i = 0; i < 4; ++i) {
+        const float f = __shfl(inverse, 4 * g + i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float f = __shfl(inverse, 4 * g + i);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[t][k][i] *= f;
-        }
+        for (int k = 0; k < 8; ++k) acc[k][i] *= f;
     }
-    auto give = [&](f4* to) {
+    if constexpr (RW < 4) {
+        f4* const sums = reinterpret_cast<f4*>(lds);
+        __syncthreads();
+        if (group)
 #pragma unroll
-        for (int t = 0; t < NRT; ++t)
+            for (int k = 0; k < 8; ++k) sums[(wave * 8 + k) * 64 + lane] = acc[k];
+        __syncthreads();
+        if (group) return;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to[(t * 8 + k) * 64 + lane] = acc[t][k];
-    };
-    auto take = [&](const f4* from) {
+        for (int o = RW; o < 4; o += RW)
 #pragma unroll
-        for (int t = 0; t < NRT; ++t)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[t][k] += from[(t * 8 + k) * 64 + lane];
-    };
-    f4* const other = sums + NRT * 8 * 64;
-    if (wave >= 2) give(wave == 2 ? sums : other);
-    __syncthreads();
-    if (wave < 2) take(wave == 0 ? sums : other);
-    __syncthreads();
-    if (wave == 1) give(sums);
-    __syncthreads();
-    if (wave != 0) return;
-    take(sums);
+            for (int k = 0; k < 8; ++k) acc[k] += sums[((wave + o) * 8 + k) * 64 + lane];
+    }
 
     float* to = (p.splits > 1 ? j.part + int64_t(split) * p.L * p.R * j.C : j.dw) + int64_t(a) * p.R * j.C + c;
 #pragma unroll
-    for (int t = 0; t < NRT; ++t)
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 4 * g + i;
+        if (r >= p.R) continue;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + NRT * (4 * g + i) + t;
-            if (r >= p.R) continue;
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = acc[t][k][i] * s;
-            __builtin_memcpy(to + int64_t(r) * j.C, v, 32);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = acc[k][i] * s;
+        __builtin_memcpy(to + int64_t(r) * j.C, v, 32);
+    }
 }
 
 // dw = the sum over the ranges of rows, in order; four values to a thread.
@@ -856,7 +884,7 @@ struct ShrinkPlan {
     ShrinkPlan(int M, int R, int L, int C) {
         const int chunks = div_up(C, kChunk), rchunks = padded_rank(R) > 64 ? 2 : 1;
         const int64_t base = int64_t(div_up(M, kWindow)) * rchunks;
-        const int want = int(std::min<int64_t>(std::max<int64_t>(512 / base, 1), 32));
+        const int want = int(std::min<int64_t>(std::max<int64_t>(256 / base, 1), 32));
         cps = div_up(chunks, std::min(want, div_up(chunks, 4)));
         splits = div_up(chunks, cps);
         Z = shares(M, L, base * splits, 256);
@@ -868,7 +896,7 @@ wq_status shrink(const wqh::Adapters& a, const uint16_t* src, const uint16_t* w,
                  int32_t* start, int32_t* list, hipStream_t s) {
     const ShrinkPlan plan(a.M, a.R, a.L, C);
     const int RP = padded_rank(a.R);
-    Shrink p{src, w, a.slots, part, d, a.M, a.R, a.L, C, plan.splits, plan.cps, plan.Z, RP > 64 ? 2 : 1, start, list, 0};
+    Shrink p{src, w, a.slots, part, d, a.M, a.R, a.L, C, plan.splits, plan.cps, plan.Z, RP > 64 ? 2 : 1, start, list, 0, 0};
     const int lists = start ? div_up(a.L, kShrinkWaves) : 0;
     constexpr int T = 64 * kShrinkWaves;
     if (C < 8) {   // (N: K is 32 at least, so nothing is dropped)
@@ -883,9 +911,8 @@ wq_status shrink(const wqh::Adapters& a, const uint16_t* src, const uint16_t* w,
     const bool one = a.M <= 16 || (a.slots && a.L > 1 && a.M <= 256);
     return pieces(div_up(a.M, kWindow), kMaxY, [&](unsigned windows, int64_t first) {
         p.window0 = int(first);
-        dim3 grid(unsigned(p.splits), windows, unsigned(p.Z * p.rchunks));
-        if (first == 0)
-            grid.z += unsigned(div_up(lists, int64_t(p.splits) * windows));
+        p.lists = first == 0 ? div_up(lists, int64_t(p.splits) * windows) : 0;
+        const dim3 grid(unsigned(p.splits), windows, unsigned(p.lists + p.Z * p.rchunks));
         auto go = [&](auto n) {
             constexpr int NRT = decltype(n)::value;
             if (one && !d.t)

@@ -24,21 +24,31 @@ __device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
     return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
 }
 
-// Philox4x32-10's output for the counter (n, stream).
-__device__ __forceinline__ u4 philox(uint64_t n, uint64_t stream, uint32_t k0, uint32_t k1) {
-    uint32_t c0 = uint32_t(n), c1 = uint32_t(n >> 32), c2 = uint32_t(stream), c3 = uint32_t(stream >> 32);
-    // (not unrolled: the kernels hold several of these, and their code is read once)
+// Philox4x32-10's output for the counters (n[i], stream).  Several at a time:
+// a round's two products wait for the round before, and those of different
+// counters do not.  The rounds are not unrolled, which would fill the
+// instruction cache where a kernel's code runs once per wavefront.
+template <int N>
+__device__ __forceinline__ void philox(const uint64_t (&n)[N], uint64_t stream, uint32_t k0, uint32_t k1, u4 (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        w[i] = u4{uint32_t(n[i]), uint32_t(n[i] >> 32), uint32_t(stream), uint32_t(stream >> 32)};
 #pragma unroll 1
     for (int r = 0; r < 10; ++r) {
-        const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
-        c0 = xor3(uint32_t(b >> 32), c1, k0);
-        c1 = uint32_t(b);
-        c2 = xor3(uint32_t(a >> 32), c3, k1);
-        c3 = uint32_t(a);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint64_t a = uint64_t(w[i][0]) * 0xD2511F53u, b = uint64_t(w[i][2]) * 0xCD9E8D57u;
+            w[i] = u4{xor3(uint32_t(b >> 32), w[i][1], k0), uint32_t(b), xor3(uint32_t(a >> 32), w[i][3], k1),
+                      uint32_t(a)};
+        }
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    return u4{c0, c1, c2, c3};
+}
+__device__ __forceinline__ u4 philox(uint64_t n, uint64_t stream, uint32_t k0, uint32_t k1) {
+    u4 w[1];
+    philox<1>({n}, stream, k0, k1, w);
+    return w[0];
 }
 
 // Whether element i of a block's eight is kept.
@@ -48,20 +58,20 @@ __device__ __forceinline__ bool kept(u4 w, int i, uint32_t t) {
 
 typedef uint16_t us2 __attribute__((ext_vector_type(2)));
 
-// All ones in the 16 bits of those of block n's eight elements that are kept (t > 0).
-__device__ __forceinline__ u4 keep8(uint64_t n, const Drop& d, uint64_t stream) {
-    u4 w = philox(n, stream, d.key0, d.key1);
+// All ones in the 16 bits of those of block n[i]'s eight elements that are kept
+// (t > 0).
+template <int N>
+__device__ __forceinline__ void keep8(const uint64_t (&n)[N], const Drop& d, uint64_t stream, u4 (&w)[N]) {
+    philox(n, stream, d.key0, d.key1, w);
     const us2 below{uint16_t(d.t - 1), uint16_t(d.t - 1)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = w[i];
-        const us2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(us2, v), below);  // 0 below t
-        w[i] = __builtin_bit_cast(uint32_t, us2(us2{0, 0} - __builtin_elementwise_min(over, us2{1, 1})));
-    }
-    return w;
-}
-__device__ __forceinline__ u4 drop8(u4 v, uint64_t n, const Drop& d, uint64_t stream) {
-    return v & keep8(n, d, stream);
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = w[k][i];
+            const us2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(us2, v), below);  // 0 below t
+            w[k][i] = __builtin_bit_cast(uint32_t, us2(us2{0, 0} - __builtin_elementwise_min(over, us2{1, 1})));
+        }
 }
 
 }  // namespace wq
