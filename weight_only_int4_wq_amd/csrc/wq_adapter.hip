@@ -136,79 +136,69 @@ struct Shrink {
     // rows by adapter, for the gradients (null: not wanted)
     int32_t* start;        // [L + 1]
     int32_t* list;         // [M]
-    int lists;             // layers of z that make them
+    int lists;             // layers of y that make them
     int window0;           // of this launch
 };
 
-// Lists of rows by adapter: a wavefront per adapter counts the rows of lower
-// ones (its start) and writes its own in order.  256 rows to a load, eight
-// loads at a time, twice over the slots, next to the product's blocks.
-__device__ __forceinline__ void list_rows(const Shrink& p, int64_t a) {
-    const int lane = threadIdx.x & 63;
+// Lists of rows by adapter: a block per adapter, next to the product's.  Its
+// wavefronts take a range of rows each, count the rows of lower adapters (their
+// sum is the list's start) and their own, and write those in order.
+__device__ __forceinline__ void list_rows(const Shrink& p, int a, int* counts) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (a >= p.L) return;
-    constexpr int U = 8;
-    auto load = [&](int64_t m0, int (&s)[U][4]) {   // -1 where there is no adapter
-        if (m0 + 256 * U <= p.M) {
+    constexpr int U = 4;
+    const int each = (p.M + 64 * U * kShrinkWaves - 1) / (64 * U * kShrinkWaves) * 64 * U;
+    const int64_t first = int64_t(wave) * each, end = min(first + each, int64_t(p.M));
+    int s[U];
+    auto load = [&](int64_t m) {   // -1 where there is no row
 #pragma unroll
-            for (int u = 0; u < U; ++u) __builtin_memcpy(s[u], p.slots + m0 + 256 * u + 4 * lane, 16);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t m = m0 + 256 * u + 4 * lane + e;
-                    s[u][e] = m < p.M ? p.slots[m] : -1;
-                }
-        }
+        for (int u = 0; u < U; ++u) s[u] = m + 64 * u + lane < end ? p.slots[m + 64 * u + lane] : -1;
     };
     int less = 0, mine = 0;
-    for (int64_t m0 = 0; m0 < p.M; m0 += 256 * U) {
-        int s[U][4];
-        load(m0, s);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                less += unsigned(s[u][e]) < unsigned(a);
-                mine += s[u][e] == a;
-            }
-    }
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-        less += __shfl_xor(less, o);
-        mine += __shfl_xor(mine, o);
-    }
-    if (lane == 0) {
-        p.start[a] = less;
-        if (a == p.L - 1) p.start[p.L] = less + mine;
-    }
-    if (!mine) return;
-    for (int64_t m0 = 0; m0 < p.M; m0 += 256 * U) {
-        int s[U][4];
-        load(m0, s);
+#pragma unroll 1
+    for (int64_t m = first; m < end; m += 64 * U) {
+        load(m);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            uint64_t mask[4];
-            int at = less;
+            less += __builtin_popcountll(__ballot(unsigned(s[u]) < unsigned(a)));
+            mine += __builtin_popcountll(__ballot(s[u] == a));
+        }
+    }
+    if (lane == 0) {
+        counts[wave] = less;
+        counts[kShrinkWaves + wave] = mine;
+    }
+    __syncthreads();
+    int start = 0, all = 0, before = 0;
+    for (int w = 0; w < kShrinkWaves; ++w) {
+        start += counts[w];
+        if (w == wave) before = all;
+        all += counts[kShrinkWaves + w];
+    }
+    if (threadIdx.x == 0) {
+        p.start[a] = start;
+        if (a == p.L - 1) p.start[p.L] = start + all;
+    }
+    if (!mine) return;
+    int at = start + before;
+#pragma unroll 1
+    for (int64_t m = first; m < end; m += 64 * U) {
+        load(m);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                mask[e] = __ballot(s[u][e] == a);
-                at += lanes_below(mask[e]);
-                less += __builtin_popcountll(mask[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (s[u][e] == a) p.list[at++] = int(m0 + 256 * u + 4 * lane + e);
+        for (int u = 0; u < U; ++u) {
+            const uint64_t mask = __ballot(s[u] == a);
+            if (s[u] == a) p.list[at + lanes_below(mask)] = int(m + 64 * u + lane);
+            at += __builtin_popcountll(mask);
         }
     }
 }
 
 // One adapter's rows of a window, up to 16 MT, against 16 NRT of its rank's
 // rows, over the block's range of columns; the wavefronts take pieces of it in
-// turn, the next one's loads in flight.  Rows past the adapter's repeat its
+// turn, with AHEAD the next one's loads in flight.  Rows past the adapter's repeat its
 // last one, and rows past the rank likewise: they cost no traffic, and what
 // they give is not kept.
-template <int MT, int NRT, bool DROP>
+template <int MT, int NRT, bool DROP, bool AHEAD>
 __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, int cnt, int order, int r0, int split,
                                             f4* sum) {
     constexpr int STEPS = MT * NRT > 8 ? 1 : 2, COLS = 32 * STEPS;   // 128 bytes of a row, or what the registers hold
@@ -248,7 +238,7 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
     if (c0 < end) load(c0, v);
 #pragma unroll 1
     for (; c0 < end; c0 += NEXT) {
-        if (c0 + NEXT < end) load(c0 + NEXT, next);
+        if (AHEAD && c0 + NEXT < end) load(c0 + NEXT, next);
         if (c0 + COLS > p.C)   // columns that other lanes hold too: zeros on both sides
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
@@ -278,7 +268,10 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
 #pragma unroll
                 for (int n = 0; n < NRT; ++n) acc[t][n] = mfma(v.x[t][i], v.w[n][i], acc[t][n]);
         }
-        v = next;
+        if (AHEAD)
+            v = next;
+        else if (c0 + NEXT < end)
+            load(c0 + NEXT, v);
     }
 
     // the wavefronts' sums: w and w + 4, then the four in order
@@ -314,28 +307,29 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
 }
 
 // Blocks: x the ranges of columns (the XCDs take neighbours in turn, so that
-// each holds its own range of every adapter in L2), y the window, z the rank's
-// 64s and Z shares of the window's adapters; before those the lists' blocks.
+// each holds its own range of every adapter in L2), y the window, behind the
+// layers that make the lists, z the rank's 64s and Z shares of the window's
+// adapters.
 //
-// ONE: the 16-row form alone, for decode batches of many adapters: it leaves
-// registers for more wavefronts, and those blocks wait for a few short loads.
+// ONE: 16 rows at a time and one piece in flight, for decode batches of many
+// adapters: that leaves registers for twice the wavefronts, and those blocks
+// wait for a few short loads.
 template <int NRT, bool DROP, bool ONE>
-__global__ __launch_bounds__(64 * kShrinkWaves, NRT > 2 || !ONE ? 2 : 4) void shrink_kernel(const Shrink p) {
+__global__ __launch_bounds__(64 * kShrinkWaves, ONE ? 4 : 2) void shrink_kernel(const Shrink p) {
     constexpr int MT = ONE ? 1 : 4;
     __shared__ f4 sum[MT * NRT * 64 * (kShrinkWaves / 2)];
-    if (int(blockIdx.z) < p.lists) {
-        const int64_t b = (int64_t(blockIdx.z) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-        list_rows(p, b * kShrinkWaves + (threadIdx.x >> 6));
+    if (int(blockIdx.y) < p.lists) {
+        list_rows(p, int((blockIdx.y * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x), reinterpret_cast<int*>(sum));
         return;
     }
-    const int bz = blockIdx.z - p.lists;
+    const int bz = blockIdx.z;
     const int split = blockIdx.x, r0 = p.rchunks > 1 ? (bz & 1) * 64 : 0, z = p.rchunks > 1 ? bz >> 1 : bz;
-    const int64_t m0 = int64_t(p.window0 + int(blockIdx.y)) * kWindow;
+    const int64_t m0 = int64_t(p.window0 + int(blockIdx.y) - p.lists) * kWindow;
     const int slot = slot_of(p.slots, m0 + (threadIdx.x & 63), p.M, p.L);
     each_adapter(slot, z, p.Z, [&](int a, int cnt, int order) {
 #pragma unroll 1
         for (; cnt > 0; cnt -= 16 * MT) {
-            shrink_rows<MT, NRT, DROP>(p, m0, a, min(cnt, 16 * MT), order, r0, split, sum);
+            shrink_rows<MT, NRT, DROP, !ONE>(p, m0, a, min(cnt, 16 * MT), order, r0, split, sum);
             order = __shfl(order, (threadIdx.x + 16 * MT) & 63);
         }
     });
@@ -603,64 +597,75 @@ struct Outer {
 };
 
 // Rows of one adapter against 128 columns and 16 RW of the rank.  The block's
-// four wavefronts take 32 rows each, a matrix step, from memory through
-// dropout into fragments; the products of a step go to RW wavefronts, 16 of the
-// rank each, over LDS (RW = 1: to itself).  So the rows are read and masked
-// once whatever the rank, and a wavefront's sums take 32 registers.  With
-// RW < 4 groups of RW wavefronts take different rows and meet at the end.
+// four wavefronts take 32 rows each, a matrix step: src through dropout into
+// fragments, h into fragments of its 16s.  The products of a step go to RW
+// wavefronts, 16 of the rank each, over LDS (RW = 1: to itself).  So the rows
+// are read, masked and split once whatever the rank, and a wavefront's sums
+// take 32 registers.  With RW < 4 groups of RW wavefronts take different rows
+// and meet at the end.  The next rows' loads are in flight during the products.
 //
-// h is brought into fp16's range for each of its columns r, by a power of two
-// that follows the largest magnitude so far, with room for it to grow 2^5 times
-// before the sums are rescaled.
+// h is split in two fp16 numbers after a power of two for each step and column
+// has brought it into their range; the step's products are brought back as they
+// are added to the fp32 sums.
 // Blocks: x the column tiles of both gradients, y the range of rows, z the
 // rank's 64s and the adapter.
 template <int RW>
-__global__ __launch_bounds__(256, 3) void outer_kernel(const Outer p) {
-    __shared__ u4 lds[4 * 8 * 64];
+__global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
+    __shared__ u4 xs[4 * 8 * 64];                        // [step][column fragment][lane]
+    __shared__ u4 hs[RW > 1 ? 4 * RW * 2 * 64 : 1];      // [step][16 of the rank][first, second part][lane]
+    __shared__ f4 back[RW > 1 ? 4 * RW * 4 : 1];         // [step][16 of the rank][16]: the powers' inverses
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
     const int group = wave / RW * RW;   // the first wavefront whose rows this one takes
+    const int mine = wave - group;      // which 16 of the rank: r0 + RW * (row of the fragment) + mine
     const bool second = int(blockIdx.x) >= p.job[0].tiles;
     const OuterJob& j = p.job[second];
     const int tile = blockIdx.x - (second ? p.job[0].tiles : 0), split = blockIdx.y;
-    const int r0 = (p.rchunks > 1 ? (blockIdx.z & 1) * 64 : 0) + 16 * (wave - group);
+    const int r0 = p.rchunks > 1 ? (blockIdx.z & 1) * 64 : 0;
     const int a = p.adapter0 + int(p.rchunks > 1 ? blockIdx.z >> 1 : blockIdx.z);
     const int at = p.start ? p.start[a] : 0, cnt = p.start ? p.start[a + 1] - at : a == 0 ? p.M : 0;
     const int c = held(tile * kCols + 8 * c16, j.C);
     const bool drop = j.drop.t != 0;
     const uint64_t stream = drop ? wq::drop_stream(j.drop) : 0;
-    // steps of 32 rows, four at a time
-    const int rounds = (cnt + 127) / 128;
-    const int end = int(int64_t(split + 1) * rounds / p.splits);
-    const float* const hr = j.h + min(r0 + c16, p.R - 1);   // (past the rank: what it gives is not kept)
+    // rounds of four steps of 32 rows
+    const int rounds = (cnt + 127) / 128, end = int(int64_t(split + 1) * rounds / p.splits);
+    int round = int(int64_t(split) * rounds / p.splits);
+    // a lane's r: RW side by side; past the rank others are taken, and what they give is not kept
+    const int held_r = min(r0 + RW * c16, p.R - RW);
     f4 acc[8];
-    float mul = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = f4{0.f, 0.f, 0.f, 0.f};
-    // row 8 g + i of a step (past the adapter's: its last one)
-    auto rows = [&](int step, int (&m)[8]) {
+
+    // rows 8 g + i of the wavefront's step (past the adapter's: its last one)
+    auto rows = [&](int of, int (&m)[8]) {
+        const int n = of * 128 + wave * 32;
+        if (p.list && n + 32 <= cnt) {
+            __builtin_memcpy(m, p.list + at + n + 8 * g, 32);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = min(n + 8 * g + i, cnt - 1);
+        if (p.list)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = p.list[at + m[i]];
+    };
+    u4 x[8];
+    float h[8][RW];
+    int m[8], next[8];
+    auto load = [&] {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int n = min(step * 32 + 8 * g + i, cnt - 1);
-            m[i] = p.list ? p.list[at + n] : n;
+            x[i] = load8(j.src + int64_t(m[i]) * j.C + c);
+            __builtin_memcpy(h[i], j.h + int64_t(m[i]) * p.R + held_r, 4 * RW);
         }
     };
-
+    if (round < end) {
+        rows(round, m);
+        load();
+        rows(round + 1 < end ? round + 1 : round, next);
+    }
 #pragma unroll 1
-    for (int round = int(int64_t(split) * rounds / p.splits); round < end; ++round) {
-        const int step = round * 4 + wave;
-        int m[8];
-        u4 x[8], w[8];
-        rows(step, m);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = load8(j.src + int64_t(m[i]) * j.C + c);
-        float h[RW][8];
-#pragma unroll
-        for (int q = 0; q < RW; ++q) {
-            int n[8];
-            if (RW > 1) rows(round * 4 + group + q, n);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[q][i] = hr[int64_t(RW > 1 ? n[i] : m[i]) * p.R];
-        }
+    for (; round < end; ++round) {
+        const int first = round * 128 + wave * 32 + 8 * g;   // the lane's first row in the adapter's
         if (drop)
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
@@ -672,77 +677,90 @@ __global__ __launch_bounds__(256, 3) void outer_kernel(const Outer p) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x[i + k] &= keep[k];
             }
-        if (round * 128 + 128 > cnt) {   // rows past the adapter's count as zeros
+        if (RW > 1 && p.R % RW) {   // a lane whose r's end inside RW of them took the rank's last RW
+            const int by = r0 + RW * c16 - held_r;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v[RW];
+#pragma unroll
+                for (int t = 0; t < RW; ++t) {
+                    v[t] = h[i][t];
+#pragma unroll
+                    for (int k = 1; t + k < RW; ++k) v[t] = by == k ? h[i][t + k] : v[t];
+                }
+#pragma unroll
+                for (int t = 0; t < RW; ++t) h[i][t] = v[t];
+            }
+        }
+        if (round * 128 + 128 > cnt)   // rows past the adapter's count as zeros
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (step * 32 + 8 * g + i >= cnt) x[i] = u4{0, 0, 0, 0};
+                if (first + i >= cnt) {
+                    x[i] = u4{0, 0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < RW; ++q)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if ((round * 4 + group + q) * 32 + 8 * g + i >= cnt) h[q][i] = 0.f;
-        }
+                    for (int t = 0; t < RW; ++t) h[i][t] = 0.f;
+                }
+        u4 w[8], hi[RW], lo[RW];
+        f4 own{0.f, 0.f, 0.f, 0.f};   // RW = 1: the wavefront's inverses
         transpose8(x, w);
-        if constexpr (RW > 1) {
-            __syncthreads();   // the round before is read
 #pragma unroll
-            for (int k = 0; k < 8; ++k) lds[(wave * 8 + k) * 64 + lane] = w[k];
-        }
-        float most = 0.f;
+        for (int t = 0; t < RW; ++t) {
+            float most = 0.f, inverse;
 #pragma unroll
-        for (int q = 0; q < RW; ++q)
+            for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, finite_magnitude(h[i][t]));
+            most = __builtin_fmaxf(most, __shfl_xor(most, 16));
+            most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+            const float scale = to_range(most, 13, inverse);
+            if (RW == 1)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, finite_magnitude(h[q][i]));
-        most = __builtin_fmaxf(most, __shfl_xor(most, 16));
-        most = __builtin_fmaxf(most, __shfl_xor(most, 32));
-        const bool grow = most * mul >= 32768.f || (mul == 0.f && most > 0.f);
-        if (__ballot(grow)) {
-            float ratio = 1.f, inverse;
-            if (grow) {
-                const float next = to_range(most, 9, inverse);
-                ratio = mul == 0.f ? 1.f : next / mul;
-                mul = next;
-            }
+                for (int i = 0; i < 4; ++i) own[i] = __shfl(inverse, 4 * g + i);
+            else if (g == 0)
+                reinterpret_cast<float*>(back)[(wave * RW + t) * 16 + c16] = inverse;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f = __shfl(ratio, 4 * g + i);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k][i] *= f;
+                uint32_t u, v;
+                split_h(h[2 * i][t] * scale, h[2 * i + 1][t] * scale, u, v);
+                hi[t][i] = u;
+                lo[t][i] = v;
             }
         }
-        const float scale = mul == 0.f ? 1.f : mul;
-        if constexpr (RW > 1) __syncthreads();
+        if constexpr (RW > 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) xs[(wave * 8 + k) * 64 + lane] = w[k];
+#pragma unroll
+            for (int t = 0; t < RW; ++t) {
+                hs[((wave * RW + t) * 2 + 0) * 64 + lane] = hi[t];
+                hs[((wave * RW + t) * 2 + 1) * 64 + lane] = lo[t];
+            }
+        }
+        if (round + 1 < end) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = next[i];
+            load();
+            rows(round + 2 < end ? round + 2 : round, next);
+        }
+        if (RW > 1) __syncthreads();
 #pragma unroll
         for (int q = 0; q < RW; ++q) {
-            u4 hi, lo;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a, b;
-                split_h(h[q][2 * i] * scale, h[q][2 * i + 1] * scale, a, b);
-                hi[i] = a;
-                lo[i] = b;
-            }
+            const int step = group + q;
+            const u4 vh = RW > 1 ? hs[((step * RW + mine) * 2 + 0) * 64 + lane] : hi[0];
+            const u4 vl = RW > 1 ? hs[((step * RW + mine) * 2 + 1) * 64 + lane] : lo[0];
+            const f4 f = RW > 1 ? back[(step * RW + mine) * 4 + g] : own;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const u4 v = RW > 1 ? lds[((group + q) * 8 + k) * 64 + lane] : w[k];
-                acc[k] = mfma(hi, v, acc[k]);
-                acc[k] = mfma(lo, v, acc[k]);
+                const u4 v = RW > 1 ? xs[(step * 8 + k) * 64 + lane] : w[k];
+                f4 t{0.f, 0.f, 0.f, 0.f};
+                t = mfma(vh, v, t);
+                t = mfma(vl, v, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[k][i] = __builtin_fmaf(t[i], f[i], acc[k][i]);
             }
         }
+        if (RW > 1) __syncthreads();
     }
 
-    // back from the powers of two, then the wavefronts of different rows in order
-    const float s = (drop ? j.drop.keep : 1.f) * (cnt ? p.scales[a] : 0.f);
-    const float inverse = mul == 0.f ? 1.f : 1.f / mul;   // (a power of two: exact)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float f = __shfl(inverse, 4 * g + i);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k][i] *= f;
-    }
-    if constexpr (RW < 4) {
-        f4* const sums = reinterpret_cast<f4*>(lds);
-        __syncthreads();
+    if constexpr (RW < 4) {   // the wavefronts of different rows, in order
+        f4* const sums = reinterpret_cast<f4*>(xs);
         if (group)
 #pragma unroll
             for (int k = 0; k < 8; ++k) sums[(wave * 8 + k) * 64 + lane] = acc[k];
@@ -754,10 +772,11 @@ __global__ __launch_bounds__(256, 3) void outer_kernel(const Outer p) {
             for (int k = 0; k < 8; ++k) acc[k] += sums[((wave + o) * 8 + k) * 64 + lane];
     }
 
+    const float s = (drop ? j.drop.keep : 1.f) * (cnt ? p.scales[a] : 0.f);
     float* to = (p.splits > 1 ? j.part + int64_t(split) * p.L * p.R * j.C : j.dw) + int64_t(a) * p.R * j.C + c;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * g + i;
+        const int r = r0 + RW * (4 * g + i) + mine;
         if (r >= p.R) continue;
         float v[8];
 #pragma unroll
@@ -810,8 +829,9 @@ __global__ __launch_bounds__(256) void narrow_shrink_kernel(const Shrink p, int 
             v += wq::h2f(p.src[m * p.C + c]) * wq::h2f(p.w[(int64_t(a) * p.R + r) * p.C + c]);
     p.part[q] = v;
 }
-__global__ __launch_bounds__(64 * kShrinkWaves) void list_kernel(const Shrink p, int64_t first) {
-    list_rows(p, (first + blockIdx.x) * kShrinkWaves + (threadIdx.x >> 6));
+__global__ __launch_bounds__(64 * kShrinkWaves) void list_kernel(const Shrink p) {
+    __shared__ int counts[2 * kShrinkWaves];
+    list_rows(p, int(blockIdx.x), counts);
 }
 
 // out of C columns; thread 0 of a row's columns also leaves the row's sums.
@@ -870,13 +890,19 @@ wq_status pieces(int64_t total, int64_t most, const Launch& launch) {
     }
     return WQ_OK;
 }
-constexpr int kMaxY = 65535;   // blocks of a launch in y or z
+constexpr int kMaxY = 65535;        // blocks of a launch in y or z
+constexpr int kMaxWidth = 1 << 22;  // adapters, and columns
 
 // How many blocks share the work of a window whose adapters are not known here,
 // where `blocks` alone leave units idle.
 int shares(int M, int L, int64_t blocks, int want) {
     return int(std::max<int64_t>(1, std::min<int64_t>(std::min(std::min(L, M), kWindow), want / blocks)));
 }
+
+// Batches of up to this many rows with slots and several adapters are taken for
+// decode batches, a row or a few to an adapter.
+constexpr int kMixedM = 256;
+bool mixed(const wqh::Adapters& a) { return a.slots && a.L > 1 && a.M <= kMixedM; }
 
 // Ranges of the long side of a shrink, and the blocks that share a window.
 struct ShrinkPlan {
@@ -887,7 +913,7 @@ struct ShrinkPlan {
         const int want = int(std::min<int64_t>(std::max<int64_t>(256 / base, 1), 32));
         cps = div_up(chunks, std::min(want, div_up(chunks, 4)));
         splits = div_up(chunks, cps);
-        Z = shares(M, L, base * splits, 256);
+        Z = shares(M, L, base * splits, M <= kMixedM ? 512 : 256);
     }
     size_t bytes(int M, int R) const { return round256(size_t(splits) * M * padded_rank(R) * 4); }
 };
@@ -897,22 +923,29 @@ wq_status shrink(const wqh::Adapters& a, const uint16_t* src, const uint16_t* w,
     const ShrinkPlan plan(a.M, a.R, a.L, C);
     const int RP = padded_rank(a.R);
     Shrink p{src, w, a.slots, part, d, a.M, a.R, a.L, C, plan.splits, plan.cps, plan.Z, RP > 64 ? 2 : 1, start, list, 0, 0};
-    const int lists = start ? div_up(a.L, kShrinkWaves) : 0;
+    const int lists = start ? a.L : 0;   // blocks
     constexpr int T = 64 * kShrinkWaves;
+    auto list_all = [&] {
+        return pieces(lists, kMaxWidth, [&](unsigned now, int64_t) { list_kernel<<<now, T, 0, s>>>(p); });
+    };
     if (C < 8) {   // (N: K is 32 at least, so nothing is dropped)
         const wq_status st = pieces((int64_t(a.M) * RP + 255) / 256, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
             narrow_shrink_kernel<<<now, 256, 0, s>>>(p, RP, first);
         });
-        if (st != WQ_OK) return st;
-        return pieces(lists, wqh::kMaxBlocks / 2, [&](unsigned now, int64_t first) {
-            list_kernel<<<now, T, 0, s>>>(p, first);
-        });
+        return st != WQ_OK ? st : list_all();
     }
-    const bool one = a.M <= 16 || (a.slots && a.L > 1 && a.M <= 256);
-    return pieces(div_up(a.M, kWindow), kMaxY, [&](unsigned windows, int64_t first) {
+    const bool one = a.M <= 16 || mixed(a);
+    const unsigned zs = unsigned(p.Z * p.rchunks);
+    int layers = div_up(lists, int64_t(p.splits) * zs);
+    if (layers > 16) {   // a launch of their own
+        layers = 0;
+        const wq_status st = list_all();
+        if (st != WQ_OK) return st;
+    }
+    return pieces(div_up(a.M, kWindow), kMaxY - 16, [&](unsigned windows, int64_t first) {
         p.window0 = int(first);
-        p.lists = first == 0 ? div_up(lists, int64_t(p.splits) * windows) : 0;
-        const dim3 grid(unsigned(p.splits), windows, unsigned(p.lists + p.Z * p.rchunks));
+        p.lists = first == 0 ? layers : 0;
+        const dim3 grid(unsigned(p.splits), unsigned(p.lists) + windows, zs);
         auto go = [&](auto n) {
             constexpr int NRT = decltype(n)::value;
             if (one && !d.t)
@@ -944,7 +977,7 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     const int wide = out ? div_up(C, 4 * kCols) : 1;   // blocks of 512 columns
     p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), windows * wide / 1024)));
     const int cblocks = div_up(wide, p.span);
-    p.halves = a.M > kWindow / 2 && windows * cblocks < 512 ? 2 : 1;
+    p.halves = a.M > kWindow / 2 && !mixed(a) && windows * cblocks < 512 ? 2 : 1;
     p.Z = shares(a.M, a.L, windows * cblocks * p.halves, 512);
     return pieces(windows, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
         p.window0 = int(first);
