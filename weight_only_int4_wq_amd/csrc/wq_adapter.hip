@@ -27,6 +27,7 @@ using wq::u4;
 constexpr int kWindow = 64;   // rows a block looks at: a wavefront's lanes
 constexpr int kChunk = 128;   // columns of src by which a shrink is split into ranges
 constexpr int kShrinkWaves = 8;
+constexpr int kPad = 128;     // numbers behind the last list: a round of the gradients reads whole ones
 constexpr int kCols = 128;    // columns of out and dw of a wavefront: 16 lanes of 8
 
 // Eight fp16 values at p, which need not be aligned to more than one of them
@@ -106,20 +107,40 @@ __device__ __forceinline__ float to_range(float most, int top, float& inverse) {
     inverse = __builtin_bit_cast(float, uint32_t(127 - k) << 23);
     return __builtin_bit_cast(float, uint32_t(127 + k) << 23);
 }
-__device__ __forceinline__ float finite_magnitude(float v) {
-    const float a = __builtin_fabsf(v);
-    return a <= 3.402823466e38f ? a : 0.f;
+// The largest finite magnitude of v (0 where there is none).  Infinities and NaN
+// sort above every number, so that one comparison tells whether to look again.
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N], bool& odd) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) most = max(most, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
+    odd = most >= 0x7F800000u;
+    if (odd) {
+        most = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t m = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
+            most = max(most, m < 0x7F800000u ? m : 0u);
+        }
+    }
+    return __builtin_bit_cast(float, most);
 }
 typedef float f2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack_h(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, wq::h2));
 }
-// a and b as sums of two fp16 numbers each (an infinity: itself and zero).
-__device__ __forceinline__ void split_h(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_h(a, b);
+// scale a and scale b (a power of two) as sums of two fp16 numbers each: the
+// second is what the first leaves, one multiply-add.
+__device__ __forceinline__ void split_h(float a, float b, float scale, uint32_t& hi, uint32_t& lo) {
+    hi = pack_h(a * scale, b * scale);
     const wq::h2 h = wq::as_h2(hi);
-    const float fa = float(h[0]), fb = float(h[1]);
-    lo = pack_h(a == fa ? 0.f : a - fa, b == fb ? 0.f : b - fb);
+    lo = pack_h(__builtin_fmaf(a, scale, -float(h[0])), __builtin_fmaf(b, scale, -float(h[1])));
+}
+// An infinity leaves NaN there: zero instead.
+__device__ __forceinline__ uint32_t without_rest(uint32_t hi, uint32_t lo) {
+    if ((hi & 0x7FFFu) == 0x7C00u) lo &= 0xFFFF0000u;
+    if ((hi & 0x7FFF0000u) == 0x7C000000u) lo &= 0xFFFFu;
+    return lo;
 }
 
 // --------------------------------------------------------------- shrink ----
@@ -135,7 +156,7 @@ struct Shrink {
     int Z, rchunks;        // blocks that share a window's adapters; 64-wide ranges of the rank
     // rows by adapter, for the gradients (null: not wanted)
     int32_t* start;        // [L + 1]
-    int32_t* list;         // [M]
+    int32_t* list;         // [M + kPad], zeros behind the rows
     int lists;             // layers of y that make them
     int window0;           // of this launch
 };
@@ -179,6 +200,7 @@ __device__ __forceinline__ void list_rows(const Shrink& p, int a, int* counts) {
         p.start[a] = start;
         if (a == p.L - 1) p.start[p.L] = start + all;
     }
+    if (a == p.L - 1 && threadIdx.x < kPad) p.list[start + all + threadIdx.x] = 0;
     if (!mine) return;
     int at = start + before;
 #pragma unroll 1
@@ -380,11 +402,11 @@ __device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cn
     for (int s = 0; s < p.splits; ++s, h += next)
 #pragma unroll
         for (int i = 0; i < RP / 16; ++i) v[i] += *reinterpret_cast<const f4*>(h + 4 * i);
-    float most = 0.f;
+    float all[RP / 4];
 #pragma unroll
-    for (int i = 0; i < RP / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) most = __builtin_fmaxf(most, finite_magnitude(v[i][j]));
+    for (int i = 0; i < RP / 4; ++i) all[i] = v[i >> 2][i & 3];
+    bool odd;
+    float most = largest(all, odd);
     most = __builtin_fmaxf(most, __shfl_xor(most, 1));
     most = __builtin_fmaxf(most, __shfl_xor(most, 2));
     float inverse;
@@ -392,10 +414,12 @@ __device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cn
     if (q == 0) back[row] = inverse;
     uint32_t* to = reinterpret_cast<uint32_t*>(parts + row * T::STRIDE + q * (RP / 4));
 #pragma unroll
-    for (int i = 0; i < RP / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            split_h(v[i][2 * j] * scale, v[i][2 * j + 1] * scale, to[2 * i + j], to[RP / 2 + 2 * i + j]);
+    for (int i = 0; i < RP / 8; ++i) {
+        uint32_t hi, lo;
+        split_h(all[2 * i], all[2 * i + 1], scale, hi, lo);
+        to[i] = hi;
+        to[RP / 2 + i] = odd ? without_rest(hi, lo) : lo;
+    }
     if (keep_sum && row < cnt) {
         float* at = p.sum + m * p.R;
 #pragma unroll
@@ -409,7 +433,7 @@ __device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cn
 }
 
 // One adapter's rows against the block's columns.
-template <int RP, bool DROP>
+template <int RP, bool DROP, bool ADD>
 __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, int cnt, int order, uint16_t* parts,
                                             float* back) {
     typedef ExpandTile<RP> T;
@@ -439,7 +463,7 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
     // where row 16 t + 4 g + i begins, from the window's first on
     auto row_at = [&](int t, int i) { return uint32_t(__shfl(order, min(16 * t + 4 * g + i, cnt - 1))) * p.C; };
     auto load_old = [&](u4 (&v)[4], int t, int c) {
-        if (p.add)
+        if constexpr (ADD)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = load8(off(ab, row_at(t, i) + c));
     };
@@ -458,10 +482,9 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
         for (int ct = 0; ct < p.span; ++ct) {
             const int c0 = wave0 + ct * 4 * kCols, c = held(c0 + 8 * c16, p.C);
             if (c0 >= p.C) break;
-            if (ct) {
-                load_w(c);
-                load_old(old, 0, c);
-            }
+            if (ct) load_w(c);
+            const bool last = ct + 1 == p.span || c0 + 4 * kCols >= p.C;
+            const int after = last ? c : held(c0 + 4 * kCols + 8 * c16, p.C);   // the next tile's column
             u4 w[T::KB][8];
 #pragma unroll
             for (int k = 0; k < T::KB; ++k) {
@@ -476,7 +499,9 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
             }
 #pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
-                if (t + 1 < tiles) load_old(fetched, t + 1, c);
+                // the next tile's old values (the very last one's again: a branch
+                // would end in a wait for them)
+                load_old(fetched, t + 1 < tiles ? t + 1 : last ? t : 0, t + 1 < tiles ? c : after);
                 f4 acc[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
@@ -525,7 +550,8 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) old[i] = p.add ? fetched[i] : u4{0, 0, 0, 0};
+                for (int i = 0; i < 4; ++i)
+                    if constexpr (ADD) old[i] = fetched[i];
             }
         }
     }
@@ -535,7 +561,7 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
 // Blocks: x the window (neighbours on different XCDs, a window's column blocks
 // on one, so that its h comes from memory once), y the column block, z the
 // halves of an adapter's rows and Z shares of the window's adapters.
-template <int RP, bool DROP>
+template <int RP, bool DROP, bool ADD>
 __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p) {
     __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * ExpandTile<RP>::STRIDE];
     __shared__ __attribute__((aligned(16))) float back[kWindow];
@@ -551,7 +577,7 @@ __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expa
     };
     each_adapter(slot, z, p.Z, [&](int a, int cnt, int order) {
         mine(cnt, order);
-        if (cnt > 0) expand_rows<RP, DROP>(p, m0, a, cnt, order, parts, back);
+        if (cnt > 0) expand_rows<RP, DROP, ADD>(p, m0, a, cnt, order, parts, back);
     });
 
     // rows without an adapter
@@ -609,7 +635,7 @@ struct Outer {
 // are added to the fp32 sums.
 // Blocks: x the column tiles of both gradients, y the range of rows, z the
 // rank's 64s and the adapter.
-template <int RW>
+template <int RW, bool LIST>
 __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     __shared__ u4 xs[4 * 8 * 64];                        // [step][column fragment][lane]
     __shared__ u4 hs[RW > 1 ? 4 * RW * 2 * 64 : 1];      // [step][16 of the rank][first, second part][lane]
@@ -622,7 +648,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     const int tile = blockIdx.x - (second ? p.job[0].tiles : 0), split = blockIdx.y;
     const int r0 = p.rchunks > 1 ? (blockIdx.z & 1) * 64 : 0;
     const int a = p.adapter0 + int(p.rchunks > 1 ? blockIdx.z >> 1 : blockIdx.z);
-    const int at = p.start ? p.start[a] : 0, cnt = p.start ? p.start[a + 1] - at : a == 0 ? p.M : 0;
+    const int at = LIST ? p.start[a] : 0, cnt = LIST ? p.start[a + 1] - at : a == 0 ? p.M : 0;
     const int c = held(tile * kCols + 8 * c16, j.C);
     const bool drop = j.drop.t != 0;
     const uint64_t stream = drop ? wq::drop_stream(j.drop) : 0;
@@ -635,37 +661,41 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = f4{0.f, 0.f, 0.f, 0.f};
 
-    // rows 8 g + i of the wavefront's step (past the adapter's: its last one)
+    // Rows 8 g + i of the wavefront's step.  Past the adapter's: the list's next
+    // ones, which exist, or the last one.  (No branch joins behind these loads: the
+    // wait for them would be one for the products' loads before them.)
     auto rows = [&](int of, int (&m)[8]) {
-        const int n = of * 128 + wave * 32;
-        if (p.list && n + 32 <= cnt) {
-            __builtin_memcpy(m, p.list + at + n + 8 * g, 32);
-            return;
-        }
+        const int n = of * 128 + wave * 32 + 8 * g;
+        if constexpr (LIST)
+            __builtin_memcpy(m, p.list + at + n, 32);
+        else
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = min(n + 8 * g + i, cnt - 1);
-        if (p.list)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = p.list[at + m[i]];
+            for (int i = 0; i < 8; ++i) m[i] = min(n + i, p.M - 1);
     };
+    typedef float hvec __attribute__((ext_vector_type(RW)));
     u4 x[8];
-    float h[8][RW];
+    hvec hv[8];
     int m[8], next[8];
     auto load = [&] {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             x[i] = load8(j.src + int64_t(m[i]) * j.C + c);
-            __builtin_memcpy(h[i], j.h + int64_t(m[i]) * p.R + held_r, 4 * RW);
+            __builtin_memcpy(&hv[i], j.h + int64_t(m[i]) * p.R + held_r, 4 * RW);
         }
     };
     if (round < end) {
         rows(round, m);
         load();
-        rows(round + 1 < end ? round + 1 : round, next);
+        rows(min(round + 1, end - 1), next);
     }
 #pragma unroll 1
     for (; round < end; ++round) {
         const int first = round * 128 + wave * 32 + 8 * g;   // the lane's first row in the adapter's
+        float h[8][RW];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int t = 0; t < RW; ++t) h[i][t] = hv[i][t];
         if (drop)
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
@@ -705,9 +735,11 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
         transpose8(x, w);
 #pragma unroll
         for (int t = 0; t < RW; ++t) {
-            float most = 0.f, inverse;
+            float all[8], inverse;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, finite_magnitude(h[i][t]));
+            for (int i = 0; i < 8; ++i) all[i] = h[i][t];
+            bool odd;
+            float most = largest(all, odd);
             most = __builtin_fmaxf(most, __shfl_xor(most, 16));
             most = __builtin_fmaxf(most, __shfl_xor(most, 32));
             const float scale = to_range(most, 13, inverse);
@@ -719,10 +751,13 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t u, v;
-                split_h(h[2 * i][t] * scale, h[2 * i + 1][t] * scale, u, v);
+                split_h(all[2 * i], all[2 * i + 1], scale, u, v);
                 hi[t][i] = u;
                 lo[t][i] = v;
             }
+            if (odd)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lo[t][i] = without_rest(hi[t][i], lo[t][i]);
         }
         if constexpr (RW > 1) {
 #pragma unroll
@@ -733,12 +768,11 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
                 hs[((wave * RW + t) * 2 + 1) * 64 + lane] = lo[t];
             }
         }
-        if (round + 1 < end) {
+        // (the last round loads its own rows again: a branch would end in a wait for them)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = next[i];
-            load();
-            rows(round + 2 < end ? round + 2 : round, next);
-        }
+        for (int i = 0; i < 8; ++i) m[i] = next[i];
+        load();
+        rows(min(round + 2, end - 1), next);
         if (RW > 1) __syncthreads();
 #pragma unroll
         for (int q = 0; q < RW; ++q) {
@@ -983,10 +1017,15 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
         p.window0 = int(first);
         const dim3 grid(now, unsigned(cblocks), unsigned(p.Z * p.halves));
         auto go = [&](auto n) {
-            if (d.t)
-                expand_kernel<decltype(n)::value, true><<<grid, 256, 0, s>>>(p);
+            constexpr int RP = decltype(n)::value;
+            if (d.t && add)
+                expand_kernel<RP, true, true><<<grid, 256, 0, s>>>(p);
+            else if (d.t)
+                expand_kernel<RP, true, false><<<grid, 256, 0, s>>>(p);
+            else if (add)
+                expand_kernel<RP, false, true><<<grid, 256, 0, s>>>(p);
             else
-                expand_kernel<decltype(n)::value, false><<<grid, 256, 0, s>>>(p);
+                expand_kernel<RP, false, false><<<grid, 256, 0, s>>>(p);
         };
         switch (padded_rank(a.R)) {
             case 16: go(Int<16>{}); break;
@@ -1018,12 +1057,18 @@ wq_status outer(const wqh::Adapters& a, Outer& p, hipStream_t s) {
     wq_status st = pieces(a.L, kMaxY / 2, [&](unsigned now, int64_t first) {
         p.adapter0 = int(first);
         const dim3 grid(tiles, unsigned(p.splits), now * unsigned(p.rchunks));
+        auto go = [&](auto rw) {
+            if (p.list)
+                outer_kernel<decltype(rw)::value, true><<<grid, 256, 0, s>>>(p);
+            else
+                outer_kernel<decltype(rw)::value, false><<<grid, 256, 0, s>>>(p);
+        };
         if (RP == 16)
-            outer_kernel<1><<<grid, 256, 0, s>>>(p);
+            go(Int<1>{});
         else if (RP == 32)
-            outer_kernel<2><<<grid, 256, 0, s>>>(p);
+            go(Int<2>{});
         else
-            outer_kernel<4><<<grid, 256, 0, s>>>(p);
+            go(Int<4>{});
     });
     if (st != WQ_OK || p.splits == 1) return st;
     const int64_t n0 = (int64_t(a.L) * a.R * p.job[0].C + 3) / 4 * 4;
@@ -1049,7 +1094,7 @@ struct BackwardRoom {
         part = take(ShrinkPlan(M, R, L, N).bytes(M, R));
         dh = take(size_t(M) * R * 4);
         start = take((size_t(L) + 1) * 4);
-        list = take(size_t(M) * 4);
+        list = take((size_t(M) + kPad) * 4);
         outer0 = take(grads * K);
         outer1 = take(grads * N);
         bytes = at;
