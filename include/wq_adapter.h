@@ -65,14 +65,17 @@ extern "C" {
 
 /* hidden (nullable) receives x' . down^T for the backward pass, without the
  * scale.  M = 0: nothing is done.  workspace: at least
- * wq_adapters_workspace_size bytes.
+ * wq_adapters_workspace_size bytes (0 for small decode batches without
+ * dropout: then it may be NULL).
  * WQ_ERR_ARG: null or misaligned pointers, bad sizes or p, overlaps, a short
  * workspace. */
 wq_status wq_adapters(const uint16_t* x, const uint16_t* down, const uint16_t* up, const float* scales,
                       const int32_t* slots, const uint16_t* base, double p, uint64_t seed, uint64_t offset,
                       const int64_t* step, uint16_t* y, float* hidden, int32_t M, int32_t N, int32_t K, int32_t rank,
                       int32_t adapters, void* workspace, size_t workspace_bytes, void* stream);
-size_t wq_adapters_workspace_size(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t adapters);
+/* has_dropout: whether p > 0; enough for both when set. */
+size_t wq_adapters_workspace_size(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t adapters,
+                                  int32_t has_dropout);
 
 /* For dy and the x, hidden and dropout numbers of the forward call:
  *   dh[m] = s[a] dy[m] . up[a]^T,  dx[m] = dropout'(dh[m] . down[a]) + dx_add[m],

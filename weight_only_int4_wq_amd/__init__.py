@@ -13,6 +13,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -73,8 +74,8 @@ _DROP = [ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _VP]
 _SIG["wq_adapters"] = (ctypes.c_int, [_VP] * 6 + _DROP + [_VP, _VP] + [_I32] * 5 + [_VP, _SIZE, _VP])
 _SIG["wq_adapters_backward"] = (ctypes.c_int, [_VP] * 7 + _DROP + [_VP] * 4 + [_I32] * 5 + [_VP, _SIZE, _VP])
 _SIG["wq_dropout"] = (ctypes.c_int, [_VP, _VP] + _DROP + [_VP, ctypes.c_int64, _VP])
-for _name in ("wq_adapters", "wq_adapters_backward"):
-    _SIG[_name + "_workspace_size"] = (_SIZE, [_I32] * 5)
+_SIG["wq_adapters_workspace_size"] = (_SIZE, [_I32] * 6)
+_SIG["wq_adapters_backward_workspace_size"] = (_SIZE, [_I32] * 5)
 
 # Activations of the block's products, by the numbers of wq_act.
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -745,22 +746,27 @@ def gated_backward(dh, preact, packed, scales, zeros, bits: int, group_size: int
 
 # -------------------------------------------- adapters and dropout ----
 
-def adapters_workspace_size(entry: str, M: int, N: int, K: int, rank: int, adapters: int) -> int:
-    """Bytes of workspace of `entry` ("adapters" or "adapters_backward")."""
+def adapters_workspace_size(entry: str, M: int, N: int, K: int, rank: int, adapters: int,
+                            has_dropout: bool = True) -> int:
+    """Bytes of workspace of `entry` ("adapters" or "adapters_backward");
+    "adapters" without dropout may need less (has_dropout=False)."""
     _sizes(M, N, K)
     _sizes(rank, adapters, 0)
+    if entry == "adapters":
+        return int(lib().wq_adapters_workspace_size(M, N, K, rank, adapters, int(bool(has_dropout))))
     return int(getattr(lib(), f"wq_{entry}_workspace_size")(M, N, K, rank, adapters))
 
 
 def _on_device(entry, device, args):
     """wq_<entry> on the tensors' device (made current for the call) and its
     current stream."""
-    torch = _torch()
+    torch = _torch_module
     if device.type != "cuda":
         raise ValueError(f"tensor arguments must be GPU tensors, got one on {device}")
-    fn = getattr(lib(), entry)
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() != device.index:
+    fn, at = getattr(_lib or lib(), entry), device.index
+    stream = torch._C._cuda_getCurrentRawStream(at)
+    # (the plain query: tensors on a GPU exist, so the runtime is initialised)
+    if torch._C._cuda_getDevice() != at:
         with torch.cuda.device(device):
             code = fn(*args, stream)
     else:
@@ -781,10 +787,11 @@ def _drop_args(p, seed, offset, step, device):
 def _pool_args(down, up, scales, slots, M, N, K, device):
     """Check a pool of adapters; returns (rank, adapters, the addresses of
     down, up, scales and slots)."""
-    torch = _torch()
-    if down.__class__ is not torch.Tensor or down.dim() != 3:
-        _dev(down, torch.float16, "down", 3, device=device)
-    count, rank, _ = down.shape
+    torch = _torch_module
+    T, half, index = torch.Tensor, torch.float16, device.index
+    if down.__class__ is not T or down.dim() != 3:
+        _dev(down, half, "down", 3, device=device)
+    count, rank, _ = shape = down.shape
     if not 1 <= rank <= 128:
         raise ValueError(f"ranks of 1 to 128 are supported, got {rank}")
     if count < 1 or N < 1 or K < 32 or K % 32:
@@ -793,21 +800,37 @@ def _pool_args(down, up, scales, slots, M, N, K, device):
     if M + N + K > 0x7FFFFFFF or count > 0x7FFFFFFF:
         _sizes(M, N, K)
         _sizes(count, 0, 0)
-    return rank, count, _arg(down, torch.float16, "down", (count, rank, K), device), \
-        _arg(up, torch.float16, "up", (count, rank, N), device), _arg(scales, torch.float32, "scales", (count,), device), \
+    # the checks of _arg in line: a decode call's kernel takes a few microseconds
+    if (index is not None and down.dtype is half and down.get_device() == index and down.is_contiguous()
+            and shape == (count, rank, K) and up.__class__ is T and up.dtype is half and up.get_device() == index
+            and up.is_contiguous() and up.shape == (count, rank, N) and scales.__class__ is T
+            and scales.dtype is torch.float32 and scales.get_device() == index and scales.is_contiguous()
+            and scales.shape == (count,)):
+        return rank, count, down.data_ptr(), up.data_ptr(), scales.data_ptr(), \
+            None if slots is None else _arg(slots, torch.int32, "slots", (M,), device)
+    return rank, count, _arg(down, half, "down", (count, rank, K), device), \
+        _arg(up, half, "up", (count, rank, N), device), _arg(scales, torch.float32, "scales", (count,), device), \
         _opt(slots, torch.int32, "slots", (M,), device)
 
 
-def _room(entry, workspace, M, N, K, rank, count, device):
-    """Address and bytes of the workspace, allocated where none is given."""
-    torch = _torch()
+@functools.lru_cache(maxsize=4096)
+def _adapters_need(entry, *sizes):
+    """Bytes of workspace for these sizes (a pure function of them)."""
+    return getattr(lib(), entry)(*sizes)
+
+
+def _room(workspace, device, M, entry, *sizes):
+    """The workspace, allocated where none is given, and its address and bytes."""
     if workspace is not None:
         workspace = _workspace_arg(workspace, device)
     elif M and device.type == "cuda":
-        need = getattr(lib(), entry)(M, N, K, rank, count)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+        need = _adapters_need(entry, M, *sizes)
+        if need:
+            workspace = _torch().empty((need,), dtype=_torch().uint8, device=device)
+    if workspace is None:
+        return None, None, 0
     # (the tensor is returned to live until the call is enqueued)
-    return workspace, (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def adapters(x, down, up, scales, slots=None, base=None, p: float = 0.0, seed: int = 0, offset: int = 0, step=None,
@@ -835,9 +858,9 @@ def adapters(x, down, up, scales, slots=None, base=None, p: float = 0.0, seed: i
     if (x.requires_grad or down.requires_grad or up.requires_grad or _needs_gradient(scales)
             or base is not None and _needs_gradient(base)) and torch.is_grad_enabled():
         _say_detached_call("x, down, up, scales or base")
-    base_at = _opt(base, half, "base", (M, N), d)
+    base_at = None if base is None else _arg(base, half, "base", (M, N), d)
     if out is None:
-        out = torch.empty((M, N), dtype=half, device=d)
+        out = x.new_empty((M, N)) if base is None else torch.empty_like(base)
         y = out.data_ptr()
     else:
         y = _arg(out, half, "out", (M, N), d)
@@ -845,11 +868,12 @@ def adapters(x, down, up, scales, slots=None, base=None, p: float = 0.0, seed: i
     if hidden is not None:
         h = _arg(hidden, torch.float32, "hidden", (M, rank), d)
     elif save_hidden:
-        hidden = torch.empty((M, rank), dtype=torch.float32, device=d)
+        hidden = x.new_empty((M, rank), dtype=torch.float32)
         h = hidden.data_ptr()
-    workspace, room = _room("wq_adapters_workspace_size", workspace, M, N, K, rank, count, d)
+    workspace, ws, nbytes = _room(workspace, d, M, "wq_adapters_workspace_size", N, K, rank, count,
+                                  int(p * 65536 + 0.5 >= 1))
     _on_device("wq_adapters", d, (x.data_ptr(), down_at, up_at, scales_at, slots_at, base_at, *drop, y, h, M, N, K, rank,
-                                  count, *room))
+                                  count, ws, nbytes))
     return out if hidden is None else (out, hidden)
 
 
@@ -881,20 +905,20 @@ def adapters_backward(dy, x, hidden, down, up, scales, slots=None, p: float = 0.
         if out is not None or dx_add is not None:
             raise ValueError("out and dx_add are for a call that needs dx")
     elif out is None:
-        out = torch.empty((M, K), dtype=half, device=d)
+        out = dy.new_empty((M, K))
         dx = out.data_ptr()
     else:
         dx = _arg(out, half, "out", (M, K), d)
     if need_weights:
         x_at = _arg(x, half, "x", (M, K), d)
         h = _arg(hidden, torch.float32, "hidden", (M, rank), d)
-        ddown = torch.empty((count, rank, K), dtype=torch.float32, device=d)
-        dup = torch.empty((count, rank, N), dtype=torch.float32, device=d)
-    workspace, room = _room("wq_adapters_backward_workspace_size", workspace, M, N, K, rank, count, d)
+        ddown = dy.new_empty((count, rank, K), dtype=torch.float32)
+        dup = dy.new_empty((count, rank, N), dtype=torch.float32)
+    workspace, ws, nbytes = _room(workspace, d, M, "wq_adapters_backward_workspace_size", N, K, rank, count)
     _on_device("wq_adapters_backward", d,
                (dy.data_ptr(), x_at, h, down_at, up_at, scales_at, slots_at, *drop, add_at, dx,
                 None if ddown is None else ddown.data_ptr(), None if dup is None else dup.data_ptr(), M, N, K, rank,
-                count, *room))
+                count, ws, nbytes))
     return out, ddown, dup
 
 

@@ -26,7 +26,7 @@ using wq::u4;
 
 constexpr int kWindow = 64;   // rows a block looks at: a wavefront's lanes
 constexpr int kChunk = 128;   // columns of src by which a shrink is split into ranges
-constexpr int kShrinkWaves = 8;
+constexpr int kShrinkWaves = 8, kDirectWaves = 8;
 constexpr int kPad = 128;     // numbers behind the last list: a round of the gradients reads whole ones
 constexpr int kCols = 128;    // columns of out and dw of a wavefront: 16 lanes of 8
 
@@ -38,6 +38,10 @@ __device__ __forceinline__ u4 load8(const uint16_t* p) {
     return v;
 }
 __device__ __forceinline__ void store8(uint16_t* p, u4 v) { __builtin_memcpy(p, &v, 16); }
+
+// The wavefront's number, as the scalar that it is: the matrix instructions do not
+// heed the execution mask, so what leads to them has to branch.
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // Within a window or an adapter, element numbers fit 32 bits (64 rows, or 128
 // of the rank, of at most 2^22 columns): a uniform base and a 32-bit offset,
@@ -165,7 +169,7 @@ struct Shrink {
 // wavefronts take a range of rows each, count the rows of lower adapters (their
 // sum is the list's start) and their own, and write those in order.
 __device__ __forceinline__ void list_rows(const Shrink& p, int a, int* counts) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_of();
     if (a >= p.L) return;
     constexpr int U = 4;
     const int each = (p.M + 64 * U * kShrinkWaves - 1) / (64 * U * kShrinkWaves) * 64 * U;
@@ -224,7 +228,7 @@ template <int MT, int NRT, bool DROP, bool AHEAD>
 __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, int cnt, int order, int r0, int split,
                                             f4* sum) {
     constexpr int STEPS = MT * NRT > 8 ? 1 : 2, COLS = 32 * STEPS;   // 128 bytes of a row, or what the registers hold
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_of(), c16 = lane & 15, g = lane >> 4;
     f4 acc[MT][NRT];
     const uint16_t* const xb = p.src + m0 * p.C;
     const uint16_t* const wb = p.w + int64_t(a) * p.R * p.C;
@@ -432,12 +436,90 @@ __device__ __forceinline__ void expand_parts(const Expand& p, int64_t m0, int cn
     }
 }
 
+// 32 rows of w (16, twice, where both parts share a fragment) at the lane's eight
+// columns; those past the rank repeat its last one.
+template <int RP>
+__device__ __forceinline__ void load_w(u4 (&v)[8], const uint16_t* wb, int k, int c, int R, int C) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = ExpandTile<RP>::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i;
+        v[i] = load8(off(wb, uint32_t(min(r, R - 1)) * C + c));
+    }
+}
+// ... into fragments, with zeros past the rank, as h has there.
+template <int RP>
+__device__ __forceinline__ void make_w(u4 (&v)[8], u4 (&w)[8], int k, int R) {
+    const int g = (threadIdx.x & 63) >> 4;
+    if (R < RP) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((ExpandTile<RP>::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i) >= R) v[i] = u4{0, 0, 0, 0};
+    }
+    transpose8(v, w);
+}
+
+// 16 rows of h (their parts) times the wavefront's 128 columns of w, onto their
+// old values.  at: where the lane's four rows and columns begin, from ob on; c0
+// the tile's first column, c the lane's; n: rows of the 16 that are.
+template <int RP, bool DROP>
+__device__ __forceinline__ void expand_tile(const uint16_t* parts, const float* back, const u4 (&w)[ExpandTile<RP>::KB][8],
+                                            const u4 (&old)[4], float s, const uint32_t (&at)[4], uint16_t* ob, int c0,
+                                            int c, int C, int n, const Drop& d, uint64_t stream, uint64_t eight) {
+    typedef ExpandTile<RP> T;
+    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+    f4 acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+    const uint16_t* h = parts + c16 * T::STRIDE + 8 * g;
+#pragma unroll
+    for (int k = 0; k < T::KB; ++k) {
+        const u4 hi = *reinterpret_cast<const u4*>(h + 32 * k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = mfma(hi, w[k][j], acc[j]);
+        if constexpr (!T::BOTH) {
+            const u4 lo = *reinterpret_cast<const u4*>(h + RP + 32 * k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
+        }
+    }
+    u4 keep[4];
+    if constexpr (DROP) {
+        uint64_t m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = eight + (at[i] >> 3);
+        wq::keep8(m, d, stream, keep);
+    }
+    const f4 inverse = *reinterpret_cast<const f4*>(back + 4 * g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (a power of two: exact but where the result is below fp16's numbers anyway)
+        const float f = inverse[i] * s;
+        u4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const wq::h2 o = wq::as_h2(old[i][j]);
+            v[j] = pack_h(__builtin_fmaf(acc[2 * j][i], f, float(o[0])),
+                          __builtin_fmaf(acc[2 * j + 1][i], f, float(o[1])));
+        }
+        if constexpr (DROP) v = (v & keep[i]) | (old[i] & ~keep[i]);
+        if (4 * g + i >= n) continue;
+        if (C - 8 >= c0) {
+            store8(off(ob, at[i]), v);
+        } else {   // the last, fewer than eight columns: those before c0 are another tile's
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                if (c + j >= c0) off(ob, at[i])[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+}
+
 // One adapter's rows against the block's columns.
 template <int RP, bool DROP, bool ADD>
 __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, int cnt, int order, uint16_t* parts,
                                             float* back) {
     typedef ExpandTile<RP> T;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4, cb = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = wave_of(), c16 = lane & 15, g = lane >> 4, cb = blockIdx.y;
     const uint64_t stream = DROP ? wq::drop_stream(p.drop) : 0, eight = uint64_t(m0) * (p.C / 8);
     const uint16_t* const wb = p.w + int64_t(a) * p.R * p.C;
     const uint16_t* const ab = p.add + m0 * p.C;
@@ -448,17 +530,10 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
     u4 raw[AHEAD ? T::KB : 1][8], old[4], fetched[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) old[i] = u4{0, 0, 0, 0};
-    auto load_piece = [&](u4 (&v)[8], int k, int c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i;
-            v[i] = load8(off(wb, uint32_t(min(r, p.R - 1)) * p.C + c));
-        }
-    };
-    auto load_w = [&](int c) {
+    auto load_ahead = [&](int c) {
         if constexpr (AHEAD)
 #pragma unroll
-            for (int k = 0; k < T::KB; ++k) load_piece(raw[k], k, c);
+            for (int k = 0; k < T::KB; ++k) load_w<RP>(raw[k], wb, k, c, p.R, p.C);
     };
     // where row 16 t + 4 g + i begins, from the window's first on
     auto row_at = [&](int t, int i) { return uint32_t(__shfl(order, min(16 * t + 4 * g + i, cnt - 1))) * p.C; };
@@ -471,7 +546,7 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
     const bool any = p.out && wave0 < p.C;
     if (any) {
         const int c = held(wave0 + 8 * c16, p.C);
-        load_w(c);
+        load_ahead(c);
         load_old(old, 0, c);
     }
     expand_parts<RP>(p, m0, cnt, order, p.sum && cb == 0, parts, back);
@@ -482,76 +557,29 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
         for (int ct = 0; ct < p.span; ++ct) {
             const int c0 = wave0 + ct * 4 * kCols, c = held(c0 + 8 * c16, p.C);
             if (c0 >= p.C) break;
-            if (ct) load_w(c);
+            if (ct) load_ahead(c);
             const bool last = ct + 1 == p.span || c0 + 4 * kCols >= p.C;
             const int after = last ? c : held(c0 + 4 * kCols + 8 * c16, p.C);   // the next tile's column
             u4 w[T::KB][8];
 #pragma unroll
             for (int k = 0; k < T::KB; ++k) {
                 u4(&v)[8] = raw[AHEAD ? k : 0];
-                if constexpr (!AHEAD) load_piece(v, k, c);
-                if (p.R < RP) {   // rows past the rank: zeros, as h is there
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if ((T::BOTH ? 8 * (g & 1) + i : 32 * k + 8 * g + i) >= p.R) v[i] = u4{0, 0, 0, 0};
-                }
-                transpose8(v, w[k]);
+                if constexpr (!AHEAD) load_w<RP>(v, wb, k, c, p.R, p.C);
+                make_w<RP>(v, w[k], k, p.R);
             }
 #pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
                 // the next tile's old values (the very last one's again: a branch
                 // would end in a wait for them)
                 load_old(fetched, t + 1 < tiles ? t + 1 : last ? t : 0, t + 1 < tiles ? c : after);
-                f4 acc[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
-                const uint16_t* h = parts + (16 * t + c16) * T::STRIDE + 8 * g;
-#pragma unroll
-                for (int k = 0; k < T::KB; ++k) {
-                    const u4 hi = *reinterpret_cast<const u4*>(h + 32 * k);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] = mfma(hi, w[k][j], acc[j]);
-                    if constexpr (!T::BOTH) {
-                        const u4 lo = *reinterpret_cast<const u4*>(h + RP + 32 * k);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
-                    }
-                }
                 uint32_t at[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) at[i] = row_at(t, i) + c;
-                u4 keep[4];
-                if constexpr (DROP) {
-                    uint64_t n[4];
+                expand_tile<RP, DROP>(parts + 16 * t * T::STRIDE, back + 16 * t, w, old, s, at, ob, c0, c, p.C,
+                                      cnt - 16 * t, p.drop, stream, eight);
+                if constexpr (ADD)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) n[i] = eight + (at[i] >> 3);
-                    wq::keep8(n, p.drop, stream, keep);
-                }
-                const f4 inverse = *reinterpret_cast<const f4*>(back + 16 * t + 4 * g);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // (a power of two: exact but where the result is below fp16's numbers anyway)
-                    const float f = inverse[i] * s;
-                    u4 v;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const wq::h2 o = wq::as_h2(old[i][j]);
-                        v[j] = pack_h(__builtin_fmaf(acc[2 * j][i], f, float(o[0])),
-                                      __builtin_fmaf(acc[2 * j + 1][i], f, float(o[1])));
-                    }
-                    if constexpr (DROP) v = (v & keep[i]) | (old[i] & ~keep[i]);
-                    if (16 * t + 4 * g + i >= cnt) continue;
-                    if (p.C - 8 >= c0) {
-                        store8(off(ob, at[i]), v);
-                    } else {   // the last, fewer than eight columns: those before c0 are another tile's
-#pragma unroll
-                        for (int j = 1; j < 8; ++j)
-                            if (c + j >= c0) off(ob, at[i])[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if constexpr (ADD) old[i] = fetched[i];
+                    for (int i = 0; i < 4; ++i) old[i] = fetched[i];
             }
         }
     }
@@ -565,7 +593,7 @@ template <int RP, bool DROP, bool ADD>
 __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p) {
     __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * ExpandTile<RP>::STRIDE];
     __shared__ __attribute__((aligned(16))) float back[kWindow];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_of(), c16 = lane & 15, g = lane >> 4;
     const int half = p.halves > 1 ? blockIdx.z & 1 : 0, z = p.halves > 1 ? blockIdx.z >> 1 : blockIdx.z;
     const int64_t m0 = int64_t(p.window0 + int(blockIdx.x)) * kWindow;
     const int slot = slot_of(p.slots, m0 + lane, p.M, p.L);
@@ -599,6 +627,150 @@ __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expa
             const int i = i0 + threadIdx.x;
             const int64_t m = m0 + __shfl(order, (i / p.R) & 63);
             if (i < cnt * p.R) p.sum[m * p.R + i % p.R] = 0.f;
+        }
+}
+
+// --------------------------------------------------------------- direct ----
+
+struct Direct {
+    const uint16_t* x;     // [M][K]
+    const uint16_t* down;  // [L][R][K]
+    const uint16_t* up;    // [L][R][N]
+    const float* scales;
+    const int32_t* slots;
+    const uint16_t* base;  // [M][N], nullable, may be y
+    uint16_t* y;           // [M][N]
+    float* hidden;         // [M][R], nullable
+    int M, R, L, K, N;
+    int Z, waves;          // blocks that share the window's adapters; wavefronts with columns of y
+};
+
+// Both products of a decode batch in one launch.  Every block makes h of its
+// adapter's rows itself, its wavefronts an eighth of K each, while the
+// second product's operands are on their way; `waves` of them then take 128
+// columns each.  A launch of 2 x 4 us and the wait between the two products
+// become one of 5, for reading down once per column block, from L2: worth it
+// while that is a few hundred KB.
+template <int RP, bool ADD>
+__global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct p) {
+    typedef ExpandTile<RP> T;
+    constexpr int NRT = RP / 16, STEPS = 4 / NRT, COLS = 32 * STEPS, NEXT = kDirectWaves * COLS;
+    __shared__ f4 sum[kDirectWaves * NRT * 64];
+    __shared__ __attribute__((aligned(16))) uint16_t parts[16 * T::STRIDE];
+    __shared__ __attribute__((aligned(16))) float back[16];
+    const int lane = threadIdx.x & 63, wave = wave_of(), c16 = lane & 15, g = lane >> 4;
+    const int y0 = (int(blockIdx.x) * p.waves + wave) * kCols, yc = held(y0 + 8 * c16, p.N);
+    const bool mine = wave < p.waves && y0 < p.N;   // has columns of y
+    const int slot = slot_of(p.slots, lane, p.M, p.L);
+
+    each_adapter(slot, blockIdx.y, p.Z, [&](int a, int cnt, int order) {
+        const uint16_t* const db = p.down + int64_t(a) * p.R * p.K;
+#pragma unroll 1
+        for (; cnt > 0; cnt -= 16, order = __shfl(order, (lane + 16) & 63)) {
+            uint32_t at[4];
+            u4 raw[8], old[4], w[T::KB][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                old[i] = u4{0, 0, 0, 0};
+                at[i] = uint32_t(__shfl(order, min(4 * g + i, cnt - 1))) * p.N + yc;
+            }
+            if (mine) {
+                load_w<RP>(raw, p.up + int64_t(a) * p.R * p.N, 0, yc, p.R, p.N);
+                if constexpr (ADD)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) old[i] = load8(off(p.base, at[i]));
+            }
+            const uint32_t xr = uint32_t(__shfl(order, min(c16, cnt - 1))) * p.K;
+            uint32_t wr[NRT];
+            f4 acc[NRT];
+#pragma unroll
+            for (int n = 0; n < NRT; ++n) {
+                wr[n] = uint32_t(min(16 * n + c16, p.R - 1)) * p.K;
+                acc[n] = f4{0.f, 0.f, 0.f, 0.f};
+            }
+            struct Part {
+                u4 x[STEPS], w[NRT][STEPS];
+            } v, next;
+            auto load = [&](int c0, Part& q) {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int c = held(c0 + 32 * i + 8 * g, p.K);
+                    q.x[i] = load8(off(p.x, xr + c));
+#pragma unroll
+                    for (int n = 0; n < NRT; ++n) q.w[n][i] = load8(off(db, wr[n] + c));
+                }
+            };
+            int c0 = wave * COLS;
+            if (c0 < p.K) load(c0, v);
+#pragma unroll 1
+            for (; c0 < p.K; c0 += NEXT) {
+                if (c0 + NEXT < p.K) load(c0 + NEXT, next);
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    if (c0 + 32 * i >= p.K) continue;   // (K is a multiple of 32: held ones are whole steps)
+#pragma unroll
+                    for (int n = 0; n < NRT; ++n) acc[n] = mfma(v.x[i], v.w[n][i], acc[n]);
+                }
+                v = next;
+            }
+#pragma unroll
+            for (int n = 0; n < NRT; ++n) sum[(n * kDirectWaves + wave) * 64 + lane] = acc[n];
+            __syncthreads();
+            if (wave == 0) {   // rows 4 g + i, columns 16 n + l % 16 of h, summed in order, scaled and split
+#pragma unroll
+                for (int n = 0; n < NRT; ++n) {
+                    acc[n] = sum[n * kDirectWaves * 64 + lane];
+#pragma unroll
+                    for (int q = 1; q < kDirectWaves; ++q) acc[n] += sum[(n * kDirectWaves + q) * 64 + lane];
+                    if (16 * n + c16 >= p.R) acc[n] = f4{0.f, 0.f, 0.f, 0.f};
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float all[NRT], inverse;
+#pragma unroll
+                    for (int n = 0; n < NRT; ++n) all[n] = acc[n][i];
+                    bool odd;
+                    float most = largest(all, odd);
+#pragma unroll
+                    for (int o = 1; o < 16; o *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, o));
+                    const float scale = to_range(most, 13, inverse);
+                    if (c16 == 0) back[4 * g + i] = inverse;
+                    uint16_t* to = parts + (4 * g + i) * T::STRIDE + c16;
+                    const int64_t m = __shfl(order, min(4 * g + i, cnt - 1));
+#pragma unroll
+                    for (int n = 0; n < NRT; ++n) {
+                        uint32_t hi, lo;
+                        split_h(all[n], 0.f, scale, hi, lo);
+                        if (odd) lo = without_rest(hi, lo);
+                        to[16 * n] = uint16_t(hi);
+                        to[RP + 16 * n] = uint16_t(lo);
+                        if (p.hidden && blockIdx.x == 0 && 4 * g + i < cnt && 16 * n + c16 < p.R)
+                            p.hidden[m * p.R + 16 * n + c16] = all[n];
+                    }
+                }
+            }
+            __syncthreads();
+            if (mine) {
+                make_w<RP>(raw, w[0], 0, p.R);
+                expand_tile<RP, false>(parts, back, w, old, p.scales[a], at, p.y, y0, yc, p.N, cnt, Drop{}, 0, 0);
+            }
+        }
+    });
+
+    // rows without an adapter
+    const uint64_t none = blockIdx.y == 0 ? __ballot(slot < 0 && lane < p.M) : 0;
+    if (!none) return;
+    const int cnt = __builtin_popcountll(none), order = compact(none);
+    if (mine && p.y != p.base)
+        for (int row = 0; row < cnt; row += 4) {
+            const uint32_t at = uint32_t(__shfl(order, min(row + g, cnt - 1))) * p.N + yc;
+            store8(off(p.y, at), ADD ? load8(off(p.base, at)) : u4{0, 0, 0, 0});
+        }
+    if (p.hidden && blockIdx.x == 0)
+        for (int i0 = 0; i0 < cnt * p.R; i0 += 64 * kDirectWaves) {
+            const int i = i0 + threadIdx.x;
+            const int64_t m = __shfl(order, (i / p.R) & 63);
+            if (i < cnt * p.R) p.hidden[m * p.R + i % p.R] = 0.f;
         }
 }
 
@@ -640,7 +812,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     __shared__ u4 xs[4 * 8 * 64];                        // [step][column fragment][lane]
     __shared__ u4 hs[RW > 1 ? 4 * RW * 2 * 64 : 1];      // [step][16 of the rank][first, second part][lane]
     __shared__ f4 back[RW > 1 ? 4 * RW * 4 : 1];         // [step][16 of the rank][16]: the powers' inverses
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_of(), c16 = lane & 15, g = lane >> 4;
     const int group = wave / RW * RW;   // the first wavefront whose rows this one takes
     const int mine = wave - group;      // which 16 of the rank: r0 + RW * (row of the fragment) + mine
     const bool second = int(blockIdx.x) >= p.job[0].tiles;
@@ -1036,6 +1208,34 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     });
 }
 
+// Whether a forward pass without dropout is one launch: up to kDirectM rows that
+// differ in their adapters, or 16 that do not, a rank that fits a fragment, and a
+// first factor that every block can read for itself.
+constexpr int kDirectM = 32;
+constexpr int kDirectBytes = 384 << 10;
+bool direct_fits(int M, int N, int K, int R, int L) {
+    return M <= (L > 1 ? kDirectM : 16) && padded_rank(R) <= 32 && int64_t(padded_rank(R)) * K * 2 <= kDirectBytes &&
+           N >= 8;
+}
+
+wq_status direct(const wqh::Adapters& a, const uint16_t* x, const uint16_t* down, const uint16_t* up,
+                 const uint16_t* base, uint16_t* y, float* hidden, int N, int K, hipStream_t s) {
+    Direct p{x, down, up, a.scales, a.slots, base, y, hidden, a.M, a.R, a.L, K, N, std::min(a.L, a.M), 4};
+    if (int64_t(div_up(N, 4 * kCols)) * p.Z > 256) p.waves = kDirectWaves;
+    const dim3 grid(unsigned(div_up(N, p.waves * kCols)), unsigned(p.Z));
+    auto go = [&](auto n) {
+        if (base)
+            direct_kernel<decltype(n)::value, true><<<grid, 64 * kDirectWaves, 0, s>>>(p);
+        else
+            direct_kernel<decltype(n)::value, false><<<grid, 64 * kDirectWaves, 0, s>>>(p);
+    };
+    if (padded_rank(a.R) == 16)
+        go(Int<16>{});
+    else
+        go(Int<32>{});
+    return wqh::launch_status();
+}
+
 // Ranges of rows of the gradients.
 int outer_splits(int M, int R, int L, int K, int N) {
     const int64_t blocks = int64_t(L) * (padded_rank(R) > 64 ? 2 : 1) * (div_up(K, kCols) + div_up(N, kCols));
@@ -1105,10 +1305,13 @@ struct BackwardRoom {
 
 namespace wqh {
 
-size_t adapters_workspace(int M, int, int K, int R, int L) { return ShrinkPlan(M, R, L, K).bytes(M, R); }
+size_t adapters_workspace(int M, int N, int K, int R, int L, bool dropping) {
+    return !dropping && direct_fits(M, N, K, R, L) ? 0 : ShrinkPlan(M, R, L, K).bytes(M, R);
+}
 
 wq_status adapters_forward(const Adapters& a, const uint16_t* x, const uint16_t* down, const uint16_t* up,
                            const uint16_t* base, uint16_t* y, float* hidden, int N, int K, void* ws, hipStream_t s) {
+    if (!a.drop.t && direct_fits(a.M, N, K, a.R, a.L)) return direct(a, x, down, up, base, y, hidden, N, K, s);
     float* part = static_cast<float*>(ws);
     const wq_status st = shrink(a, x, down, a.drop, part, K, nullptr, nullptr, s);
     return st != WQ_OK ? st

@@ -67,7 +67,7 @@ extern "C" wq_status wq_adapters(const uint16_t* x, const uint16_t* down, const 
     if (rank > kMaxRank) return WQ_ERR_UNSUPPORTED;
     if (M == 0) return WQ_OK;
     if (!x || !down || !up || !scales || !y) return WQ_ERR_ARG;
-    const size_t need = wqh::adapters_workspace(M, N, K, rank, adapters);
+    const size_t need = wqh::adapters_workspace(M, N, K, rank, adapters, a.drop.t != 0);
     if (need > (workspace ? workspace_bytes : 0)) return WQ_ERR_ARG;
     const size_t ny = size_t(M) * N * 2, pool = size_t(adapters) * rank * 2;
     if (clash({{y, ny}, {hidden, size_t(M) * rank * 4}, {workspace, workspace_bytes}},
@@ -77,9 +77,10 @@ extern "C" wq_status wq_adapters(const uint16_t* x, const uint16_t* down, const 
     return wqh::adapters_forward(a, x, down, up, base, y, hidden, N, K, workspace, static_cast<hipStream_t>(stream));
 }
 
-extern "C" size_t wq_adapters_workspace_size(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t adapters) {
+extern "C" size_t wq_adapters_workspace_size(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t adapters,
+                                             int32_t has_dropout) {
     return sizes_ok(M, N, K, rank, adapters) && rank <= kMaxRank && M > 0
-               ? wqh::adapters_workspace(M, N, K, rank, adapters) : 0;
+               ? wqh::adapters_workspace(M, N, K, rank, adapters, has_dropout != 0) : 0;
 }
 
 extern "C" wq_status wq_adapters_backward(const uint16_t* dy, const uint16_t* x, const float* hidden,

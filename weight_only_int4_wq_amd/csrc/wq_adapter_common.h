@@ -86,7 +86,7 @@ struct Adapters {
     wq::Drop drop;
 };
 
-size_t adapters_workspace(int M, int N, int K, int R, int L);
+size_t adapters_workspace(int M, int N, int K, int R, int L, bool dropping);
 wq_status adapters_forward(const Adapters& a, const uint16_t* x, const uint16_t* down, const uint16_t* up,
                            const uint16_t* base, uint16_t* y, float* hidden, int N, int K, void* ws, hipStream_t s);
 size_t adapters_backward_workspace(int M, int N, int K, int R, int L);
