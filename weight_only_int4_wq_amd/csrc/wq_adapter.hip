@@ -646,15 +646,15 @@ struct Direct {
 };
 
 // Both products of a decode batch in one launch.  Every block makes h of its
-// adapter's rows itself, its wavefronts an eighth of K each, while the
-// second product's operands are on their way; `waves` of them then take 128
-// columns each.  A launch of 2 x 4 us and the wait between the two products
+// adapter's rows itself, its wavefronts an eighth of K each, up to 4096
+// in one go (rank 16); the second product's operands are on their way while those meet, and `waves` of
+// the wavefronts then take 128 columns each.  A launch of 2 x 4 us and the wait between the two products
 // become one of 5, for reading down once per column block, from L2: worth it
 // while that is a few hundred KB.
 template <int RP, bool ADD>
 __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct p) {
     typedef ExpandTile<RP> T;
-    constexpr int NRT = RP / 16, STEPS = 4 / NRT, COLS = 32 * STEPS, NEXT = kDirectWaves * COLS;
+    constexpr int NRT = RP / 16, STEPS = 16 / NRT, COLS = 32 * STEPS, NEXT = kDirectWaves * COLS;
     __shared__ f4 sum[kDirectWaves * NRT * 64];
     __shared__ __attribute__((aligned(16))) uint16_t parts[16 * T::STRIDE];
     __shared__ __attribute__((aligned(16))) float back[16];
@@ -674,12 +674,6 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
                 old[i] = u4{0, 0, 0, 0};
                 at[i] = uint32_t(__shfl(order, min(4 * g + i, cnt - 1))) * p.N + yc;
             }
-            if (mine) {
-                load_w<RP>(raw, p.up + int64_t(a) * p.R * p.N, 0, yc, p.R, p.N);
-                if constexpr (ADD)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) old[i] = load8(off(p.base, at[i]));
-            }
             const uint32_t xr = uint32_t(__shfl(order, min(c16, cnt - 1))) * p.K;
             uint32_t wr[NRT];
             f4 acc[NRT];
@@ -690,28 +684,28 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
             }
             struct Part {
                 u4 x[STEPS], w[NRT][STEPS];
-            } v, next;
-            auto load = [&](int c0, Part& q) {
+            } v;
+#pragma unroll 1
+            for (int c0 = wave * COLS; c0 < p.K; c0 += NEXT) {
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     const int c = held(c0 + 32 * i + 8 * g, p.K);
-                    q.x[i] = load8(off(p.x, xr + c));
+                    v.x[i] = load8(off(p.x, xr + c));
 #pragma unroll
-                    for (int n = 0; n < NRT; ++n) q.w[n][i] = load8(off(db, wr[n] + c));
+                    for (int n = 0; n < NRT; ++n) v.w[n][i] = load8(off(db, wr[n] + c));
                 }
-            };
-            int c0 = wave * COLS;
-            if (c0 < p.K) load(c0, v);
-#pragma unroll 1
-            for (; c0 < p.K; c0 += NEXT) {
-                if (c0 + NEXT < p.K) load(c0 + NEXT, next);
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     if (c0 + 32 * i >= p.K) continue;   // (K is a multiple of 32: held ones are whole steps)
 #pragma unroll
                     for (int n = 0; n < NRT; ++n) acc[n] = mfma(v.x[i], v.w[n][i], acc[n]);
                 }
-                v = next;
+            }
+            if (mine) {   // in flight while the sums meet
+                load_w<RP>(raw, p.up + int64_t(a) * p.R * p.N, 0, yc, p.R, p.N);
+                if constexpr (ADD)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) old[i] = load8(off(p.base, at[i]));
             }
 #pragma unroll
             for (int n = 0; n < NRT; ++n) sum[(n * kDirectWaves + wave) * 64 + lane] = acc[n];
