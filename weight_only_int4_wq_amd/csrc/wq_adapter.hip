@@ -1233,7 +1233,7 @@ wq_status direct(const wqh::Adapters& a, const uint16_t* x, const uint16_t* down
 // Ranges of rows of the gradients.
 int outer_splits(int M, int R, int L, int K, int N) {
     const int64_t blocks = int64_t(L) * (padded_rank(R) > 64 ? 2 : 1) * (div_up(K, kCols) + div_up(N, kCols));
-    return int(std::max<int64_t>(1, std::min<int64_t>(std::min(div_up(M, 128), 32), 1024 / blocks)));
+    return int(std::max<int64_t>(1, std::min<int64_t>(std::min(div_up(div_up(M, L), 128), 32), 1024 / blocks)));
 }
 
 wq_status outer(const wqh::Adapters& a, Outer& p, hipStream_t s) {
