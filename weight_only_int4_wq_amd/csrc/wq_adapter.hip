@@ -645,17 +645,21 @@ struct Direct {
     int Z, waves;          // blocks that share the window's adapters; wavefronts with columns of y
 };
 
-// Both products of a decode batch in one launch.  Every block makes h of its
-// adapter's rows itself, its wavefronts an eighth of K each, up to 4096
-// in one go (rank 16); the second product's operands are on their way while those meet, and `waves` of
-// the wavefronts then take 128 columns each.  A launch of 2 x 4 us and the wait between the two products
-// become one of 5, for reading down once per column block, from L2: worth it
-// while that is a few hundred KB.
-template <int RP, bool ADD>
+// The value of the lane N before in its row of 16, around.
+template <int N>
+__device__ __forceinline__ uint32_t row_rotated(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + N, 0xF, 0xF, false));
+}
+
+// Both products of a decode batch in one launch, for ranks up to 16.  Every block
+// makes h of its adapter's rows itself, its wavefronts an eighth of K each, up
+// to 4096 in one go; the second product's operands are on their way while those
+// meet, and `waves` of the wavefronts then take 128 columns each.
+template <bool ADD>
 __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct p) {
+    constexpr int RP = 16, STEPS = 16, COLS = 32 * STEPS;
     typedef ExpandTile<RP> T;
-    constexpr int NRT = RP / 16, STEPS = 16 / NRT, COLS = 32 * STEPS, NEXT = kDirectWaves * COLS;
-    __shared__ f4 sum[kDirectWaves * NRT * 64];
+    __shared__ f4 sum[kDirectWaves * 64];
     __shared__ __attribute__((aligned(16))) uint16_t parts[16 * T::STRIDE];
     __shared__ __attribute__((aligned(16))) float back[16];
     const int lane = threadIdx.x & 63, wave = wave_of(), c16 = lane & 15, g = lane >> 4;
@@ -675,30 +679,21 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
                 at[i] = uint32_t(__shfl(order, min(4 * g + i, cnt - 1))) * p.N + yc;
             }
             const uint32_t xr = uint32_t(__shfl(order, min(c16, cnt - 1))) * p.K;
-            uint32_t wr[NRT];
-            f4 acc[NRT];
-#pragma unroll
-            for (int n = 0; n < NRT; ++n) {
-                wr[n] = uint32_t(min(16 * n + c16, p.R - 1)) * p.K;
-                acc[n] = f4{0.f, 0.f, 0.f, 0.f};
-            }
-            struct Part {
-                u4 x[STEPS], w[NRT][STEPS];
-            } v;
+            const uint32_t wr = uint32_t(min(c16, p.R - 1)) * p.K;
+            f4 acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-            for (int c0 = wave * COLS; c0 < p.K; c0 += NEXT) {
+            for (int c0 = wave * COLS; c0 < p.K; c0 += kDirectWaves * COLS) {
+                u4 vx[STEPS], vw[STEPS];
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     const int c = held(c0 + 32 * i + 8 * g, p.K);
-                    v.x[i] = load8(off(p.x, xr + c));
-#pragma unroll
-                    for (int n = 0; n < NRT; ++n) v.w[n][i] = load8(off(db, wr[n] + c));
+                    vx[i] = load8(off(p.x, xr + c));
+                    vw[i] = load8(off(db, wr + c));
                 }
 #pragma unroll
                 for (int i = 0; i < STEPS; ++i) {
                     if (c0 + 32 * i >= p.K) continue;   // (K is a multiple of 32: held ones are whole steps)
-#pragma unroll
-                    for (int n = 0; n < NRT; ++n) acc[n] = mfma(v.x[i], v.w[n][i], acc[n]);
+                    acc = mfma(vx[i], vw[i], acc);
                 }
             }
             if (mine) {   // in flight while the sums meet
@@ -707,41 +702,36 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
 #pragma unroll
                     for (int i = 0; i < 4; ++i) old[i] = load8(off(p.base, at[i]));
             }
-#pragma unroll
-            for (int n = 0; n < NRT; ++n) sum[(n * kDirectWaves + wave) * 64 + lane] = acc[n];
+            sum[wave * 64 + lane] = acc;
             __syncthreads();
-            if (wave == 0) {   // rows 4 g + i, columns 16 n + l % 16 of h, summed in order, scaled and split
+            if (wave == 0) {   // rows 4 g + i, column l % 16 of h, summed in order, scaled and split
+                acc = sum[lane];
 #pragma unroll
-                for (int n = 0; n < NRT; ++n) {
-                    acc[n] = sum[n * kDirectWaves * 64 + lane];
-#pragma unroll
-                    for (int q = 1; q < kDirectWaves; ++q) acc[n] += sum[(n * kDirectWaves + q) * 64 + lane];
-                    if (16 * n + c16 >= p.R) acc[n] = f4{0.f, 0.f, 0.f, 0.f};
-                }
+                for (int q = 1; q < kDirectWaves; ++q) acc += sum[q * 64 + lane];
+                if (c16 >= p.R) acc = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float all[NRT], inverse;
-#pragma unroll
-                    for (int n = 0; n < NRT; ++n) all[n] = acc[n][i];
-                    bool odd;
-                    float most = largest(all, odd);
-#pragma unroll
-                    for (int o = 1; o < 16; o *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, o));
-                    const float scale = to_range(most, 13, inverse);
+                    float inverse;
+                    uint32_t bits = __builtin_bit_cast(uint32_t, acc[i]) & 0x7FFFFFFFu;
+                    bits = bits < 0x7F800000u ? bits : 0u;   // (of the finite ones)
+                    bits = max(bits, row_rotated<8>(bits));
+                    bits = max(bits, row_rotated<4>(bits));
+                    bits = max(bits, row_rotated<2>(bits));
+                    bits = max(bits, row_rotated<1>(bits));
+                    const float scale = to_range(__builtin_bit_cast(float, bits), 13, inverse);
                     if (c16 == 0) back[4 * g + i] = inverse;
                     uint16_t* to = parts + (4 * g + i) * T::STRIDE + c16;
-                    const int64_t m = __shfl(order, min(4 * g + i, cnt - 1));
-#pragma unroll
-                    for (int n = 0; n < NRT; ++n) {
-                        uint32_t hi, lo;
-                        split_h(all[n], 0.f, scale, hi, lo);
-                        if (odd) lo = without_rest(hi, lo);
-                        to[16 * n] = uint16_t(hi);
-                        to[RP + 16 * n] = uint16_t(lo);
-                        if (p.hidden && blockIdx.x == 0 && 4 * g + i < cnt && 16 * n + c16 < p.R)
-                            p.hidden[m * p.R + 16 * n + c16] = all[n];
-                    }
+                    uint32_t hi, lo;
+                    split_h(acc[i], 0.f, scale, hi, lo);
+                    to[0] = uint16_t(hi);
+                    to[RP] = uint16_t(without_rest(hi, lo));
                 }
+                if (p.hidden && blockIdx.x == 0)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t m = __shfl(order, min(4 * g + i, cnt - 1));
+                        if (4 * g + i < cnt && c16 < p.R) p.hidden[m * p.R + c16] = acc[i];
+                    }
             }
             __syncthreads();
             if (mine) {
@@ -1099,12 +1089,17 @@ int shares(int M, int L, int64_t blocks, int want) {
     return int(std::max<int64_t>(1, std::min<int64_t>(std::min(std::min(L, M), kWindow), want / blocks)));
 }
 
-// Batches of up to this many rows with slots and several adapters are taken for
-// decode batches, a row or a few to an adapter.
-constexpr int kMixedM = 256;
-bool mixed(const wqh::Adapters& a) { return a.slots && a.L > 1 && a.M <= kMixedM; }
+// Batches of fewer than 16 rows to an adapter are taken for decode batches: the
+// shrink takes 16 rows at a time (us against 64 at a time, the whole call, K = N
+// = 4096, rank 16: 128 rows of 32 adapters 10.7 and 16.9, 1000 rows of 100 in any
+// order 59 and 123, in runs 16.5 and 26.0; above the border, 256 rows of 8 in
+// runs, 10.3 and 9.8, 200 rows of 4 at rank 64, 23.3 and 14.9).
+bool mixed(const int32_t* slots, int M, int L) { return slots && M < 16LL * L; }
 
-// Ranges of the long side of a shrink, and the blocks that share a window.
+// Ranges of the long side of a shrink, and the blocks that share a window: one
+// round of blocks on 256 units (two took 55.7 us instead of 47.8 for a whole call
+// of 4096 rows, K = 4096, N = 11008, rank 64: every range is read again by the
+// second product).
 struct ShrinkPlan {
     int splits, cps, Z;
     ShrinkPlan(int M, int R, int L, int C) {
@@ -1113,7 +1108,7 @@ struct ShrinkPlan {
         const int want = int(std::min<int64_t>(std::max<int64_t>(256 / base, 1), 32));
         cps = div_up(chunks, std::min(want, div_up(chunks, 4)));
         splits = div_up(chunks, cps);
-        Z = shares(M, L, base * splits, M <= kMixedM ? 512 : 256);
+        Z = shares(M, L, base * splits, M < 16LL * L ? 512 : 256);
     }
     size_t bytes(int M, int R) const { return round256(size_t(splits) * M * padded_rank(R) * 4); }
 };
@@ -1134,7 +1129,7 @@ wq_status shrink(const wqh::Adapters& a, const uint16_t* src, const uint16_t* w,
         });
         return st != WQ_OK ? st : list_all();
     }
-    const bool one = a.M <= 16 || mixed(a);
+    const bool one = a.M <= 16 || mixed(a.slots, a.M, a.L);
     const unsigned zs = unsigned(p.Z * p.rchunks);
     int layers = div_up(lists, int64_t(p.splits) * zs);
     if (layers > 16) {   // a launch of their own
@@ -1177,7 +1172,8 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     const int wide = out ? div_up(C, 4 * kCols) : 1;   // blocks of 512 columns
     p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), windows * wide / 1024)));
     const int cblocks = div_up(wide, p.span);
-    p.halves = a.M > kWindow / 2 && !mixed(a) && windows * cblocks < 512 ? 2 : 1;
+    // (2048 rows, K = N = 4096, rank 16: 14.8 us with halves, 15.5 without)
+    p.halves = a.M > kWindow / 2 && !mixed(a.slots, a.M, a.L) && windows * cblocks < 512 ? 2 : 1;
     p.Z = shares(a.M, a.L, windows * cblocks * p.halves, 512);
     return pieces(windows, wqh::kMaxBlocks, [&](unsigned now, int64_t first) {
         p.window0 = int(first);
@@ -1202,14 +1198,16 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     });
 }
 
-// Whether a forward pass without dropout is one launch: up to kDirectM rows that
-// differ in their adapters, or 16 that do not, a rank that fits a fragment, and a
-// first factor that every block can read for itself.
-constexpr int kDirectM = 32;
-constexpr int kDirectBytes = 384 << 10;
+// Whether a forward pass without dropout is one launch.  On the GPU both forms
+// take as long for a few rows to an adapter (us, one launch and two; K = N =
+// 4096, rank 16: 1 row 7.6 and 6.8, 4 rows of one adapter 8.8 and 7.5, 16 rows of
+// 16 adapters 7.2 and 8.4; N = 12288, 16 rows of 16 adapters 8.6 and 8.8), and a
+// launch and a workspace less save the caller 5 of 15 us.  Many rows of one
+// adapter (16: 10.8 and 7.6), wider ranks (32, 8 rows: 12.4 and 8.5) and longer
+// rows (K = 11008: 21.7 and 12.2) are two.
+constexpr int kDirectM = 16, kDirectK = 4096;
 bool direct_fits(int M, int N, int K, int R, int L) {
-    return M <= (L > 1 ? kDirectM : 16) && padded_rank(R) <= 32 && int64_t(padded_rank(R)) * K * 2 <= kDirectBytes &&
-           N >= 8;
+    return M <= kDirectM && M <= 4LL * L && R <= 16 && K <= kDirectK && N >= 8;
 }
 
 wq_status direct(const wqh::Adapters& a, const uint16_t* x, const uint16_t* down, const uint16_t* up,
@@ -1217,20 +1215,17 @@ wq_status direct(const wqh::Adapters& a, const uint16_t* x, const uint16_t* down
     Direct p{x, down, up, a.scales, a.slots, base, y, hidden, a.M, a.R, a.L, K, N, std::min(a.L, a.M), 4};
     if (int64_t(div_up(N, 4 * kCols)) * p.Z > 256) p.waves = kDirectWaves;
     const dim3 grid(unsigned(div_up(N, p.waves * kCols)), unsigned(p.Z));
-    auto go = [&](auto n) {
-        if (base)
-            direct_kernel<decltype(n)::value, true><<<grid, 64 * kDirectWaves, 0, s>>>(p);
-        else
-            direct_kernel<decltype(n)::value, false><<<grid, 64 * kDirectWaves, 0, s>>>(p);
-    };
-    if (padded_rank(a.R) == 16)
-        go(Int<16>{});
+    if (base)
+        direct_kernel<true><<<grid, 64 * kDirectWaves, 0, s>>>(p);
     else
-        go(Int<32>{});
+        direct_kernel<false><<<grid, 64 * kDirectWaves, 0, s>>>(p);
     return wqh::launch_status();
 }
 
-// Ranges of rows of the gradients.
+// Ranges of rows of the gradients: about four blocks to a unit, as blocks with
+// dropout's masks and without are of unequal length (4096 rows of 4 adapters, K =
+// 11008, N = 4096, rank 64: 82 us with two ranges and their sum, 112 with one),
+// and no more than an adapter's share of the rows fills.
 int outer_splits(int M, int R, int L, int K, int N) {
     const int64_t blocks = int64_t(L) * (padded_rank(R) > 64 ? 2 : 1) * (div_up(K, kCols) + div_up(N, kCols));
     return int(std::max<int64_t>(1, std::min<int64_t>(std::min(div_up(div_up(M, L), 128), 32), 1024 / blocks)));
