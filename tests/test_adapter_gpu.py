@@ -196,6 +196,37 @@ def test_forward(M, K, N, R, L, kind, add, p):
         assert torch.equal(base, y)
 
 
+# the form of one launch: rows, ranks and K up to its limits and past them, N
+# whose last tile has fewer than eight columns of its own
+@pytest.mark.parametrize("M,K,N,R,L,kind,add", [
+    (1, 32, 8, 1, 1, None, True), (2, 64, 9, 16, 3, "other", False), (3, 4096, 129, 5, 2, "random", True),
+    (4, 4096, 4096, 16, 1, None, True), (4, 1056, 135, 9, 4, "runs", True), (5, 512, 640, 16, 1, None, True),
+    (8, 4096, 12288, 16, 8, "random", True), (13, 2080, 1000, 12, 40, "random", False), (16, 4096, 385, 16, 16, "random", True),
+    (16, 4096, 513, 16, 4, "none", True), (16, 4096, 512, 16, 4, "runs", False), (16, 4128, 512, 16, 16, "random", True),
+    (16, 4096, 512, 17, 16, "random", True), (17, 4096, 512, 16, 16, "random", True), (6, 3200, 131, 3, 1000, "random", True)])
+def test_a_few_rows(M, K, N, R, L, kind, add):
+    P, x, slots = Pool(15, L, R, N, K), randn(1, M, K), make_slots(kind, M, L)
+    base = randn(2, M, N) if add else None
+    y, hidden = wq.adapters(x, *P.args, slots=slots, base=base, save_hidden=True)
+    check_forward(P, x, slots, base, 0.0, y, hidden, "few rows")
+    assert torch.equal(wq.adapters(x, *P.args, slots=slots, base=base), y)
+    if add:
+        assert torch.equal(wq.adapters(x, *P.args, slots=slots, base=base, out=base), y)
+
+
+def test_rows_in_another_order():
+    """A permutation of the rows and their slots is one of the outputs, whatever
+    fragments the rows share (the sums' order does not depend on them)."""
+    M, K, N, R, L = 190, 1024, 600, 16, 5
+    P, x, slots = Pool(16, L, R, N, K), randn(1, M, K), make_slots("runs", M, L)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    perm = torch.randperm(M, generator=g, device="cuda")
+    y, h = wq.adapters(x, *P.args, slots=slots, save_hidden=True)
+    y2, h2 = wq.adapters(x[perm].contiguous(), *P.args, slots=slots[perm].contiguous(), save_hidden=True)
+    assert torch.equal(y[perm], y2) and torch.equal(h[perm], h2)
+
+
 @pytest.mark.parametrize("M,K,N,R,L,kind,add,p", CASES)
 def test_backward(M, K, N, R, L, kind, add, p):
     P, x, slots = Pool(21, L, R, N, K), randn(3, M, K), make_slots(kind, M, L)
