@@ -84,8 +84,8 @@ def within_limits(got):
 
 BIG = 1 << 22
 SIZES = [dict(M=M, N=N, K=K, R=R, L=L, slots=slots, p=p)
-         for M, N, K, L in ((1, 1, 32, 1), (1, BIG, BIG, 1), (5, 7, 64, BIG), (16, 8, 64, 70000), (64, 129, 96, 64),
-                            (300, 4096, 4096, BIG), (4099, 72, 64, 33000), ((1 << 22) + 1, 130, 64, 3),
+         for M, N, K, L in ((1, 1, 32, 1), (1, BIG, BIG, 1), (5, 7, 64, 1 << 20), (16, 8, 64, 70000), (64, 129, 96, 64),
+                            (300, 4096, 4096, 1 << 20), (4099, 72, 64, 33000), ((1 << 22) + 1, 130, 64, 3),
                             (1 << 28, 9, 64, 2), (1 << 28, 3, 32, 40000))
          for R in (1, 17, 128) for slots in (False, True) for p in (0.0, 0.5)]
 
