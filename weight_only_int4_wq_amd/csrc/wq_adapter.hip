@@ -340,6 +340,11 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
 // ONE: 16 rows at a time and one piece in flight, for decode batches of many
 // adapters: that leaves registers for twice the wavefronts, and those blocks
 // wait for a few short loads.
+//
+// Bound by latency below some 2000 rows, then by memory, with dropout by the
+// masks' vector instructions.  Measured, us: 2048 rows, C = 4096, rank 16, 6.6;
+// 4096 rows, rank 64, 22, with dropout 15 (33.5 MB either way); 128 rows of 24
+// adapters, C = 11008, rank 64 (34 MB of weights, by two windows), 15.6.
 template <int NRT, bool DROP, bool ONE>
 __global__ __launch_bounds__(64 * kShrinkWaves, ONE ? 4 : 2) void shrink_kernel(const Shrink p) {
     constexpr int MT = ONE ? 1 : 4;
@@ -589,6 +594,12 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
 // Blocks: x the window (neighbours on different XCDs, a window's column blocks
 // on one, so that its h comes from memory once), y the column block, z the
 // halves of an adapter's rows and Z shares of the window's adapters.
+//
+// Bound by memory for long rows, by latency below.  Measured, us: 4096 x 11008,
+// rank 64, 45 for the 180 MB of old values and results (4.0 TB/s; a copy reaches
+// 4.87), with dropout 71 (masks: 2.2 times the vector instructions, two
+// wavefronts to a unit; three spilled 37 registers and took 84); 2048 x 4096,
+// rank 16, 10.9; 16 rows 4 to 5.
 template <int RP, bool DROP, bool ADD>
 __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p) {
     __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * ExpandTile<RP>::STRIDE];
@@ -654,7 +665,9 @@ __device__ __forceinline__ uint32_t row_rotated(uint32_t v) {
 // Both products of a decode batch in one launch, for ranks up to 16.  Every block
 // makes h of its adapter's rows itself, its wavefronts an eighth of K each, up
 // to 4096 in one go; the second product's operands are on their way while those
-// meet, and `waves` of the wavefronts then take 128 columns each.
+// meet, and `waves` of the wavefronts then take 128 columns each.  Bound by the
+// chain of loads: 8.2 us for a row of 4096 -> 4096, 10.0 for 16 rows of 16
+// adapters -> 12288.
 template <bool ADD>
 __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct p) {
     constexpr int RP = 16, STEPS = 16, COLS = 32 * STEPS;
@@ -791,6 +804,11 @@ struct Outer {
 // are added to the fp32 sums.
 // Blocks: x the column tiles of both gradients, y the range of rows, z the
 // rank's 64s and the adapter.
+//
+// Bound by vector instructions: masks (half of them, with dropout), the split of
+// h, addresses; then by latency.  Measured, us: 4096 rows of 4 adapters, C = 11008
+// and 4096, rank 64, dropout, 73 for the 124 MB read (every 16 of the rank
+// masking for itself: 81 to 92); 2048 rows, C = 4096 twice, rank 16, 12.4.
 template <int RW, bool LIST>
 __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     __shared__ u4 xs[4 * 8 * 64];                        // [step][column fragment][lane]
