@@ -331,3 +331,33 @@ def test_order_of_the_draws():
     keep, factor = O.drop_keep((30, 40), 0.25, 5, 6)
     assert factor == 4 / 3 and 0.7 < keep.mean() < 0.8
     assert O.drop_keep((3, 5), 0.0, 5, 6)[0].all()
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_the_tensors_device_is_current_during_the_call(index, monkeypatch):
+    """The library runs on the tensors' device and its current stream, whichever
+    device was current before."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Library:
+        @staticmethod
+        def wq_dropout(*args):
+            seen.append((current[0], *args))
+            return 0
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 70 + i, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(wq, "_lib", Library)
+    wq._on_device("wq_dropout", torch.device("cuda", index), (5, 6))
+    assert seen == [(index, 5, 6, 70 + index)] and current == [0]
