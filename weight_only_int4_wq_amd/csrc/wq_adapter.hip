@@ -596,9 +596,10 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
 // halves of an adapter's rows and Z shares of the window's adapters.
 //
 // Bound by memory for long rows, by latency below.  Measured, us: 4096 x 11008,
-// rank 64, 45 for the 180 MB of old values and results (4.0 TB/s; a copy reaches
-// 4.87), with dropout 71 (masks: 2.2 times the vector instructions, two
-// wavefronts to a unit; three spilled 37 registers and took 84); 2048 x 4096,
+// rank 64, 42 for the 180 MB of old values and results (4.3 TB/s; a copy reaches
+// 4.87), with dropout 64 (masks: 2.2 times the vector instructions, two
+// wavefronts to a unit; three spilled 37 registers and were a fifth slower);
+// 2048 x 4096,
 // rank 16, 10.9; 16 rows 4 to 5.
 template <int RP, bool DROP, bool ADD>
 __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p) {
@@ -1188,7 +1189,10 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
         });
     const int64_t windows = div_up(a.M, kWindow);
     const int wide = out ? div_up(C, 4 * kCols) : 1;   // blocks of 512 columns
-    p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), windows * wide / 1024)));
+    // columns to a block so that two blocks to a unit run in one round (4096 x
+    // 11008, rank 64: 42.4 us, with dropout 63.8; 512 to a block, 2.75 rounds, 45.2
+    // and 71.2)
+    p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), (windows * wide + 511) / 512)));
     const int cblocks = div_up(wide, p.span);
     // (2048 rows, K = N = 4096, rank 16: 14.8 us with halves, 15.5 without)
     p.halves = a.M > kWindow / 2 && !mixed(a.slots, a.M, a.L) && windows * cblocks < 512 ? 2 : 1;
