@@ -43,6 +43,7 @@
  * Arithmetic: products accumulate in fp32, and hidden keeps its 32 bits;
  * on the way into the second product it is split into two fp16 numbers with
  * 21 bits of significand together.  y and dx are rounded once.
+ * Infinities and NaN in any operand give what the products and sums give them.
  *
  * Conventions: fp16 arrays, fp32 outputs and the workspace are 16-byte
  * aligned, slots and scales 4-byte, step 8-byte.  Outputs and the workspace

@@ -140,11 +140,27 @@ __device__ __forceinline__ void split_h(float a, float b, float scale, uint32_t&
     const wq::h2 h = wq::as_h2(hi);
     lo = pack_h(__builtin_fmaf(a, scale, -float(h[0])), __builtin_fmaf(b, scale, -float(h[1])));
 }
-// An infinity leaves NaN there: zero instead.
+// An infinity of h leaves NaN in the rest: zero instead.
 __device__ __forceinline__ uint32_t without_rest(uint32_t hi, uint32_t lo) {
     if ((hi & 0x7FFFu) == 0x7C00u) lo &= 0xFFFF0000u;
     if ((hi & 0x7FFF0000u) == 0x7C000000u) lo &= 0xFFFFu;
     return lo;
+}
+
+// An infinity of the other operand makes NaN of a rest that is zero or of the
+// other sign, where h times it is an infinity.  So sums that are not finite are made
+// again without the split.  Whether a lane holds one: IEEE 754's maximum keeps NaN, and is
+// one instruction for two values (16 to a 16 x 128 tile; all of this takes 0.1 to
+// 0.2 us of a decode call, 1% of a large one).
+__device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
+template <int N>
+__device__ __forceinline__ bool any_odd(const f4 (&v)[N]) {
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_maximum(most, __builtin_fabsf(v[j][i]));
+    return __ballot(!finite(most)) != 0;
 }
 
 // --------------------------------------------------------------- shrink ----
@@ -488,6 +504,20 @@ __device__ __forceinline__ void expand_tile(const uint16_t* parts, const float* 
             for (int j = 0; j < 8; ++j) acc[j] = mfma(lo, w[k][j], acc[j]);
         }
     }
+    // The first parts alone (twice where both share an instruction) have h's signs, and
+    // their sum is the same infinity or NaN, or it is finite: then the two parts' sum had
+    // left fp32's range.
+    if (any_odd(acc)) {
+        h = parts + c16 * T::STRIDE + 8 * (T::BOTH ? g & 1 : g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f4 t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < T::KB; ++k) t = mfma(*reinterpret_cast<const u4*>(h + 32 * k), w[k][j], t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = finite(t[i]) ? acc[j][i] : t[i];
+        }
+    }
     u4 keep[4];
     if constexpr (DROP) {
         uint64_t m[4];
@@ -829,7 +859,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     const uint64_t stream = drop ? wq::drop_stream(j.drop) : 0;
     // rounds of four steps of 32 rows
     const int rounds = (cnt + 127) / 128, end = int(int64_t(split + 1) * rounds / p.splits);
-    int round = int(int64_t(split) * rounds / p.splits);
+    const int begin = int(int64_t(split) * rounds / p.splits);
     // a lane's r: RW side by side; past the rank others are taken, and what they give is not kept
     const int held_r = min(r0 + RW * c16, p.R - RW);
     f4 acc[8];
@@ -858,13 +888,13 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
             __builtin_memcpy(&hv[i], j.h + int64_t(m[i]) * p.R + held_r, 4 * RW);
         }
     };
-    if (round < end) {
-        rows(round, m);
+    if (begin < end) {
+        rows(begin, m);
         load();
-        rows(min(round + 1, end - 1), next);
+        rows(min(begin + 1, end - 1), next);
     }
 #pragma unroll 1
-    for (; round < end; ++round) {
+    for (int round = begin; round < end; ++round) {
         const int first = round * 128 + wave * 32 + 8 * g;   // the lane's first row in the adapter's
         float h[8][RW];
 #pragma unroll
@@ -979,6 +1009,47 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
         for (int o = RW; o < 4; o += RW)
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[k] += sums[((wave + o) * 8 + k) * 64 + lane];
+    }
+
+    if (any_odd(acc)) {   // row by row in fp32, the loads of four at once
+        f4 plain[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) plain[k] = f4{0.f, 0.f, 0.f, 0.f};
+        const int last = int(std::min(int64_t(end) * 128, int64_t(cnt)));
+#pragma unroll 1
+        for (int n = begin * 128; n < last; n += 4) {
+            u4 v[4], keep[4];
+            f4 q[4];
+            uint64_t eight[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int nth = min(n + u, last - 1);
+                const int64_t row = LIST ? p.list[at + nth] : nth;
+                eight[u] = (uint64_t(row) * j.C + c) >> 3;
+                v[u] = load8(j.src + row * j.C + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[u][i] = j.h[row * p.R + min(r0 + RW * (4 * g + i) + mine, p.R - 1)];
+            }
+            if (drop) {
+                wq::keep8(eight, j.drop, stream, keep);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] &= keep[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (n + u >= last) break;
+                float f[8];
+                wq::load_h<8>(reinterpret_cast<const uint16_t*>(&v[u]), f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) plain[k][i] = __builtin_fmaf(q[u][i], f[k], plain[k][i]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[k][i] = finite(acc[k][i]) ? acc[k][i] : plain[k][i];
     }
 
     const float s = (drop ? j.drop.keep : 1.f) * (cnt ? p.scales[a] : 0.f);
