@@ -27,6 +27,7 @@ using wq::u4;
 constexpr int kWindow = 64;   // rows a block looks at: a wavefront's lanes
 constexpr int kChunk = 128;   // columns of src by which a shrink is split into ranges
 constexpr int kShrinkWaves = 8, kDirectWaves = 8;
+constexpr int kDirectM = 16, kDirectK = 4096;   // the one-launch form's: a fragment's rows, K in a block's registers
 constexpr int kPad = 128;     // numbers behind the last list: a round of the gradients reads whole ones
 constexpr int kCols = 128;    // columns of out and dw of a wavefront: 16 lanes of 8
 
@@ -684,7 +685,7 @@ struct Direct {
     uint16_t* y;           // [M][N]
     float* hidden;         // [M][R], nullable
     int M, R, L, K, N;
-    int Z, waves;          // blocks that share the window's adapters; wavefronts with columns of y
+    int waves;             // wavefronts with columns of y
 };
 
 // The value of the lane N before in its row of 16, around.
@@ -693,15 +694,16 @@ __device__ __forceinline__ uint32_t row_rotated(uint32_t v) {
     return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + N, 0xF, 0xF, false));
 }
 
-// Both products of a decode batch in one launch, for ranks up to 16.  Every block
-// makes h of its adapter's rows itself, its wavefronts an eighth of K each, up
-// to 4096 in one go; the second product's operands are on their way while those
-// meet, and `waves` of the wavefronts then take 128 columns each.  Bound by the
+// Both products of a decode batch in one launch, for ranks and batches up to 16.
+// Blocks: x the columns, y the adapters that occur, one each.  Every block
+// makes h of its adapter's rows itself, its wavefronts 512 of K's up to 4096
+// channels each, in one go; the second product's operands are on their way while
+// those meet, and `waves` of the wavefronts then take 128 columns each.  Bound by the
 // chain of loads: 8.2 us for a row of 4096 -> 4096, 10.0 for 16 rows of 16
 // adapters -> 12288.
 template <bool ADD>
 __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct p) {
-    constexpr int RP = 16, STEPS = 16, COLS = 32 * STEPS;
+    constexpr int RP = 16, STEPS = kDirectK / (32 * kDirectWaves), COLS = 32 * STEPS;
     typedef ExpandTile<RP> T;
     __shared__ f4 sum[kDirectWaves * 64];
     __shared__ __attribute__((aligned(16))) uint16_t parts[16 * T::STRIDE];
@@ -711,84 +713,83 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
     const bool mine = wave < p.waves && y0 < p.N;   // has columns of y
     const int slot = slot_of(p.slots, lane, p.M, p.L);
 
-    each_adapter(slot, blockIdx.y, p.Z, [&](int a, int cnt, int order) {
+    int a = 0, cnt = 0, order = 0;   // the block's adapter and its rows
+    each_adapter(slot, blockIdx.y, gridDim.y, [&](int of, int rows, int first) { a = of, cnt = rows, order = first; });
+    if (cnt > 0) {
         const uint16_t* const db = p.down + int64_t(a) * p.R * p.K;
-#pragma unroll 1
-        for (; cnt > 0; cnt -= 16, order = __shfl(order, (lane + 16) & 63)) {
-            uint32_t at[4];
-            u4 raw[8], old[4], w[T::KB][8];
+        uint32_t at[4];
+        u4 raw[8], old[4], w[T::KB][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                old[i] = u4{0, 0, 0, 0};
-                at[i] = uint32_t(__shfl(order, min(4 * g + i, cnt - 1))) * p.N + yc;
+        for (int i = 0; i < 4; ++i) {
+            old[i] = u4{0, 0, 0, 0};
+            at[i] = uint32_t(__shfl(order, min(4 * g + i, cnt - 1))) * p.N + yc;
+        }
+        const uint32_t xr = uint32_t(__shfl(order, min(c16, cnt - 1))) * p.K;
+        const uint32_t wr = uint32_t(min(c16, p.R - 1)) * p.K;
+        f4 acc{0.f, 0.f, 0.f, 0.f};
+        const int c0 = wave * COLS;
+        if (c0 < p.K) {
+            u4 vx[STEPS], vw[STEPS];
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int c = held(c0 + 32 * i + 8 * g, p.K);
+                vx[i] = load8(off(p.x, xr + c));
+                vw[i] = load8(off(db, wr + c));
             }
-            const uint32_t xr = uint32_t(__shfl(order, min(c16, cnt - 1))) * p.K;
-            const uint32_t wr = uint32_t(min(c16, p.R - 1)) * p.K;
-            f4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int c0 = wave * COLS; c0 < p.K; c0 += kDirectWaves * COLS) {
-                u4 vx[STEPS], vw[STEPS];
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int c = held(c0 + 32 * i + 8 * g, p.K);
-                    vx[i] = load8(off(p.x, xr + c));
-                    vw[i] = load8(off(db, wr + c));
-                }
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    if (c0 + 32 * i >= p.K) continue;   // (K is a multiple of 32: held ones are whole steps)
-                    acc = mfma(vx[i], vw[i], acc);
-                }
-            }
-            if (mine) {   // in flight while the sums meet
-                load_w<RP>(raw, p.up + int64_t(a) * p.R * p.N, 0, yc, p.R, p.N);
-                if constexpr (ADD)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) old[i] = load8(off(p.base, at[i]));
-            }
-            sum[wave * 64 + lane] = acc;
-            __syncthreads();
-            if (wave == 0) {   // rows 4 g + i, column l % 16 of h, summed in order, scaled and split
-                acc = sum[lane];
-#pragma unroll
-                for (int q = 1; q < kDirectWaves; ++q) acc += sum[q * 64 + lane];
-                if (c16 >= p.R) acc = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float inverse;
-                    uint32_t bits = __builtin_bit_cast(uint32_t, acc[i]) & 0x7FFFFFFFu;
-                    bits = bits < 0x7F800000u ? bits : 0u;   // (of the finite ones)
-                    bits = max(bits, row_rotated<8>(bits));
-                    bits = max(bits, row_rotated<4>(bits));
-                    bits = max(bits, row_rotated<2>(bits));
-                    bits = max(bits, row_rotated<1>(bits));
-                    const float scale = to_range(__builtin_bit_cast(float, bits), 13, inverse);
-                    if (c16 == 0) back[4 * g + i] = inverse;
-                    uint16_t* to = parts + (4 * g + i) * T::STRIDE + c16;
-                    uint32_t hi, lo;
-                    split_h(acc[i], 0.f, scale, hi, lo);
-                    to[0] = uint16_t(hi);
-                    to[RP] = uint16_t(without_rest(hi, lo));
-                }
-                if (p.hidden && blockIdx.x == 0)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t m = __shfl(order, min(4 * g + i, cnt - 1));
-                        if (4 * g + i < cnt && c16 < p.R) p.hidden[m * p.R + c16] = acc[i];
-                    }
-            }
-            __syncthreads();
-            if (mine) {
-                make_w<RP>(raw, w[0], 0, p.R);
-                expand_tile<RP, false>(parts, back, w, old, p.scales[a], at, p.y, y0, yc, p.N, cnt, Drop{}, 0, 0);
+            for (int i = 0; i < STEPS; ++i) {
+                if (c0 + 32 * i >= p.K) continue;   // (K is a multiple of 32: held ones are whole steps)
+                acc = mfma(vx[i], vw[i], acc);
             }
         }
-    });
+        if (mine) {   // in flight while the sums meet
+            load_w<RP>(raw, p.up + int64_t(a) * p.R * p.N, 0, yc, p.R, p.N);
+            if constexpr (ADD)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) old[i] = load8(off(p.base, at[i]));
+        }
+        sum[wave * 64 + lane] = acc;
+        __syncthreads();
+        if (wave == 0) {   // rows 4 g + i, column l % 16 of h, summed in order, scaled and split
+            acc = sum[lane];
+#pragma unroll
+            for (int q = 1; q < kDirectWaves; ++q) acc += sum[q * 64 + lane];
+            if (c16 >= p.R) acc = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float inverse;
+                uint32_t bits = __builtin_bit_cast(uint32_t, acc[i]) & 0x7FFFFFFFu;
+                bits = bits < 0x7F800000u ? bits : 0u;   // (of the finite ones)
+                bits = max(bits, row_rotated<8>(bits));
+                bits = max(bits, row_rotated<4>(bits));
+                bits = max(bits, row_rotated<2>(bits));
+                bits = max(bits, row_rotated<1>(bits));
+                const float scale = to_range(__builtin_bit_cast(float, bits), 13, inverse);
+                if (c16 == 0) back[4 * g + i] = inverse;
+                uint16_t* to = parts + (4 * g + i) * T::STRIDE + c16;
+                uint32_t hi, lo;
+                split_h(acc[i], 0.f, scale, hi, lo);
+                to[0] = uint16_t(hi);
+                to[RP] = uint16_t(without_rest(hi, lo));
+            }
+            if (p.hidden && blockIdx.x == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t m = __shfl(order, min(4 * g + i, cnt - 1));
+                    if (4 * g + i < cnt && c16 < p.R) p.hidden[m * p.R + c16] = acc[i];
+                }
+        }
+        __syncthreads();
+        if (mine) {
+            make_w<RP>(raw, w[0], 0, p.R);
+            expand_tile<RP, false>(parts, back, w, old, p.scales[a], at, p.y, y0, yc, p.N, cnt, Drop{}, 0, 0);
+        }
+    }
 
     // rows without an adapter
     const uint64_t none = blockIdx.y == 0 ? __ballot(slot < 0 && lane < p.M) : 0;
     if (!none) return;
-    const int cnt = __builtin_popcountll(none), order = compact(none);
+    cnt = __builtin_popcountll(none), order = compact(none);
     if (mine && p.y != p.base)
         for (int row = 0; row < cnt; row += 4) {
             const uint32_t at = uint32_t(__shfl(order, min(row + g, cnt - 1))) * p.N + yc;
@@ -1298,16 +1299,16 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
 // launch and a workspace less save the caller 5 of 15 us.  Many rows of one
 // adapter (16: 10.8 and 7.6), wider ranks (32, 8 rows: 12.4 and 8.5) and longer
 // rows (K = 11008: 21.7 and 12.2) are two.
-constexpr int kDirectM = 16, kDirectK = 4096;
 bool direct_fits(int M, int N, int K, int R, int L) {
     return M <= kDirectM && M <= 4LL * L && R <= 16 && K <= kDirectK && N >= 8;
 }
 
 wq_status direct(const wqh::Adapters& a, const uint16_t* x, const uint16_t* down, const uint16_t* up,
                  const uint16_t* base, uint16_t* y, float* hidden, int N, int K, hipStream_t s) {
-    Direct p{x, down, up, a.scales, a.slots, base, y, hidden, a.M, a.R, a.L, K, N, std::min(a.L, a.M), 4};
-    if (int64_t(div_up(N, 4 * kCols)) * p.Z > 256) p.waves = kDirectWaves;
-    const dim3 grid(unsigned(div_up(N, p.waves * kCols)), unsigned(p.Z));
+    Direct p{x, down, up, a.scales, a.slots, base, y, hidden, a.M, a.R, a.L, K, N, 4};
+    const int Z = std::min(a.L, a.M);   // adapters that can occur
+    if (int64_t(div_up(N, 4 * kCols)) * Z > 256) p.waves = kDirectWaves;
+    const dim3 grid(unsigned(div_up(N, p.waves * kCols)), unsigned(Z));
     if (base)
         direct_kernel<true><<<grid, 64 * kDirectWaves, 0, s>>>(p);
     else
