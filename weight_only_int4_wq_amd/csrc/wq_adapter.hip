@@ -757,8 +757,9 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
             if (c16 >= p.R) acc = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const float v = acc[i];   // (a bit cast of a vector's element gives its first one's)
                 float inverse;
-                uint32_t bits = __builtin_bit_cast(uint32_t, acc[i]) & 0x7FFFFFFFu;
+                uint32_t bits = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
                 bits = bits < 0x7F800000u ? bits : 0u;   // (of the finite ones)
                 bits = max(bits, row_rotated<8>(bits));
                 bits = max(bits, row_rotated<4>(bits));
@@ -768,7 +769,7 @@ __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct 
                 if (c16 == 0) back[4 * g + i] = inverse;
                 uint16_t* to = parts + (4 * g + i) * T::STRIDE + c16;
                 uint32_t hi, lo;
-                split_h(acc[i], 0.f, scale, hi, lo);
+                split_h(v, 0.f, scale, hi, lo);
                 to[0] = uint16_t(hi);
                 to[RP] = uint16_t(without_rest(hi, lo));
             }
