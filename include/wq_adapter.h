@@ -40,10 +40,16 @@
  * device, nullable: 0) lets a captured graph draw another mask on every
  * replay: the caller advances it between the replays.
  *
- * Arithmetic: products accumulate in fp32, and hidden keeps its 32 bits;
- * on the way into the second product it is split into two fp16 numbers with
- * 21 bits of significand together.  y and dx are rounded once.
- * Infinities and NaN in any operand give what the products and sums give them.
+ * Arithmetic: products accumulate in fp32, and hidden keeps its 32 bits.  On
+ * the way into the second product an element of it (of dh, of the hidden of a
+ * backward call) is split into two fp16 numbers, after a power of two has
+ * brought the largest one beside it into fp16's range: it is off by at most
+ * 2^-22 of itself or 2^-38 of that largest one, whichever is more, and is zero
+ * below 2^-39 of it.  Beside it, for y and dx, is its row; for ddown and dup its
+ * column of 32 rows that follow one another among the adapter's: a row there that
+ * is more than 2^16 times smaller than another has fewer than 22 bits.  y and
+ * dx are rounded once.  Infinities and NaN in any operand give what the
+ * products and sums give them.
  *
  * Conventions: fp16 arrays, fp32 outputs and the workspace are 16-byte
  * aligned, slots and scales 4-byte, step 8-byte.  Outputs and the workspace

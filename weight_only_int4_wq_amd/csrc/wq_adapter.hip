@@ -135,7 +135,10 @@ __device__ __forceinline__ uint32_t pack_h(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, wq::h2));
 }
 // scale a and scale b (a power of two) as sums of two fp16 numbers each: the
-// second is what the first leaves, one multiply-add.
+// second is what the first leaves, one multiply-add.  The matrix instructions that
+// take fp16 weights as they are take fp16 beside them; two parts leave 2^-22 of
+// a value (2^-25 where that is more, 2^-38 of the largest), near fp32's own 2^-24,
+// for twice the instructions, and a third part would be half as many again.
 __device__ __forceinline__ void split_h(float a, float b, float scale, uint32_t& hi, uint32_t& lo) {
     hi = pack_h(a * scale, b * scale);
     const wq::h2 h = wq::as_h2(hi);
