@@ -40,7 +40,8 @@
  * device, nullable: 0) lets a captured graph draw another mask on every
  * replay: the caller advances it between the replays.
  *
- * Arithmetic: products accumulate in fp32, and hidden keeps its 32 bits.  On
+ * Arithmetic: products accumulate in fp32 (whose rounding counts a subnormal
+ * fp16 operand as 2^-14), and hidden keeps its 32 bits.  On
  * the way into the second product an element of it (of dh, of the hidden of a
  * backward call) is split into two fp16 numbers, after a power of two has
  * brought the largest one beside it into fp16's range: it is off by at most

@@ -213,3 +213,25 @@ def test_small_elements_beside_large_ones_in_a_row(M, R):
     fits = ref.abs() < 6e4
     assert fits[:, ::2].all()
     near(torch.where(fits, y.double(), 0.0), torch.where(fits, ref, 0.0), tol + U * (ref.abs() + tol) + 2.0 ** -25, "y")
+
+
+@pytest.mark.parametrize("M,R,N", [(3, 16, 264), (40, 16, 264), (70, 48, 136), (128, 128, 72)])
+def test_subnormal_operands(M, R, N):
+    """The matrix cores align a product by its operands' exponents, and an fp16
+    subnormal's is 2^-14 whatever its leading bit: the sums' rounding counts it
+    so, in y with a subnormal up and in dup with a subnormal dy."""
+    g, K = generator(M + R), 64
+    least = lambda t: torch.where(t != 0, t.abs().clamp(min=2.0 ** -14), 0.0)  # noqa: E731
+    up = (integers(g, -1023, 1024, 1, R, N).double() * 2.0 ** -24).half()
+    x, down = randn(1, M, K), randn(2, 1, R, K)
+    y, hidden = wq.adapters(x, down, up, torch.full((1,), 1024.0, device="cuda"), save_hidden=True)
+    h, u = hidden.double(), up[0].double()
+    ref = 1024 * (h @ u)
+    tol = 1024 * (error_of(h, 1) @ u.abs() + 2 * (2 * R + 64) * E32 * (h.abs() @ least(u))) + 4 * E32 * ref.abs()
+    near(y, ref, tol + U * (ref.abs() + tol) + 2.0 ** -25, "y")
+    dy = (integers(g, -1023, 1024, M, N).double() * 2.0 ** -24).half()
+    _, _, dup = wq.adapters_backward(dy, x, hidden, down, up, torch.full((1,), 1024.0, device="cuda"), need_dx=False)
+    d, error = dy.double(), torch.cat([error_of(p, 0) for p in h.split(32)])
+    ref = 1024 * (h.T @ d)
+    tol = 1024 * (error.T @ d.abs() + 2 * (2 * M + 64) * E32 * (h.abs().T @ least(d))) + 4 * E32 * ref.abs() + 2.0 ** -149
+    near(dup[0], ref, tol, "dup")
