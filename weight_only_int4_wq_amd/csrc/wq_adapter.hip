@@ -154,8 +154,8 @@ __device__ __forceinline__ uint32_t without_rest(uint32_t hi, uint32_t lo) {
 // An infinity of the other operand makes NaN of a rest that is zero or of the
 // other sign, where h times it is an infinity.  So sums that are not finite are made
 // again without the split.  Whether a lane holds one: IEEE 754's maximum keeps NaN, and is
-// one instruction for two values (16 to a 16 x 128 tile; all of this takes 0.1 to
-// 0.2 us of a decode call, 1% of a large one).
+// one instruction for two values (16 to a 16 x 128 tile; all of this takes up to
+// 0.3 us of a decode call, 1% of a large one).
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
 template <int N>
 __device__ __forceinline__ bool any_odd(const f4 (&v)[N]) {
@@ -362,9 +362,14 @@ __device__ __forceinline__ void shrink_rows(const Shrink& p, int64_t m0, int a, 
 // wait for a few short loads.
 //
 // Bound by latency below some 2000 rows, then by memory, with dropout by the
-// masks' vector instructions.  Measured, us: 2048 rows, C = 4096, rank 16, 6.6;
-// 4096 rows, rank 64, 22, with dropout 15 (33.5 MB either way); 128 rows of 24
-// adapters, C = 11008, rank 64 (34 MB of weights, by two windows), 15.6.
+// masks' vector instructions.  Measured, us, all rows of one adapter and in five or
+// four runs (a window at a run's border takes its adapters one after the other, and
+// the launch lasts as long as that block): 2048 rows, C = 4096, rank 16, 6.0 to 6.7
+// and 8.6 to 9.7; 4096 rows, rank 64, 12.2 and 18.9 to 22.2; with dropout, of one
+// adapter, 15.2.  128 rows of 24 adapters, C = 11008, rank 64, 14.4 to 15.2: the 34 MB
+// of weights come from memory once, a block takes two or three adapters in series.
+// Rows of odd length are read by accesses that are aligned to 2 bytes, at half the
+// rate: 311 rows of C = 5001, rank 8, 9.1, of 5004 4.7, with lists or without.
 template <int NRT, bool DROP, bool ONE>
 __global__ __launch_bounds__(64 * kShrinkWaves, ONE ? 4 : 2) void shrink_kernel(const Shrink p) {
     constexpr int MT = ONE ? 1 : 4;
@@ -630,11 +635,11 @@ __device__ __forceinline__ void expand_rows(const Expand& p, int64_t m0, int a, 
 // halves of an adapter's rows and Z shares of the window's adapters.
 //
 // Bound by memory for long rows, by latency below.  Measured, us: 4096 x 11008,
-// rank 64, 42 for the 180 MB of old values and results (4.3 TB/s; a copy reaches
-// 4.87), with dropout 64 (masks: 2.2 times the vector instructions, two
+// rank 64, 43 for the 180 MB of old values and results (4.2 TB/s; a copy reaches
+// 4.92), with dropout 66 (masks: 2.5 times the vector instructions, two
 // wavefronts to a unit; three spilled 37 registers and were a fifth slower);
-// 2048 x 4096,
-// rank 16, 10.9; 16 rows 4 to 5.
+// 2048 x 4096, rank 16, 10.7; 16 rows 4 to 5.  128 x 4096 of 24 adapters, rank 64,
+// 14: h's 22 ranges are summed two at a time, and only then are w's loads issued.
 template <int RP, bool DROP, bool ADD>
 __global__ __launch_bounds__(256, RP > 64 ? 1 : 2) void expand_kernel(const Expand p) {
     __shared__ __attribute__((aligned(16))) uint16_t parts[kWindow * ExpandTile<RP>::STRIDE];
@@ -702,8 +707,8 @@ __device__ __forceinline__ uint32_t row_rotated(uint32_t v) {
 // makes h of its adapter's rows itself, its wavefronts 512 of K's up to 4096
 // channels each, in one go; the second product's operands are on their way while
 // those meet, and `waves` of the wavefronts then take 128 columns each.  Bound by the
-// chain of loads: 8.2 us for a row of 4096 -> 4096, 10.0 for 16 rows of 16
-// adapters -> 12288.
+// chain of loads, with every column block reading all of an adapter's `down`: 8.2 us
+// for a row of 4096 -> 4096, 10.1 for 16 rows of 16 adapters -> 12288.
 template <bool ADD>
 __global__ __launch_bounds__(64 * kDirectWaves) void direct_kernel(const Direct p) {
     constexpr int RP = 16, STEPS = kDirectK / (32 * kDirectWaves), COLS = 32 * STEPS;
@@ -843,8 +848,9 @@ struct Outer {
 //
 // Bound by vector instructions: masks (half of them, with dropout), the split of
 // h, addresses; then by latency.  Measured, us: 4096 rows of 4 adapters, C = 11008
-// and 4096, rank 64, dropout, 73 for the 124 MB read (every 16 of the rank
-// masking for itself: 81 to 92); 2048 rows, C = 4096 twice, rank 16, 12.4.
+// and 4096, rank 64, dropout, 73 to 76 for the 124 MB read (every 16 of the rank
+// masking for itself: 81 to 92); 2048 rows, C = 4096 twice, rank 16, 12.3 to 13.0
+// in 16 ranges of a single round each, whose rows are loaded twice.
 template <int RW, bool LIST>
 __global__ __launch_bounds__(256, 2) void outer_kernel(const Outer p) {
     __shared__ u4 xs[4 * 8 * 64];                        // [step][column fragment][lane]
@@ -1266,8 +1272,8 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     const int64_t windows = div_up(a.M, kWindow);
     const int wide = out ? div_up(C, 4 * kCols) : 1;   // blocks of 512 columns
     // columns to a block so that two blocks to a unit run in one round (4096 x
-    // 11008, rank 64: 42.4 us, with dropout 63.8; 512 to a block, 2.75 rounds, 45.2
-    // and 71.2)
+    // 11008, rank 64: 42.8 us, with dropout 66.9; 512 to a block, 2.75 rounds, 46.0
+    // and 72.2)
     p.span = int(std::max<int64_t>(1, std::min<int64_t>(std::min(wide, 8), (windows * wide + 511) / 512)));
     const int cblocks = div_up(wide, p.span);
     // (2048 rows, K = N = 4096, rank 16: 14.8 us with halves, 15.5 without)
@@ -1296,13 +1302,15 @@ wq_status expand(const wqh::Adapters& a, const float* part, int splits, const ui
     });
 }
 
-// Whether a forward pass without dropout is one launch.  On the GPU both forms
-// take as long for a few rows to an adapter (us, one launch and two; K = N =
-// 4096, rank 16: 1 row 7.6 and 6.8, 4 rows of one adapter 8.8 and 7.5, 16 rows of
-// 16 adapters 7.2 and 8.4; N = 12288, 16 rows of 16 adapters 8.6 and 8.8), and a
-// launch and a workspace less save the caller 5 of 15 us.  Many rows of one
-// adapter (16: 10.8 and 7.6), wider ranks (32, 8 rows: 12.4 and 8.5) and longer
-// rows (K = 11008: 21.7 and 12.2) are two.
+// Whether a forward pass without dropout is one launch.  It saves a caller who
+// launches from the host 4.5 of 14.2 us, a launch and a workspace.  On the GPU itself,
+// in a replayed graph, it gains for short rows and loses at the longest (us, one
+// launch and two; rank 16: K = N = 1024, 1 row 4.4 and 6.2, 16 rows of 16 adapters
+// 5.1 and 8.1; K = 2048, N = 11008, rank 8, 16 of 16 6.3 and 8.4; K = N = 4096, 1 row
+// 7.6 and 6.6, 4 of one adapter 8.9 and 7.1, 16 of 16 9.2 and 8.3): one block reads an
+// adapter's whole `down`.  Many rows of one adapter (16: 10.8 and 7.6), wider ranks
+// (32, 8 rows: 12.4 and 8.5) and longer rows (K = 11008: 21.7 and 12.2) lost more than
+// the launch saves, measured before the form was held to a block's registers.
 bool direct_fits(int M, int N, int K, int R, int L) {
     return M <= kDirectM && M <= 4LL * L && R <= 16 && K <= kDirectK && N >= 8;
 }
