@@ -50,7 +50,7 @@
  * column of 32 rows that follow one another among the adapter's: a row there that
  * is more than 2^16 times smaller than another has fewer than 22 bits.  y and
  * dx are rounded once.  Infinities and NaN in any operand give what the
- * products and sums give them.
+ * products and sums of these numbers give them.
  *
  * Conventions: fp16 arrays, fp32 outputs and the workspace are 16-byte
  * aligned, slots and scales 4-byte, step 8-byte.  Outputs and the workspace
